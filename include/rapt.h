@@ -445,6 +445,109 @@ rapt_status rla_l2_fwd_noalloc(const void* q, const void* k, const void* v, rapt
                                int32_t B, int32_t L, int32_t H, int32_t d, float eps, void* out,
                                rapt_stream_t stream);
 
+/*
+ * The rest of a block around the attention: norms and residual stream, gated feed-forward, and the
+ * gradients of the projections. None of them is on the pages as code; the norm's contract is the
+ * features' (fp32 statistics and gains, eps inside the root; ruDNN README §7).
+ */
+
+/* Activations of a gate: z, z sigmoid(z), z Phi(z) (Phi the normal distribution function),
+ * max(z, 0) (derivative 0 at 0), sigmoid(z) = 1 / (1 + e^-z). */
+typedef enum rapt_act {
+  RAPT_ACT_NONE = 0,
+  RAPT_ACT_SILU = 1,
+  RAPT_ACT_GELU = 2,
+  RAPT_ACT_RELU = 3,
+  RAPT_ACT_SIGMOID = 4
+} rapt_act;
+
+/*
+ * The join of a block's output with the residual stream, and the norm before the next block, for
+ * every row of D values:
+ *   n = w_post * y * (mean(y^2) + eps)^(-1/2)     the norm after the block (w_post NULL: n = y)
+ *   r = x + scale * act(gate) * n                 (scale NULL: 1; gate NULL: no gate)
+ *   h = w_pre * r * (mean(r^2) + eps)^(-1/2)      the norm before the next block
+ *   x, y, gate       [T, D] of `dtype`: residual stream, block output, gate before its activation.
+ *                    y NULL: r = x (the norm before the first block); gate, w_post and scale are
+ *                    then NULL, too.
+ *   w_post, scale, w_pre  fp32 [D].
+ *   r, h             nullable [T, D] of `dtype`, at least one of them; h needs w_pre. h is formed
+ *                    from r before r's rounding. Each may be x, y or gate itself (a row's values are
+ *                    read before any of them is overwritten), but not the other.
+ * All arithmetic is fp32; outputs are rounded once. Requirements: T >= 0 (0 does nothing; the
+ * [T, D] pointers are not looked at),
+ * 1 <= D <= 16384 (RAPT_ERR_UNSUPPORTED beyond), eps finite and > 0. Rows of any length are taken;
+ * those of a multiple of 16 bytes are read and written 16 bytes at a time. A row depends on no other.
+ */
+rapt_status rapt_residual_norm_fwd(const void* x, const void* y, const void* gate, rapt_dtype dtype,
+                                   int32_t T, int32_t D, rapt_act act, const float* w_post,
+                                   const float* scale, const float* w_pre, float eps, void* r, void* h,
+                                   rapt_stream_t stream);
+
+/*
+ * Gradients of sum(dr * r) + sum(dh * h) for rapt_residual_norm_fwd, everything formed again from
+ * the forward's inputs.
+ *   dr, dh           [T, D] of `dtype`, either may be NULL (zero), not both. dh needs x and w_pre;
+ *                    x may be NULL without dh.
+ *   dx, dy, dgate    nullable [T, D] of `dtype`; dy and dgate need y and gate. Each may be any of the
+ *                    [T, D] inputs itself, but no two of them the same.
+ *   dw_post, dscale, dw_pre  nullable fp32 [D]; each needs its gain (dw_pre needs dh, too). Sums over
+ *                    all rows (zeros for T = 0) in fp32 and in a fixed order: the same bits every
+ *                    time on the same GPU model.
+ *   workspace        rapt_residual_norm_bwd_workspace_size() bytes, 16-byte aligned, where any of
+ *                    the three sums is asked for (else it may be NULL).
+ * Requirements as for the forward.
+ */
+size_t rapt_residual_norm_bwd_workspace_size(int32_t T, int32_t D, rapt_dtype dtype);
+rapt_status rapt_residual_norm_bwd(const void* dr, const void* dh, const void* x, const void* y,
+                                   const void* gate, rapt_dtype dtype, int32_t T, int32_t D,
+                                   rapt_act act, const float* w_post, const float* scale,
+                                   const float* w_pre, float eps, void* dx, void* dy, void* dgate,
+                                   float* dw_post, float* dscale, float* dw_pre, void* workspace,
+                                   size_t workspace_bytes, rapt_stream_t stream);
+
+/*
+ * Gated feed-forward: h = act(x w_gate^T) * (x w_up^T), both projections, the activation and the
+ * product in one kernel (the down projection is a rapt_linear_fwd of h).
+ *   x [M, K], w_gate, w_up [F, K] (a linear layer's weights), h [M, F], all bf16.
+ * Tensor cores, fp32 accumulation; act and the product are formed in fp32 and rounded once.
+ * Requirements: M >= 0 (0 does nothing), K % 8 == 0 and F % 8 == 0 (RAPT_ERR_UNSUPPORTED
+ * otherwise); h must not alias an input. A row of h depends on the same row of x alone.
+ * dev_status as for rapt_linear_fwd.
+ */
+rapt_status rapt_glu_fwd(const void* x, const void* w_gate, const void* w_up, int32_t M, int32_t F,
+                         int32_t K, rapt_act act, void* h, uint32_t* dev_status, rapt_stream_t stream);
+
+/*
+ * Gradients of sum(dh * h) for rapt_glu_fwd: with g = x w_gate^T and u = x w_up^T formed again,
+ *   dg = dh * u * act'(g),  du = dh * act(g)            (rounded to bf16: the operands of what follows)
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x.
+ *   dh [M, F], dx [M, K] nullable, dw_gate and dw_up [F, K] both or neither (zeros for M = 0), bf16.
+ *   workspace        rapt_glu_bwd_workspace_size() bytes, 16-byte aligned: dg, du and, where few
+ *                    output tiles share a long sum, fp32 parts of it, added in a fixed order.
+ * Requirements as for the forward; no output aliases an input or another output.
+ */
+size_t rapt_glu_bwd_workspace_size(int32_t M, int32_t F, int32_t K);
+rapt_status rapt_glu_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up, int32_t M,
+                         int32_t F, int32_t K, rapt_act act, void* dx, void* dw_gate, void* dw_up,
+                         uint32_t* dev_status, void* workspace, size_t workspace_bytes,
+                         rapt_stream_t stream);
+
+/*
+ * Gradients of sum(dy * y) for y = x W^T (rapt_linear_fwd; the layer's q | k | v and output
+ * projections): dx = dy W, dw = dy^T x.
+ *   dy [M, N], x [M, K], w [N, K], dx [M, K], dw [N, K], all bf16; dx or dw may be NULL, not both.
+ *   x may be NULL without dw, w without dx. dw is zeros for M = 0.
+ *   workspace        rapt_linear_bwd_workspace_size() bytes, 16-byte aligned (may be 0).
+ * Tensor cores, fp32 accumulation, results rounded once; long sums of few output tiles are split and
+ * their fp32 parts added in a fixed order. Requirements: M >= 0, N % 8 == 0, K % 8 == 0; outputs
+ * alias nothing. dev_status as for rapt_linear_fwd.
+ */
+size_t rapt_linear_bwd_workspace_size(int32_t M, int32_t N, int32_t K);
+rapt_status rapt_linear_bwd(const void* dy, const void* x, const void* w, int32_t M, int32_t N,
+                            int32_t K, void* dx, void* dw, uint32_t* dev_status, void* workspace,
+                            size_t workspace_bytes, rapt_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

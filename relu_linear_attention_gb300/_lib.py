@@ -23,6 +23,11 @@ RAPT_ERR_WORKSPACE = 3
 RAPT_ERR_CUDA = 4
 RAPT_F32 = 0
 RAPT_BF16 = 1
+RAPT_ACT_NONE = 0
+RAPT_ACT_SILU = 1
+RAPT_ACT_GELU = 2
+RAPT_ACT_RELU = 3
+RAPT_ACT_SIGMOID = 4
 RAPT_DEV_BAD_CU_SEQLENS = 1
 RAPT_DEV_INTERNAL = 2
 
@@ -119,6 +124,18 @@ SIGNATURES = {
     "rla_l2_fwd_noalloc": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32,
                                      c_int32, c_int32, c_int32, c_int32, c_float, c_void_p,
                                      c_void_p]),
+    "rapt_residual_norm_fwd": (c_int32, [c_void_p] * 3 + [c_int32] * 4 + [c_void_p] * 3 +
+                               [c_float, c_void_p, c_void_p, c_void_p]),
+    "rapt_residual_norm_bwd_workspace_size": (c_size_t, [c_int32] * 3),
+    "rapt_residual_norm_bwd": (c_int32, [c_void_p] * 5 + [c_int32] * 4 + [c_void_p] * 3 + [c_float] +
+                               [c_void_p] * 7 + [c_size_t, c_void_p]),
+    "rapt_glu_fwd": (c_int32, [c_void_p] * 3 + [c_int32] * 4 + [c_void_p] * 3),
+    "rapt_glu_bwd_workspace_size": (c_size_t, [c_int32] * 3),
+    "rapt_glu_bwd": (c_int32, [c_void_p] * 4 + [c_int32] * 4 + [c_void_p] * 5 +
+                     [c_size_t, c_void_p]),
+    "rapt_linear_bwd_workspace_size": (c_size_t, [c_int32] * 3),
+    "rapt_linear_bwd": (c_int32, [c_void_p] * 3 + [c_int32] * 3 + [c_void_p] * 4 +
+                        [c_size_t, c_void_p]),
 }
 
 RAPT_L2_NOALLOC_SCRATCH_BYTES = 16 << 20

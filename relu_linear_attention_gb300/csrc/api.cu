@@ -81,7 +81,7 @@ const char* rapt_status_string(rapt_status s) {
   }
 }
 
-int32_t rapt_abi_version(void) { return 10300; }
+int32_t rapt_abi_version(void) { return 10400; }
 
 uint64_t rapt_launch_counter(void) { return rapt::launch_count(); }
 

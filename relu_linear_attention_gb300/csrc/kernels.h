@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "activation.cuh"
 #include "common.cuh"
 
 namespace rapt {
@@ -303,5 +304,60 @@ int l2_default_splits(int B, int L, int H);
 size_t l2_workspace_bytes_for_splits(int B, int H, int d, int nsplit);
 cudaError_t launch_rla_l2_with_splits(DType dt, int d, const L2Args& a, int nsplit,
                                       cudaStream_t stream);
+
+// SMs of the current device (asked once per device).
+cudaError_t device_sms(int* sms);
+
+// Norms before and after a block with its gate and residual scale (residual_norm.cu) over T rows of
+// D columns. y, gate, w_post, scale and w_pre may be null; forward: r and h may be null; backward:
+// dr or dh may be null, x is read where dh is given, and dx, dy, dgate may be null. part (backward):
+// the column sums' partials, 3 D floats for each CTA, residual_norm_ws_bytes() in all; null where no
+// gain gradient is asked for.
+struct ResidualNormArgs {
+  const void* x;
+  const void* y;
+  const void* gate;
+  const float* w_post;
+  const float* scale;
+  const float* w_pre;
+  const void* dr;
+  const void* dh;
+  void* r;
+  void* h;
+  void* dx;
+  void* dy;
+  void* dgate;
+  float* part;
+  long T;
+  int D;
+  Act act;
+  float eps;
+};
+constexpr int kResidualNormMaxD = 16384;
+size_t residual_norm_ws_bytes(long T, int D);
+cudaError_t launch_residual_norm_fwd(DType dt, const ResidualNormArgs& a, cudaStream_t stream);
+cudaError_t launch_residual_norm_bwd(DType dt, const ResidualNormArgs& a, float* dw_post, float* dscale,
+                                     float* dw_pre, cudaStream_t stream);
+
+// The gated feed-forward h = act(x w_gate^T) (x w_up^T) and its gradients, and the gradients of
+// y = x w^T, on the tensor cores (block_gemm_tc.cu; bf16, fp32 accumulation). x [M, K], w_gate and
+// w_up [F, K], h and dh [M, F]; dy [M, N], w [N, K]; M > 0; K, F and N multiples of 8. dx, the dw's
+// (both or none) may be null. The workspace holds dg and du (glu) and the partial sums of split
+// tiles.
+struct GluArgs {
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  int M, F, K;
+  Act act;
+  uint32_t* dev_status;
+};
+cudaError_t launch_glu_fwd(const GluArgs& g, void* h, cudaStream_t stream);
+size_t glu_bwd_ws_bytes(int M, int F, int K, bool dx, bool dw);
+cudaError_t launch_glu_bwd(const GluArgs& g, const void* dh, void* dx, void* dw_gate, void* dw_up, void* ws,
+                           cudaStream_t stream);
+size_t linear_bwd_ws_bytes(int M, int N, int K, bool dx, bool dw);
+cudaError_t launch_linear_bwd(const void* dy, const void* x, const void* w, void* dx, void* dw, int M, int N, int K,
+                              void* ws, uint32_t* dev_status, cudaStream_t stream);
 
 }  // namespace rapt
