@@ -8,9 +8,30 @@ namespace rapt {
 
 enum class Act { None = 0, Silu = 1, Gelu = 2, Relu = 3, Sigmoid = 4 };
 
-// 1 / (1 + e^-z), both to about 2 ulp. e^-z overflows to infinity below z = -88; the quotient is
-// then an exact 0.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + e^-z) from the hardware's 2^x and 1/x, each within 2 ulp. e^-z overflows to infinity below
+// z = -88; the quotient is then an exact 0.
+__device__ __forceinline__ float sigmoid_f(float z) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
+
+// The normal distribution function Phi(z), and e^(-z^2 / 2). With x = |z| / sqrt(2), Abramowitz and
+// Stegun's formula 7.1.26 gives erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x), within
+// 1.5e-7, and Phi(-|z|) is half of that: the exponential is the one that the derivative needs.
+__device__ __forceinline__ float phi_f(float z, float& bell) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, x, 1.f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(bell) : "f"(x * x * -1.4426950408889634f));
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  const float tail = 0.5f * q * t * bell;
+  return z < 0.f ? tail : 1.f - tail;
+}
 
 // act(z), and act'(z) where GRAD. relu'(0) = 0.
 template <bool GRAD>
@@ -25,9 +46,10 @@ __device__ __forceinline__ void act_one(Act act, float z, float& a, float& da) {
       if (GRAD) da = z > 0.f ? 1.f : 0.f;
       break;
     case Act::Gelu: {  // z Phi(z); derivative Phi(z) + z phi(z)
-      const float cdf = 0.5f * erfcf(z * -0.70710678118654752f);
+      float bell;
+      const float cdf = phi_f(z, bell);
       a = z * cdf;
-      if (GRAD) da = fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), cdf);
+      if (GRAD) da = fmaf(z * 0.39894228040143268f, bell, cdf);
       break;
     }
     case Act::Sigmoid: {

@@ -308,10 +308,10 @@ cudaError_t launch_rla_l2_with_splits(DType dt, int d, const L2Args& a, int nspl
 // SMs of the current device (asked once per device).
 cudaError_t device_sms(int* sms);
 
-// Norms before and after a block with its gate and residual scale (residual_norm.cu) over T rows of
+// Norms before and after a block with its gate and residual scale (residual_norm_fwd.cu, residual_norm_bwd.cu) over T rows of
 // D columns. y, gate, w_post, scale and w_pre may be null; forward: r and h may be null; backward:
 // dr or dh may be null, x is read where dh is given, and dx, dy, dgate may be null. part (backward):
-// the column sums' partials, 3 D floats for each CTA, residual_norm_ws_bytes() in all; null where no
+// the column sums' partials, 2 D floats for each CTA, residual_norm_ws_bytes() in all; null where no
 // gain gradient is asked for.
 struct ResidualNormArgs {
   const void* x;

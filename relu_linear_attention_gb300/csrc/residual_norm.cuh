@@ -1,0 +1,431 @@
+// Norms before and after a block, fused with its gate and residual scale (sm_103a).
+//
+// Forward, per row of D values (x the residual stream, y the block's output, z its gate):
+//     n = w_post y sg,  sg = (mean y^2 + eps)^(-1/2)      (n = y without a post norm)
+//     r = x + s act(z) n
+//     h = w_pre r rho,  rho = (mean r^2 + eps)^(-1/2)
+// Backward of sum dr . r + sum dh . h, with a = act(z), rh = r rho, yh = y sg, t = w_pre dh:
+//     g  = dr + rho (t - rh mean(t rh)),  dx = g,  dw_pre = sum_rows dh rh
+//     dz = s n act'(z) g,  ds = sum_rows a n g
+//     dn = s a g,  dw_post = sum_rows dn yh,  u = w_post dn,  dy = sg (u - yh mean(u yh))
+// where mean(t rh) = rho mean(t r): the two sums over r need no rho, so they share one reduction.
+//
+// HBM bound: the forward moves 5 tensors, the backward 8, each once. A CTA takes a row at a time (or,
+// below 257 columns, 8 to 32 lanes take one) and keeps the rows ahead of it in flight in a ring in
+// shared memory; each thread copies and reads only its own columns there, so the ring needs no
+// barrier. What is missing (columns past the row's end, rows past the last, absent tensors) is zeros
+// in the ring, so the arithmetic has no branches. The sums of a row are one reduction: beside r's own
+// (sum r^2; backward: also sum t r) it carries sum y^2 of the NEXT row, which that row needs before
+// its r, and the backward's sum u yh = sum e g, with e = s a n the joined term, is split by g's terms,
+//     sum e g = sum e dr + rho sum e t - rho^2 mean(t rh) sum e r,
+// so that it needs no g and no reduction of its own; the rounding of every term stays relative to the
+// terms that g itself adds. With ws = w_post s and G = sum_rows a yh g the gain gradients are
+// dw_post = s G and ds = w_post G: one column sum serves both. Every thread owns the same columns of
+// every row: gains and column sums stay in registers (the sums in fp32, over the CTA's rows). The
+// partial sums go to the workspace, one row per CTA, and a second small launch adds them in CTA order:
+// no atomics, the same bits every time. Arithmetic is fp32 (two values per instruction where there is
+// one); h is formed from the unrounded r and every output is rounded once.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include "activation.cuh"
+#include "kernels.h"
+
+namespace rapt {
+namespace rn {
+
+
+// ---------------------------------------------------------------- two fp32 values per instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// ---------------------------------------------------------------- a thread's columns
+// Four values of a thread, as pairs.
+struct Quad {
+  float2 p[2];
+};
+__device__ __forceinline__ Quad quad(float x) { return {{both(x), both(x)}}; }
+__device__ __forceinline__ Quad operator*(Quad a, Quad b) { return {{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1])}}; }
+__device__ __forceinline__ Quad operator*(Quad a, float b) { return a * quad(b); }
+__device__ __forceinline__ Quad fma4(Quad a, Quad b, Quad c) {
+  return {{fma2(a.p[0], b.p[0], c.p[0]), fma2(a.p[1], b.p[1], c.p[1])}};
+}
+// s + a . b, the two halves of a pair apart
+__device__ __forceinline__ float2 dot4(Quad a, Quad b, float2 s) { return fma2(a.p[1], b.p[1], fma2(a.p[0], b.p[0], s)); }
+
+// How rows lie: in 16-byte vectors; in 4-byte words (one fp32, two bf16); or (bf16 of odd D) with every
+// other row starting in the middle of a word.
+enum class Rows { Vec, Word, HalfWord };
+
+// Thread tx of a row's tpr owns 4 NC columns, as pieces of a vector or a word: piece i starts at column
+// (i tpr + tx) kPer, so that a warp's accesses are contiguous. RING false: no ring (the rows are too
+// wide for one); what would be read there is read from the row itself.
+template <typename T, Rows R, int NC, bool RING>
+struct Cols {
+  static constexpr int kBytes = R == Rows::Vec ? 16 : 4;      // of a piece
+  static constexpr int kPer = kBytes / sizeof(T);             // columns of a piece
+  static constexpr int kPieces = 4 * NC / kPer;
+  static constexpr int kWords = kBytes / 4;
+  static constexpr int kCopies = R == Rows::HalfWord ? 2 : 1;  // ring places of a piece
+  int tx, tpr, D;
+  uint32_t pitch;  // ring bytes of one piece of every thread
+
+  __device__ __forceinline__ Cols(int tx_, int tpr_, int D_)
+      : tx(tx_), tpr(tpr_), D(D_), pitch(blockDim.x * kBytes) {}
+  // Ring bytes of a thread in one stage of `tensors` rows. The threads' places lie side by side, piece
+  // by piece: a warp's copies then arrive as whole lines (a thread's places together made the copies
+  // 16-byte writes and the fp32 forward a third slower).
+  static __host__ __device__ constexpr int stride(int tensors) { return tensors * kPieces * kCopies * kBytes; }
+  __device__ __forceinline__ int col(int i) const { return (i * tpr + tx) * kPer; }
+  // Place `copy` of piece i of tensor slot k, given this thread's first place in a stage.
+  __device__ __forceinline__ uint8_t* at(uint8_t* stage, int k, int i, int copy) const {
+    return stage + ((k * kPieces + i) * kCopies + copy) * pitch;
+  }
+  // Zeros in a tensor slot that nothing is copied to.
+  __device__ __forceinline__ void clear(uint8_t* stage, int k) const {
+    if constexpr (RING) {
+#pragma unroll
+      for (int i = 0; i < kPieces * kCopies; ++i)
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) reinterpret_cast<uint32_t*>(at(stage, k, 0, i))[w] = 0;
+    }
+  }
+  // Starts the copies of this thread's columns of the row at `row` into a tensor slot (columns past the
+  // end keep the zeros of `clear`).
+  __device__ __forceinline__ void fetch(uint8_t* stage, int k, const T* row) const {
+#pragma unroll
+    for (int i = 0; i < (RING ? kPieces : 0); ++i) {
+      const int e = col(i);
+      if (e >= D) continue;
+      const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(at(stage, k, i, 0)));
+      if constexpr (R == Rows::Vec) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + e) : "memory");
+      } else if constexpr (R == Rows::Word) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(row + e) : "memory");
+      } else {
+        // the words that hold columns e and e + 1; of the second only its first half, and that only
+        // where the row starts in the middle of a word and has the column
+        const uintptr_t p = reinterpret_cast<uintptr_t>(row + e), word = p & ~uintptr_t{3};
+        const bool odd = (p & 2) != 0, pair = e + 1 < D, two = odd && pair;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(word), "r"(odd || pair ? 4 : 2)
+                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + pitch), "l"(two ? word + 4 : word),
+                     "r"(two ? 2 : 0)
+                     : "memory");
+      }
+    }
+  }
+  // This thread's columns of the row at `row` (null: zeros), from its tensor slot.
+  __device__ __forceinline__ void read(uint8_t* stage, int k, const T* row, Quad (&f)[NC]) const {
+    float v[4 * NC];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      uint32_t w[kWords] = {};
+      if constexpr (RING) {
+        if constexpr (kBytes == 16) {
+          *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at(stage, k, i, 0));
+        } else {
+          w[0] = *reinterpret_cast<const uint32_t*>(at(stage, k, i, 0));
+          if constexpr (R == Rows::HalfWord) {
+            if ((reinterpret_cast<uintptr_t>(row) & 2) != 0)
+              w[0] = (w[0] >> 16) | (*reinterpret_cast<const uint32_t*>(at(stage, k, i, 1)) << 16);
+          }
+        }
+      } else {
+        const int e = col(i);
+        const T* p = row + e;
+        if (row != nullptr && e < D) {
+          if constexpr (kBytes == 16) {
+            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+          } else if constexpr (R == Rows::Word) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+          } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+            w[0] = h[0] | (e + 1 < D ? static_cast<uint32_t>(h[1]) << 16 : 0u);
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kWords; ++q) {
+        if constexpr (sizeof(T) == 4) {
+          v[i * kPer + q] = __uint_as_float(w[q]);
+        } else {
+          v[i * kPer + 2 * q] = __uint_as_float(w[q] << 16);
+          v[i * kPer + 2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      f[c] = {{make_float2(v[4 * c], v[4 * c + 1]), make_float2(v[4 * c + 2], v[4 * c + 3])}};
+  }
+  // Stores this thread's columns to a row (none where it is null).
+  __device__ __forceinline__ void write(T* row, const Quad (&f)[NC]) const {
+    if (row == nullptr) return;
+    float v[4 * NC];
+    flat(f, v);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int e = col(i);
+      if (e >= D) continue;
+      const float* q = v + i * kPer;
+      if constexpr (sizeof(T) == 4) {
+        if constexpr (kPer == 4)
+          *reinterpret_cast<float4*>(row + e) = make_float4(q[0], q[1], q[2], q[3]);
+        else
+          row[e] = q[0];
+      } else if constexpr (kPer == 8) {
+        __nv_bfloat162 b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(q[2 * k], q[2 * k + 1]);
+        *reinterpret_cast<uint4*>(row + e) = *reinterpret_cast<const uint4*>(b);
+      } else if constexpr (R == Rows::Word) {
+        *reinterpret_cast<__nv_bfloat162*>(row + e) = __floats2bfloat162_rn(q[0], q[1]);
+      } else {
+        row[e] = __float2bfloat16_rn(q[0]);
+        if (e + 1 < D) row[e + 1] = __float2bfloat16_rn(q[1]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void flat(const Quad (&f)[NC], float (&v)[4 * NC]) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      v[4 * c] = f[c].p[0].x;
+      v[4 * c + 1] = f[c].p[0].y;
+      v[4 * c + 2] = f[c].p[1].x;
+      v[4 * c + 3] = f[c].p[1].y;
+    }
+  }
+  // The gains of this thread's columns: ones where there is no gain or no column.
+  __device__ __forceinline__ void gain(const float* w, Quad (&f)[NC]) const {
+    float v[4 * NC];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int e = col(i) + k;
+        v[i * kPer + k] = w != nullptr && e < D ? w[e] : 1.f;
+      }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      f[c] = {{make_float2(v[4 * c], v[4 * c + 1]), make_float2(v[4 * c + 2], v[4 * c + 3])}};
+  }
+  // fp32 column sums to a row of partials.
+  __device__ __forceinline__ void put_sums(float* row, const Quad (&f)[NC]) const {
+    float v[4 * NC];
+    flat(f, v);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (col(i) + k < D) row[col(i) + k] = v[i * kPer + k];
+  }
+};
+
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread's copies have arrived (N < 0: there are none).
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  if constexpr (N >= 0) asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------- reductions
+// Sums eight values over a warp: lane 4 v ends with the sum of value v. Halving the values with the
+// distance takes 9 shuffles where one value at a time takes 40.
+__device__ __forceinline__ float warp_sum8(const float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  float a[4], b[2], c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 16;
+    a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 8;
+    b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+  }
+  const bool up = lane & 4;
+  c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
+// Sums N <= 6 values over the threads of a row. A row of 8, 16 or 32 lanes uses shuffles alone; a row of
+// a whole CTA adds the warps' sums from `red` (two alternating halves, so one barrier per call
+// suffices: a half is rewritten two calls later, after a barrier that follows its last read).
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float (*red)[32][8], int& half) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = tpr >> 5;
+  if (tpr < 32) {
+    for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    return;
+  }
+  if constexpr (N <= 2) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    if (warps == 1) return;
+    if (lane == 0) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) red[half][warp][n] = v[n];
+    }
+  } else {
+    float w[8] = {};
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = v[n];
+    const float c = warp_sum8(w);
+    if (warps == 1) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] = __shfl_sync(0xffffffffu, c, 4 * n);
+      return;
+    }
+    if ((lane & 3) == 0) red[half][warp][lane >> 2] = c;
+  }
+  __syncthreads();
+  // lane 8 j + n adds value n of the warps j, j + 4, ...
+  float c = 0.f;
+  for (int j = lane >> 3; j < warps; j += 4) c += red[half][j][lane & 7];
+  c += __shfl_xor_sync(0xffffffffu, c, 8);
+  c += __shfl_xor_sync(0xffffffffu, c, 16);
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = __shfl_sync(0xffffffffu, c, n);
+  half ^= 1;
+}
+
+// x^(-1/2) within 2^-22.
+__device__ __forceinline__ float inv_root(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// act(z) (ones without a gate) and act'(z) over a thread's columns.
+template <bool GRAD, int NC>
+__device__ __forceinline__ void act_cols(bool gated, Act act, const Quad (&z)[NC], Quad (&a)[NC], Quad (&da)[NC]) {
+  if (!gated) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      a[c] = quad(1.f);
+      if (GRAD) da[c] = quad(0.f);
+    }
+    return;
+  }
+  if (act == Act::Sigmoid || act == Act::Silu) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = z[c].p[i];
+        const float2 s = make_float2(sigmoid_f(x.x), sigmoid_f(x.y)), t = fma2(s, both(-1.f), both(1.f));  // 1 - s
+        if (act == Act::Sigmoid) {
+          a[c].p[i] = s;
+          if (GRAD) da[c].p[i] = mul2(s, t);
+        } else {
+          a[c].p[i] = mul2(x, s);
+          if (GRAD) da[c].p[i] = mul2(s, fma2(x, t, both(1.f)));
+        }
+      }
+    return;
+  }
+  float zz[4 * NC], aa[4 * NC], dd[4 * NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    zz[4 * c] = z[c].p[0].x;
+    zz[4 * c + 1] = z[c].p[0].y;
+    zz[4 * c + 2] = z[c].p[1].x;
+    zz[4 * c + 3] = z[c].p[1].y;
+  }
+  if (act == Act::Gelu) {
+#pragma unroll
+    for (int i = 0; i < 4 * NC; ++i) act_one<GRAD>(Act::Gelu, zz[i], aa[i], dd[i]);
+  } else if (act == Act::Relu) {
+#pragma unroll
+    for (int i = 0; i < 4 * NC; ++i) act_one<GRAD>(Act::Relu, zz[i], aa[i], dd[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4 * NC; ++i) act_one<GRAD>(Act::None, zz[i], aa[i], dd[i]);
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    a[c] = {{make_float2(aa[4 * c], aa[4 * c + 1]), make_float2(aa[4 * c + 2], aa[4 * c + 3])}};
+    if (GRAD) da[c] = {{make_float2(dd[4 * c], dd[4 * c + 1]), make_float2(dd[4 * c + 2], dd[4 * c + 3])}};
+  }
+}
+
+// w_post s and w_pre of a thread's columns.
+template <int NC, typename C>
+__device__ __forceinline__ void load_gains(const ResidualNormArgs& a, const C& in, Quad (&ws)[NC], Quad (&wpre)[NC]) {
+  in.gain(a.w_post, ws);
+  in.gain(a.scale, wpre);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) ws[c] = ws[c] * wpre[c];
+  in.gain(a.w_pre, wpre);
+}
+
+constexpr int kFwdTensors = 3, kBwdTensors = 5;
+
+// Threads of a row (tpr: 8, 16 or 32 lanes of a warp, or a CTA of whole warps) and of a CTA, for EPT
+// columns a thread.
+struct RowShape {
+  int tpr, threads;
+};
+inline RowShape row_shape(int D, int ept) {
+  const int need = (D + ept - 1) / ept;
+  RowShape s;
+  s.tpr = need <= 8 ? 8 : need <= 16 ? 16 : (need + 31) / 32 * 32;
+  s.threads = s.tpr <= 32 ? 256 : s.tpr;
+  return s;
+}
+// Columns a thread of the backward: eight up to 512 threads, then sixteen: a CTA of eight has too few
+// registers a thread beyond (D = 5120 in fp32: 242 us with eight, 204 with sixteen).
+inline int bwd_ept(int D) { return D <= 4096 ? 8 : 16; }
+inline RowShape bwd_shape(int D) { return row_shape(D, bwd_ept(D)); }
+// CTAs of a backward launch at most (its registers hold an SM to 1024 threads): the workspace's rows
+// of partial sums.
+inline int max_parts(const RowShape& s) { return 160 * std::max(1, 1024 / s.threads); }
+
+constexpr size_t kSmemMost = 224 * 1024;  // shared memory that a CTA may ask for beside its 2 KB of sums
+
+// Bytes of a ring of `stages` rows of `tensors` tensors.
+template <typename T, Rows R, int NC>
+size_t ring_bytes(const RowShape& s, int stages, int tensors) {
+  return static_cast<size_t>(stages) * Cols<T, R, NC, true>::stride(tensors) * s.threads;
+}
+
+template <auto KERNEL>
+cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t smem, int most, int* grid,
+                        cudaStream_t stream) {
+  const long slots = s.threads / s.tpr, ctas = (a.T + slots - 1) / slots;
+  int per_sm = 1, sms = 0, dev = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  static std::atomic<unsigned long long> configured{0};  // bit per device
+  if (e == cudaSuccess && (dev >= 64 || !((configured.load(std::memory_order_relaxed) >> dev) & 1ull))) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMost));
+    if (e == cudaSuccess && dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  // all CTAs are resident at once: the rows ahead are then the whole GPU's
+  if (e == cudaSuccess && ctas > sms)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERNEL, s.threads, smem);
+  if (e != cudaSuccess) return e;
+  *grid = static_cast<int>(std::min<long>({ctas, static_cast<long>(sms) * std::max(1, per_sm), most}));
+  KERNEL<<<*grid, s.threads, smem, stream>>>(a, s.tpr);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+// How the rows of a [T, D] tensor lie.
+inline Rows rows_of(DType dt, int D) {
+  if (D % (dt == DType::BF16 ? 8 : 4) == 0) return Rows::Vec;
+  return dt == DType::F32 || D % 2 == 0 ? Rows::Word : Rows::HalfWord;
+}
+
+}  // namespace rn
+}  // namespace rapt

@@ -1,0 +1,244 @@
+// Backward of the residual norm; the mathematics and the layout of the work are in residual_norm.cuh.
+#include "residual_norm.cuh"
+
+namespace rapt {
+namespace {
+
+using namespace rn;
+
+// Partial column sums of CTA b at part[(b * 2 + k) * D + column], k = 0: G, 1: dw_pre.
+template <typename T, Rows R, int NC, int STAGES, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const ResidualNormArgs a, int tpr) {
+  using C = Cols<T, R, NC, (STAGES > 0)>;
+  __shared__ __align__(16) float red[2][32][8];
+  extern __shared__ __align__(16) uint8_t ring[];
+  int half = 0;
+  const int tx = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, D = a.D;
+  const float inv_d = 1.f / static_cast<float>(D);
+  const C in(tx, tpr, D);
+  Quad ws[NC], wpre[NC];
+  load_gains(a, in, ws, wpre);
+  const bool post = a.w_post != nullptr, gated = a.gate != nullptr, joined = a.y != nullptr, normed = a.dh != nullptr;
+  Quad gg[NC], gpre[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) gg[c] = gpre[c] = quad(0.f);
+  const long step = static_cast<long>(gridDim.x) * slots, step_off = step * D;
+  long row = static_cast<long>(blockIdx.x) * slots + slot, off = row * D;
+  uint8_t* const mine = ring + threadIdx.x * C::kBytes;
+  const uint32_t stage_bytes = blockDim.x * C::stride(kBwdTensors);
+  const auto at = [&](const void* t, long o, bool live) { return t != nullptr && live ? static_cast<const T*>(t) + o : nullptr; };
+  // tensor slots of a stage: dh, x, y, gate, dr
+  const auto fetch = [&](uint8_t* st, long rw, long o) {
+    if (rw < a.T) {
+      if (normed) {
+        in.fetch(st, 0, static_cast<const T*>(a.dh) + o);
+        in.fetch(st, 1, static_cast<const T*>(a.x) + o);
+      }
+      if (joined) in.fetch(st, 2, static_cast<const T*>(a.y) + o);
+      if (gated) in.fetch(st, 3, static_cast<const T*>(a.gate) + o);
+      if (a.dr != nullptr) in.fetch(st, 4, static_cast<const T*>(a.dr) + o);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kBwdTensors; ++k) in.clear(st, k);
+    }
+    commit_copies();
+  };
+  const auto y_square = [&](uint8_t* st, const T* y_row) {
+    Quad y[NC];
+    in.read(st, 2, y_row, y);
+    float2 q = both(0.f);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) q = dot4(y[c], y[c], q);
+    return q.x + q.y;
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) {
+#pragma unroll
+    for (int k = 0; k < kBwdTensors; ++k) in.clear(mine + s * stage_bytes, k);
+    fetch(mine + s * stage_bytes, row + s * step, off + s * step_off);
+  }
+  float sg = 1.f;
+  if (post) {
+    wait_copies<STAGES - 1>();
+    float q[1] = {y_square(mine, at(a.y, off, row < a.T))};
+    row_sum<1>(q, tpr, red, half);
+    sg = inv_root(fmaf(q[0], inv_d, a.eps));
+  }
+  uint32_t s = 0;  // offset of the stage
+  // the rows of a warp end together: those past T are zeros and not stored
+  for (long first = static_cast<long>(blockIdx.x) * slots; first < a.T;
+       first += step, row += step, off += step_off) {
+    const bool live = row < a.T;
+    const uint32_t next = s + stage_bytes == STAGES * stage_bytes ? 0 : s + stage_bytes;
+    uint8_t* const st = mine + s;
+    wait_copies<STAGES - 2>();  // this row and the next
+    Quad r[NC], av[NC], da[NC];  // x + e, act(z), act'(z): kept over the reduction
+    float q[6];
+    {
+      Quad e[NC], t[NC], d[NC];
+      if (gated) in.read(st, 3, at(a.gate, off, live), t);
+      act_cols<true>(gated, a.act, t, av, da);
+      in.read(st, 2, at(a.y, off, live), e);
+      in.read(st, 1, at(normed ? a.x : nullptr, off, live), r);
+  #pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        e[c] = e[c] * sg * ws[c] * av[c];
+        r[c] = fma4(e[c], quad(1.f), r[c]);
+      }
+      in.read(st, 0, at(a.dh, off, live), t);
+      in.read(st, 4, at(a.dr, off, live), d);
+        float2 rr = both(0.f), tr = rr, ed = rr, et = rr, er = rr;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        t[c] = t[c] * wpre[c];
+        rr = dot4(r[c], r[c], rr);
+        tr = dot4(t[c], r[c], tr);
+        ed = dot4(e[c], d[c], ed);
+        et = dot4(e[c], t[c], et);
+        er = dot4(e[c], r[c], er);
+      }
+      q[0] = rr.x + rr.y;
+      q[1] = tr.x + tr.y;
+      q[2] = ed.x + ed.y;
+      q[3] = et.x + et.y;
+      q[4] = er.x + er.y;
+    }
+    q[5] = post ? y_square(mine + next, at(a.y, off + step_off, row + step < a.T)) : 0.f;
+    row_sum<6>(q, tpr, red, half);
+    const float rho = normed ? inv_root(fmaf(q[0], inv_d, a.eps)) : 0.f;
+    const float m = rho * q[1] * inv_d;                                            // mean(t rh)
+    const float my = post ? inv_d * (q[2] + rho * (q[3] - rho * m * q[4])) : 0.f;  // mean(u yh)
+    Quad g[NC], y[NC], t[NC];
+    in.read(st, 4, at(a.dr, off, live), g);
+    in.read(st, 0, at(a.dh, off, live), t);
+    in.read(st, 2, at(a.y, off, live), y);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const Quad rh = r[c] * rho;
+      gpre[c] = fma4(t[c], rh, gpre[c]);
+      g[c] = fma4(quad(rho), fma4(rh, quad(-m), t[c] * wpre[c]), g[c]);
+    }
+    in.write(a.dx != nullptr && live ? static_cast<T*>(a.dx) + off : nullptr, g);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      y[c] = y[c] * sg;  // yh
+      const Quad ag = av[c] * g[c];
+      gg[c] = fma4(ag, y[c], gg[c]);
+      da[c] = da[c] * g[c] * (y[c] * ws[c]);
+      g[c] = fma4(y[c], quad(-my), ws[c] * ag) * sg;
+    }
+    in.write(a.dgate != nullptr && live ? static_cast<T*>(a.dgate) + off : nullptr, da);
+    in.write(a.dy != nullptr && live ? static_cast<T*>(a.dy) + off : nullptr, g);
+    fetch(st, row + STAGES * step, off + STAGES * step_off);
+    if (post) sg = inv_root(fmaf(q[5], inv_d, a.eps));
+    s = next;
+  }
+  if (a.part == nullptr) return;
+  float* out = a.part + static_cast<long>(blockIdx.x) * 2 * D;
+  if (slots == 1) {
+    in.put_sums(out, gg);
+    in.put_sums(out + D, gpre);
+    return;
+  }
+  // the slots' sums meet in shared memory, where no copy is on its way any more
+  wait_copies<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);
+  in.put_sums(sums + slot * 2 * D, gg);
+  in.put_sums(sums + slot * 2 * D + D, gpre);
+  __syncthreads();
+  for (int e = threadIdx.x; e < 2 * D; e += blockDim.x) {
+    float v = 0.f;
+    for (int i = 0; i < slots; ++i) v += sums[i * 2 * D + e];
+    out[e] = v;
+  }
+}
+
+// The gain gradients: the CTAs' partial sums added in a fixed order. blockIdx.y picks G (dw_post = s G,
+// dscale = w_post G) or dw_pre; 32 x 32 threads take 32 columns: thread (c, q) adds partials q, q + 32,
+// ..., then the 32 sums of a column are added in order of q. No partials (T = 0) gives zeros.
+struct GainGrads {
+  const float *part, *w_post, *scale;
+  float *dw_post, *dscale, *dw_pre;
+  int nparts, D;
+};
+__global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const GainGrads a) {
+  __shared__ float s[32][33];
+  const int k = blockIdx.y, c = blockIdx.x * 32 + threadIdx.x;
+  float v = 0.f;
+  if (c < a.D) {
+#pragma unroll 8
+    for (int b = threadIdx.y; b < a.nparts; b += 32) v += a.part[(static_cast<long>(b) * 2 + k) * a.D + c];
+  }
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= a.D) return;
+  float t = 0.f;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) t += s[q][threadIdx.x];
+  if (k == 1) {
+    if (a.dw_pre != nullptr) a.dw_pre[c] = t;
+    return;
+  }
+  if (a.dw_post != nullptr) a.dw_post[c] = a.scale != nullptr ? a.scale[c] * t : t;
+  if (a.dscale != nullptr) a.dscale[c] = a.w_post != nullptr ? a.w_post[c] * t : t;
+}
+
+template <typename T, Rows R, int NC, int STAGES, int MAXT, int MINB>
+cudaError_t go(const ResidualNormArgs& a, const RowShape& s, int* grid, cudaStream_t stream) {
+  size_t smem = ring_bytes<T, R, NC>(s, STAGES, kBwdTensors);
+  // the slots' column sums meet where the ring was
+  if (s.tpr <= 32) smem = std::max(smem, static_cast<size_t>(s.threads / s.tpr) * 2 * a.D * 4);
+  if constexpr (STAGES > 0 && NC > 2) {  // eight columns a thread always fit
+    if (smem > kSmemMost) return go<T, R, NC, 0, MAXT, MINB>(a, s, grid, stream);
+  }
+  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, max_parts(s), grid, stream);
+}
+// Stages of the ring: what lies in flight decides the rate, up to a point. bf16, % of the copy rate with
+// 2 / 3 / 4 stages: D = 256: 74 / 92 / 82, D = 2048 (two CTAs of 256 threads an SM): 60 / 80 / 78,
+// D = 4096 (one of 512): 51 / - / 72. fp32 and split words fill the shared memory with two.
+template <typename T, Rows R>
+cudaError_t pick(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {
+  constexpr bool kNarrow = Cols<T, R, 2, true>::stride(1) == 16;  // ring bytes of eight columns
+  const RowShape s = bwd_shape(a.D);
+  if (bwd_ept(a.D) == 8) {
+    if (s.threads <= 256) return go<T, R, 2, kNarrow ? 3 : 2, 256, 2>(a, s, grid, stream);
+    return go<T, R, 2, kNarrow ? 4 : 2, 512, 1>(a, s, grid, stream);
+  }
+  if (s.threads <= 384) return go<T, R, 4, 2, 384, 1>(a, s, grid, stream);
+  if (s.threads <= 512) return go<T, R, 4, 2, 512, 1>(a, s, grid, stream);
+  return go<T, R, 4, 0, 1024, 1>(a, s, grid, stream);
+}
+
+}  // namespace
+
+size_t residual_norm_ws_bytes(long T, int D) {
+  const RowShape s = bwd_shape(D);
+  const long slots = s.threads / s.tpr;
+  return static_cast<size_t>(std::min<long>((T + slots - 1) / slots, max_parts(s))) * 2 * D * 4;
+}
+
+cudaError_t launch_residual_norm_bwd(DType dt, const ResidualNormArgs& a, float* dw_post, float* dscale,
+                                     float* dw_pre, cudaStream_t stream) {
+  int grid = 0;
+  if (a.T > 0) {
+    const Rows r = rows_of(dt, a.D);
+    cudaError_t e;
+    if (dt == DType::F32)
+      e = r == Rows::Vec ? pick<float, Rows::Vec>(a, &grid, stream)
+                           : pick<float, Rows::Word>(a, &grid, stream);
+    else if (r == Rows::Vec)
+      e = pick<__nv_bfloat16, Rows::Vec>(a, &grid, stream);
+    else
+      e = r == Rows::Word ? pick<__nv_bfloat16, Rows::Word>(a, &grid, stream)
+                          : pick<__nv_bfloat16, Rows::HalfWord>(a, &grid, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (dw_post == nullptr && dscale == nullptr && dw_pre == nullptr) return cudaSuccess;
+  const GainGrads g{a.part, a.w_post, a.scale, dw_post, dscale, dw_pre, grid, a.D};
+  residual_norm_sum_kernel<<<dim3((a.D + 31) / 32, 2), dim3(32, 32), 0, stream>>>(g);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace rapt

@@ -51,7 +51,7 @@ def test_residual_norm_bwd_refuses(lib, kw, code):
 
 def test_workspace_queries(lib):
     q = lib.rapt_residual_norm_bwd_workspace_size
-    assert q(0, 64, 1) == 0 and q(1, 64, 1) == 3 * 64 * 4
+    assert q(0, 64, 1) == 0 and q(1, 64, 1) == 2 * 64 * 4
     assert q(1 << 20, 2048, 1) == q(1 << 21, 2048, 1) > 0  # bounded by the GPU, not by the rows
     assert q(4, 16385, 1) == 0 and q(4, 64, 3) == 0 and q(-1, 64, 1) == 0
     g = lib.rapt_glu_bwd_workspace_size
