@@ -450,17 +450,9 @@ cudaError_t launch(GemmArgs a, const Maps& maps, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = device_sms(&sms);
   if (e != cudaSuccess) return e;
-  static std::atomic<unsigned long long> configured{0};  // bit per device
   const auto kernel = block_gemm_kernel<USE, G>;
-  if (dev >= 64 || !((configured.load(std::memory_order_relaxed) >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
-    if (e != cudaSuccess) return e;
-    if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
-  const long units = static_cast<long>(a.tiles_m) * a.tiles_n * a.products * a.parts;
-  const long workers = std::min<long>(units, sms / G);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(workers * G));
+  cfg.gridDim = dim3(static_cast<unsigned>(sms / G * G));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
@@ -471,6 +463,18 @@ cudaError_t launch(GemmArgs a, const Maps& maps, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  static std::atomic<int> resident[64] = {};  // CTAs or pairs that run at once, per device
+  int workers = dev < 64 ? resident[dev].load(std::memory_order_relaxed) : 0;
+  if (workers == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&workers, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (workers < 1) return cudaErrorInvalidConfiguration;
+    if (dev < 64) resident[dev].store(workers, std::memory_order_relaxed);
+  }
+  const long units = static_cast<long>(a.tiles_m) * a.tiles_n * a.products * a.parts;
+  workers = static_cast<int>(std::min<long>(units, workers));
+  cfg.gridDim = dim3(static_cast<unsigned>(workers * G));
   e = cudaLaunchKernelEx(&cfg, kernel, a, maps);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -492,7 +496,7 @@ cudaError_t sum_parts(const GemmArgs& a, void* out0, void* out1, cudaStream_t st
   return cudaGetLastError();
 }
 
-constexpr int kG = 1;
+constexpr int kG = 2;
 
 size_t partial_bytes(long tiles, int nk) {
   const int parts = plan_parts<kG>(tiles, nk);
