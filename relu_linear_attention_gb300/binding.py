@@ -336,51 +336,54 @@ _ACT = {"none": _lib.RAPT_ACT_NONE, "silu": _lib.RAPT_ACT_SILU, "gelu": _lib.RAP
         "relu": _lib.RAPT_ACT_RELU, "sigmoid": _lib.RAPT_ACT_SIGMOID}
 
 
-def _like(name, t, dtype, shape, device):
-    """t is a contiguous CUDA tensor of this dtype, shape and device."""
-    if t.is_cuda and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+def _like(name, t, dtype, shape, index):
+    """The address of t, a contiguous tensor of this dtype and shape on CUDA device `index`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and t.is_contiguous():
         return t.data_ptr()
     _cuda_contig(name, t, dtype, shape)
-    raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
 
 
-def _opt_like(name, t, dtype, shape, device):
-    return None if t is None else _like(name, t, dtype, shape, device)
+def _opt_like(name, t, dtype, shape, index):
+    return None if t is None else _like(name, t, dtype, shape, index)
 
 
 def _act_code(act):
-    _need(act in _ACT, "act must be one of %s, got %r" % (sorted(_ACT), act))
-    return _ACT[act]
+    code = _ACT.get(act)
+    if code is None:
+        raise ValueError("act must be one of %s, got %r" % (sorted(_ACT), act))
+    return code
 
 
-def _launch(device, stream, call):
-    """call(stream handle) with `device` current; what it allocates belongs to the stream it launches on."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
+def _launch(index, stream, call):
+    """call(stream handle) with CUDA device `index` current; what it allocates belongs to the stream it
+    launches on."""
+    if stream is None and index == torch.cuda.current_device():
+        # the handle alone: a stream object costs 3 us on the host, as much as the launch
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
         s = torch.cuda.current_stream() if stream is None else stream
-        _need(s.device == device, "stream is on %s, the tensors on %s" % (s.device, device))
+        _need(s.device_index == index, "stream and tensors are on different devices")
         with torch.cuda.stream(s):
             return call(s.cuda_stream)
 
 
-def _scratch(need, workspace, device):
-    """(pointer, bytes) of the caller's workspace, or of a new one of `need` bytes, and its owner."""
+def _scratch(need, workspace, like):
+    """(address, bytes, owner) of the caller's workspace, or of a new one of `need` bytes."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, device=device, dtype=torch.uint8)
-    _need(workspace.is_cuda and workspace.is_contiguous() and workspace.device == device,
-          "workspace must be a contiguous tensor on %s" % device)
+        workspace = like.new_empty(need, dtype=torch.uint8)
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _status_ptr(dev_status, device):
+def _status_ptr(dev_status, index):
     if dev_status is None:
         return None
-    _cuda_contig("dev_status", dev_status, torch.int32)
-    _need(dev_status.numel() >= 1 and dev_status.device == device, "dev_status must be on %s" % device)
-    return dev_status.data_ptr()
+    _need(dev_status.numel() >= 1, "dev_status must have an element")
+    return _like("dev_status", dev_status, torch.int32, dev_status.shape, index)
 
 
 def rapt_residual_norm_fwd(x, y=None, *, gate=None, w_post=None, scale=None, w_pre=None,
@@ -389,30 +392,35 @@ def rapt_residual_norm_fwd(x, y=None, *, gate=None, w_post=None, scale=None, w_p
     x, y, gate [..., D] (fp32 or bf16), gains fp32 [D]; each of y, gate, w_post and scale may be
     missing (see include/rapt.h). Returns (r, h): r is x itself without y unless an r is passed, h is
     None without w_pre. r and h may be passed to be written, and may be x, y or gate themselves."""
-    dev, dt, shape = x.device, x.dtype, x.shape
+    di, dt, shape = x.get_device(), x.dtype, x.shape
     _need(dt in _DT, "dtype must be float32 or bfloat16")
-    _need(x.dim() >= 1, "x must be [..., D]")
+    _need(len(shape) >= 1, "x must be [..., D]")
     D = shape[-1]
-    xp, yp = _like("x", x, dt, shape, dev), _opt_like("y", y, dt, shape, dev)
-    gp = _opt_like("gate", gate, dt, shape, dev)
-    f32, row = torch.float32, (D,)
-    wp, sp = _opt_like("w_post", w_post, f32, row, dev), _opt_like("scale", scale, f32, row, dev)
-    pp = _opt_like("w_pre", w_pre, f32, row, dev)
+    xp, yp = _like("x", x, dt, shape, di), _opt_like("y", y, dt, shape, di)
+    gp = _opt_like("gate", gate, dt, shape, di)
+    f32, row = torch.float32, shape[-1:]
+    wp, sp = _opt_like("w_post", w_post, f32, row, di), _opt_like("scale", scale, f32, row, di)
+    pp = _opt_like("w_pre", w_pre, f32, row, di)
+    rp, hp = _opt_like("r", r, dt, shape, di), _opt_like("h", h, dt, shape, di)
     _need(h is None or w_pre is not None, "h needs w_pre")
     T = x.numel() // D if D else 0
     code, lib = _act_code(act), _lib.load()
 
     def call(s):
-        ro = torch.empty_like(x) if r is None and y is not None else r
-        ho = torch.empty_like(x) if h is None and w_pre is not None else h
-        st = lib.rapt_residual_norm_fwd(xp, yp, gp, _DT[dt], T, D, code, wp, sp, pp, eps,
-                                        _opt_like("r", ro, dt, shape, dev),
-                                        _opt_like("h", ho, dt, shape, dev), s)
+        ro, ho = r, h
+        if ro is None and y is not None:
+            ro = torch.empty_like(x)
+        if ho is None and w_pre is not None:
+            ho = torch.empty_like(x)
+        st = lib.rapt_residual_norm_fwd(
+            xp, yp, gp, _DT[dt], T, D, code, wp, sp, pp, eps,
+            rp if ro is None or rp is not None else ro.data_ptr(),
+            hp if ho is None or hp is not None else ho.data_ptr(), s)
         if st:
             _lib.check("rapt_residual_norm_fwd", st)
         return (x if ro is None else ro), ho
 
-    return _launch(dev, stream, call)
+    return _launch(di, stream, call)
 
 
 def rapt_residual_norm_bwd(dr, dh, x, y=None, *, gate=None, w_post=None, scale=None, w_pre=None,
@@ -424,32 +432,39 @@ def rapt_residual_norm_bwd(dr, dh, x, y=None, *, gate=None, w_post=None, scale=N
     [..., D] inputs."""
     first = dr if dr is not None else dh
     _need(first is not None, "one of dr and dh is needed")
-    dev, dt, shape = first.device, first.dtype, first.shape
+    di, dt, shape = first.get_device(), first.dtype, first.shape
     _need(dt in _DT, "dtype must be float32 or bfloat16")
-    _need(first.dim() >= 1, "dr and dh must be [..., D]")
+    _need(len(shape) >= 1, "dr and dh must be [..., D]")
     D = shape[-1]
-    ins = [_opt_like(n, t, dt, shape, dev)
-           for n, t in (("dr", dr), ("dh", dh), ("x", x), ("y", y), ("gate", gate))]
-    row, f32 = (D,), torch.float32
-    gains = [_opt_like(n, t, f32, row, dev)
-             for n, t in (("w_post", w_post), ("scale", scale), ("w_pre", w_pre))]
+    ins = (_opt_like("dr", dr, dt, shape, di), _opt_like("dh", dh, dt, shape, di),
+           _opt_like("x", x, dt, shape, di), _opt_like("y", y, dt, shape, di),
+           _opt_like("gate", gate, dt, shape, di))
+    row, f32 = shape[-1:], torch.float32
+    gains = (_opt_like("w_post", w_post, f32, row, di), _opt_like("scale", scale, f32, row, di),
+             _opt_like("w_pre", w_pre, f32, row, di))
     T = first.numel() // D if D else 0
     code, lib = _act_code(act), _lib.load()
 
     def call(s):
         def out(name, t, wanted):
-            if t is None and wanted:
-                t = torch.empty(shape, device=dev, dtype=dt)
-            return t, _opt_like(name, t, dt, shape, dev)
+            if t is not None:
+                return t, _like(name, t, dt, shape, di)
+            if not wanted:
+                return None, None
+            t = torch.empty_like(first)
+            return t, t.data_ptr()
 
         ox, oxp = out("dx", dx, need_dx)
         oy, oyp = out("dy", dy, need_dy and y is not None)
         og, ogp = out("dgate", dgate, need_dgate and gate is not None)
-        wanted = (need_dw and w_post is not None, need_dw and scale is not None,
-                  need_dw and w_pre is not None and dh is not None)
-        sums = [torch.empty(row, device=dev, dtype=f32) if k else None for k in wanted]
-        need = lib.rapt_residual_norm_bwd_workspace_size(T, D, _DT[dt]) if any(wanted) else 0
-        wsp, wsb, _keep = _scratch(need, workspace, dev)
+        sums = [None] * 3
+        wsp, wsb, _keep = None, 0, None
+        if need_dw:
+            sums = [None if w is None else torch.empty_like(w)
+                    for w in (w_post, scale, w_pre if dh is not None else None)]
+            if any(t is not None for t in sums):
+                need = lib.rapt_residual_norm_bwd_workspace_size(T, D, _DT[dt])
+                wsp, wsb, _keep = _scratch(need, workspace, first)
         st = lib.rapt_residual_norm_bwd(*ins, _DT[dt], T, D, code, *gains, eps, oxp, oyp, ogp,
                                         *[None if t is None else t.data_ptr() for t in sums],
                                         wsp, wsb, s)
@@ -457,60 +472,64 @@ def rapt_residual_norm_bwd(dr, dh, x, y=None, *, gate=None, w_post=None, scale=N
             _lib.check("rapt_residual_norm_bwd", st)
         return (ox, oy, og, *sums)
 
-    return _launch(dev, stream, call)
+    return _launch(di, stream, call)
 
 
 def rapt_glu_fwd(x, w_gate, w_up, *, act="silu", h=None, dev_status=None, stream=None):
     """Gated feed-forward h = act(x w_gate^T) (x w_up^T): x [..., K], w_gate and w_up [F, K], bf16.
     Returns h [..., F] bf16."""
-    dev, bf16 = x.device, torch.bfloat16
-    _need(x.dim() >= 1 and w_gate.dim() == 2, "x [..., K], w_gate and w_up [F, K]")
-    K, F = x.shape[-1], w_gate.shape[0]
-    xp = _like("x", x, bf16, x.shape, dev)
-    gp, up = _like("w_gate", w_gate, bf16, (F, K), dev), _like("w_up", w_up, bf16, (F, K), dev)
-    shape = x.shape[:-1] + (F,)
-    code, lib, sp = _act_code(act), _lib.load(), _status_ptr(dev_status, dev)
+    di, bf16, xs, ws = x.get_device(), torch.bfloat16, x.shape, w_gate.shape
+    _need(len(xs) >= 1 and len(ws) == 2 and ws[1] == xs[-1], "x [..., K], w_gate and w_up [F, K]")
+    F, K = ws
+    xp = _like("x", x, bf16, xs, di)
+    gp, up = _like("w_gate", w_gate, bf16, ws, di), _like("w_up", w_up, bf16, ws, di)
+    shape = xs[:-1] + ws[:1]
+    hp = _opt_like("h", h, bf16, shape, di)
+    code, lib, sp = _act_code(act), _lib.load(), _status_ptr(dev_status, di)
 
     def call(s):
-        o = torch.empty(shape, device=dev, dtype=bf16) if h is None else h
+        o = x.new_empty(shape) if h is None else h
         st = lib.rapt_glu_fwd(xp, gp, up, x.numel() // K if K else 0, F, K, code,
-                              _like("h", o, bf16, shape, dev), sp, s)
+                              o.data_ptr() if h is None else hp, sp, s)
         if st:
             _lib.check("rapt_glu_fwd", st)
         return o
 
-    return _launch(dev, stream, call)
+    return _launch(di, stream, call)
 
 
 def rapt_glu_bwd(dh, x, w_gate, w_up, *, act="silu", need_dx=True, need_dw=True, dx=None,
                  dw_gate=None, dw_up=None, dev_status=None, workspace=None, stream=None):
     """Gradients of sum(dh h) for rapt_glu_fwd: dh [..., F]. Returns (dx, dw_gate, dw_up), None for
     what is not needed."""
-    dev, bf16 = x.device, torch.bfloat16
-    _need(x.dim() >= 1 and w_gate.dim() == 2, "x [..., K], w_gate and w_up [F, K]")
-    K, F = x.shape[-1], w_gate.shape[0]
-    hp = _like("dh", dh, bf16, x.shape[:-1] + (F,), dev)
-    xp = _like("x", x, bf16, x.shape, dev)
-    gp, up = _like("w_gate", w_gate, bf16, (F, K), dev), _like("w_up", w_up, bf16, (F, K), dev)
+    di, bf16, xs, ws = x.get_device(), torch.bfloat16, x.shape, w_gate.shape
+    _need(len(xs) >= 1 and len(ws) == 2 and ws[1] == xs[-1], "x [..., K], w_gate and w_up [F, K]")
+    F, K = ws
+    hp = _like("dh", dh, bf16, xs[:-1] + ws[:1], di)
+    xp = _like("x", x, bf16, xs, di)
+    gp, up = _like("w_gate", w_gate, bf16, ws, di), _like("w_up", w_up, bf16, ws, di)
     M = x.numel() // K if K else 0
-    code, lib, sp = _act_code(act), _lib.load(), _status_ptr(dev_status, dev)
+    code, lib, sp = _act_code(act), _lib.load(), _status_ptr(dev_status, di)
 
     def call(s):
         def out(name, t, like, wanted):
-            if t is None and wanted:
-                t = torch.empty_like(like)
-            return t, _opt_like(name, t, bf16, like.shape, dev)
+            if t is not None:
+                return t, _like(name, t, bf16, like.shape, di)
+            if not wanted:
+                return None, None
+            t = torch.empty_like(like)
+            return t, t.data_ptr()
 
         ox, oxp = out("dx", dx, x, need_dx)
         og, ogp = out("dw_gate", dw_gate, w_gate, need_dw)
         ou, oup = out("dw_up", dw_up, w_up, need_dw)
-        wsp, wsb, _keep = _scratch(lib.rapt_glu_bwd_workspace_size(M, F, K), workspace, dev)
+        wsp, wsb, _keep = _scratch(lib.rapt_glu_bwd_workspace_size(M, F, K), workspace, x)
         st = lib.rapt_glu_bwd(hp, xp, gp, up, M, F, K, code, oxp, ogp, oup, sp, wsp, wsb, s)
         if st:
             _lib.check("rapt_glu_bwd", st)
         return ox, og, ou
 
-    return _launch(dev, stream, call)
+    return _launch(di, stream, call)
 
 
 def rapt_linear_bwd(dy, x, w, *, need_dx=True, need_dw=True, dx=None, dw=None, dev_status=None,
@@ -518,31 +537,32 @@ def rapt_linear_bwd(dy, x, w, *, need_dx=True, need_dw=True, dx=None, dw=None, d
     """Gradients of y = x W^T (rapt_linear_fwd): dx = dy W, dw = dy^T x; dy [..., N], x [..., K],
     w [N, K], bf16. x may be None without dw, w without dx. Returns (dx, dw), None for what is not
     needed."""
-    dev, bf16 = dy.device, torch.bfloat16
-    _need(dy.dim() >= 1, "dy must be [..., N]")
+    di, bf16, ys = dy.get_device(), torch.bfloat16, dy.shape
+    _need(len(ys) >= 1, "dy must be [..., N]")
     need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
     _need(not need_dx or w is not None, "dx needs w")
     _need(not need_dw or x is not None, "dw needs x")
     _need(need_dx or need_dw, "one of dx and dw must be needed")
-    N = dy.shape[-1]
     K = x.shape[-1] if x is not None else w.shape[-1]
-    lead = dy.shape[:-1]
-    yp = _like("dy", dy, bf16, dy.shape, dev)
-    xp, wp = _opt_like("x", x, bf16, lead + (K,), dev), _opt_like("w", w, bf16, (N, K), dev)
+    N, xs, ws = ys[-1], ys[:-1] + (K,), (ys[-1], K)
+    yp = _like("dy", dy, bf16, ys, di)
+    xp, wp = _opt_like("x", x, bf16, xs, di), _opt_like("w", w, bf16, ws, di)
+    dxp, dwp = _opt_like("dx", dx, bf16, xs, di), _opt_like("dw", dw, bf16, ws, di)
     M = dy.numel() // N if N else 0
-    lib, sp = _lib.load(), _status_ptr(dev_status, dev)
+    lib, sp = _lib.load(), _status_ptr(dev_status, di)
 
     def call(s):
-        ox = torch.empty(lead + (K,), device=dev, dtype=bf16) if dx is None and need_dx else dx
-        ow = torch.empty((N, K), device=dev, dtype=bf16) if dw is None and need_dw else dw
-        wsp, wsb, _keep = _scratch(lib.rapt_linear_bwd_workspace_size(M, N, K), workspace, dev)
-        st = lib.rapt_linear_bwd(yp, xp, wp, M, N, K, _opt_like("dx", ox, bf16, lead + (K,), dev),
-                                 _opt_like("dw", ow, bf16, (N, K), dev), sp, wsp, wsb, s)
+        ox = dy.new_empty(xs) if dx is None and need_dx else dx
+        ow = dy.new_empty(ws) if dw is None and need_dw else dw
+        wsp, wsb, _keep = _scratch(lib.rapt_linear_bwd_workspace_size(M, N, K), workspace, dy)
+        st = lib.rapt_linear_bwd(yp, xp, wp, M, N, K,
+                                 ox.data_ptr() if need_dx and dx is None else dxp,
+                                 ow.data_ptr() if need_dw and dw is None else dwp, sp, wsp, wsb, s)
         if st:
             _lib.check("rapt_linear_bwd", st)
         return ox, ow
 
-    return _launch(dev, stream, call)
+    return _launch(di, stream, call)
 
 
 def rapt_layer_fwd(x, w_qkv, w_o, gamma_q, gamma_k, *, heads, eps_norm=1e-6, rope_base=1e4,

@@ -593,6 +593,7 @@ size_t dw_bytes(int M, int N, int K, int products) {
 }  // namespace
 
 cudaError_t launch_glu_fwd(const GluArgs& g, void* h, cudaStream_t stream) {
+  if (g.M <= kGluDecodeRows) return launch_glu_decode(g, h, stream);
   return run_glu<Use::Glu>(g, nullptr, h, h, stream);
 }
 

@@ -353,6 +353,9 @@ struct GluArgs {
   uint32_t* dev_status;
 };
 cudaError_t launch_glu_fwd(const GluArgs& g, void* h, cudaStream_t stream);
+// launch_glu_fwd takes this for few tokens (glu_decode.cu).
+constexpr int kGluDecodeRows = 16;
+cudaError_t launch_glu_decode(const GluArgs& g, void* h, cudaStream_t stream);
 size_t glu_bwd_ws_bytes(int M, int F, int K, bool dx, bool dw);
 cudaError_t launch_glu_bwd(const GluArgs& g, const void* dh, void* dx, void* dw_gate, void* dw_up, void* ws,
                            cudaStream_t stream);
