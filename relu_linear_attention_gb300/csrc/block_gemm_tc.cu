@@ -11,17 +11,21 @@
 //            lies: its rows are the sum's index, so it is an MN-major operand.
 //   Dw       D = dy^T x, one or two products over the tokens that share x: both operands MN-major.
 //
-// One persistent CTA per SM walks units of work: an output tile of 128 rows x 256 accumulator columns,
-// or where the tiles are too few to fill the GPU, one part of a tile's sum (its fp32 partial goes to
-// the workspace and a second launch adds the parts in order). Roles:
-//   warp 0     one thread streams 64-deep slices of A and B by TMA into a ring of stages, in the
+// A pair of CTAs on two SMs forms one tile of 256 rows x up to 256 accumulator columns (cta_group::2):
+// each CTA loads its 128 rows of A and its half of B, and holds its 128 rows of the accumulator; an SM
+// then reads half of what two single tiles would (one CTA a tile, 128 x 256: 1480 TFLOP/s where pairs
+// reach 1890 on 16384 x 2048 x 5504). Pairs are persistent; one walks its whole tiles, then its share of
+// the tiles that are left over for less than a full round of all pairs: those are cut along the sum,
+// evenly, and their fp32 parts go to the workspace, where a second launch adds them in order. Roles in
+// a CTA:
+//   warp 0     one thread streams 64-deep slices of A and B by TMA into a ring of five stages, in the
 //              128-byte-swizzled layout that the tensor core reads (K-major: rows of 64 k; MN-major:
 //              blocks of 64 columns, one row per k);
-//   warp 1     one thread issues the products into one of two 256-column TMEM accumulators;
+//   warp 1     in the pair's even CTA one thread issues the products into one of two accumulators;
 //   warps 2-9  epilogue, two warps per TMEM lane quarter (half of the columns each): the other
 //              accumulator is being filled meanwhile. Each warp stages 32 rows x 64 columns of bf16 in
-//              its own 4 KB and one lane stores them by TMA, which clips ragged edges: no warp waits
-//              for another.
+//              one of its own two buffers and one lane stores them by TMA, which clips ragged edges: no
+//              warp waits for another. GluGrad's dh comes the same way, a tile ahead.
 // Operands past an edge are read as zero by TMA. Every wait is bounded (~1 s); a CTA whose wait gives
 // up sets RAPT_DEV_INTERNAL in the optional status word and stops.
 #include <cuda.h>
@@ -39,178 +43,223 @@ namespace {
 
 enum class Use { Glu, GluGrad, Dx, Dw };
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;  // per CTA: accumulator rows, accumulator columns, slice depth
+constexpr int kBM = 128, kBK = 64;         // rows of a CTA, depth of a slice
+constexpr int kPairRows = 2 * kBM;         // rows of a tile
+constexpr int kAccCols = 256;              // TMEM columns of an accumulator: the widest tile
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr long long kWait = 2000000000LL;  // ~1 s of SM cycles
 constexpr uint32_t kBox = 64 * 64 * 2;     // an MN-major block: 64 k x 64 columns
-constexpr uint32_t kHalf = 128 * kBK * 2;  // 128 rows (or columns) of a slice: 16 KB
-constexpr uint32_t kStageOut = 32 * 64 * 2;
+constexpr uint32_t kA = kBM * kBK * 2;     // a CTA's A of a slice
+constexpr uint32_t kB = kA;                // a CTA's B of a slice: up to 128 columns
+constexpr uint32_t kStage = kA + kB;
+constexpr int kStages = 5;
+constexpr uint32_t kStaged = 32 * 64 * 2;  // a staged 32 x 64 piece of a result
+constexpr uint32_t kOut = kStages * kStage;
+constexpr uint32_t kBar = kOut + 2 * kEpiWarps * kStaged;  // full[S], empty[S], accf[2], acce[2], dh[8]
+constexpr uint32_t kMisc = kBar + (2 * kStages + 4 + kEpiWarps) * 8;  // TMEM base, abort flag
+constexpr uint32_t kSmem = kMisc + 16;
+static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kRaster = 8;  // tile rows taken together
 
-template <int G>
-struct Cfg {
-  static constexpr int kStages = G == 1 ? 4 : 6;
-  static constexpr uint32_t kA = kHalf;
-  static constexpr uint32_t kB = G == 1 ? 2 * kHalf : kHalf;
-  static constexpr uint32_t kStage = kA + kB;
-  static constexpr uint32_t kOut = kStages * kStage;
-  static constexpr uint32_t kBar = kOut + kEpiWarps * kStageOut;  // full[S], empty[S], accf[2], acce[2]
-  static constexpr uint32_t kMisc = kBar + (2 * kStages + 4) * 8;  // TMEM base, abort flag
-  static constexpr uint32_t kSmem = kMisc + 16;
-  static_assert(kSmem <= 232448, "shared memory budget");
-};
-
-// The tensor maps of one launch: A and B of up to two terms (Glu: B of w_gate, w_up), outputs.
+// The tensor maps of one launch: A and B of up to two terms or products, outputs, dh.
 struct Maps {
   CUtensorMap a[2];
   CUtensorMap b[2];
   CUtensorMap out[2];
+  CUtensorMap dh;
 };
 
+// Pairs are numbered 0 .. workers - 1 in the plan; a GPU with fewer resident pairs takes several
+// numbers each. Tile t < direct is pair (t mod workers)'s, whole. The slices of the other tiles, in
+// order, are dealt out `span` to a pair.
 struct GemmArgs {
-  int rows, cols;        // of an output: M and F (Glu), M and K (Dx), N and K (Dw)
-  int tiles_m, tiles_n;  // output tiles of one product
-  int products;          // 1, or 2 (Dw of w_gate and w_up)
-  int nk[2];             // slices of the terms of one tile's sum
-  int parts;             // parts of a tile's sum (1: results are stored at once)
-  float* partial;        // parts > 1: [unit][CTA of the pair][column / 4][row][4] fp32
+  int rows, cols;            // of an output: M and F (Glu), M and K (Dx), N and K (Dw)
+  int tiles_m, tiles_n;      // output tiles of one product
+  int tiles;                 // of all products
+  int width;                 // output columns of a tile
+  int nk[2];                 // slices of the terms of one tile's sum
+  int workers, direct, span;
+  float* partial;            // parts of cut sums: [2 pair + piece][CTA][column / 4][row][4] fp32
   const __nv_bfloat16* dh;
+  __nv_bfloat16* out[2];
   Act act;
   uint32_t* dev_status;
 };
 
-// Unit u of a launch: product, tile origin and the slices [k0, k1) of its sum.
-struct Unit {
-  int product, m, n, k0, k1;
+struct Tile {
+  int product, m, n;
 };
-__device__ __forceinline__ Unit unit_at(const GemmArgs& a, int u) {
-  Unit r;
-  const int part = u % a.parts;
-  int t = u / a.parts;
-  const int per = a.tiles_m * a.tiles_n;
+// kRaster tile rows at a time, column by column: the tiles in flight share few rows of A and B.
+__device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n) {
+  Tile r;
+  const int per = tiles_m * tiles_n;
   r.product = t / per;
   t -= r.product * per;
-  // kRaster tile rows at a time, column by column: the tiles in flight share few rows of A and B
-  const int band = t / (kRaster * a.tiles_n);
-  const int first = band * kRaster, height = min(kRaster, a.tiles_m - first);
-  t -= first * a.tiles_n;
+  const int band = t / (kRaster * tiles_n);
+  const int first = band * kRaster, height = min(kRaster, tiles_m - first);
+  t -= first * tiles_n;
   r.m = first + t % height;
   r.n = t / height;
-  const int nk = a.nk[0] + a.nk[1];
-  r.k0 = static_cast<int>(static_cast<long>(nk) * part / a.parts);
-  r.k1 = static_cast<int>(static_cast<long>(nk) * (part + 1) / a.parts);
   return r;
 }
 
-// 16 accumulator columns of this thread's lane as floats.
+// Walks the units of a pair: whole tiles, then pieces of cut tiles.
+struct Walk {
+  const GemmArgs& a;
+  const int stride, nk;
+  int worker, next, piece;
+  long at, end;  // slices of the cut tiles
+  // the unit
+  int tile, k0, k1, slot;  // slot: -1 whole, else where its part goes
+  __device__ __forceinline__ Walk(const GemmArgs& a_, int first, int stride_)
+      : a(a_), stride(stride_), nk(a_.nk[0] + a_.nk[1]), worker(first), next(first), piece(0) {
+    start();
+  }
+  __device__ __forceinline__ void start() {
+    const long all = static_cast<long>(a.tiles - a.direct) * nk;
+    next = worker;
+    piece = 0;
+    at = min(static_cast<long>(worker) * a.span, all);
+    end = min(at + a.span, all);
+  }
+  __device__ __forceinline__ bool step() {
+    for (; worker < a.workers; worker += stride, start()) {
+      if (next < a.direct) {
+        tile = next;
+        k0 = 0;
+        k1 = nk;
+        slot = -1;
+        next += a.workers;
+        return true;
+      }
+      if (at < end) {
+        tile = a.direct + static_cast<int>(at / nk);
+        k0 = static_cast<int>(at % nk);
+        k1 = static_cast<int>(min(static_cast<long>(nk), k0 + (end - at)));
+        slot = 2 * worker + piece;
+        ++piece;
+        at += k1 - k0;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
 __device__ __forceinline__ void to_float16(const uint32_t (&u)[16], float (&f)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(u[i]);
 }
-// 16 values as bf16 into columns 16 j .. 16 j + 15 of row `lane` of a staged 32 x 64 tile.
-__device__ __forceinline__ void stage16(uint32_t tile, int lane, int j, const float (&f)[16]) {
+__device__ __forceinline__ void pack16(const float (&f)[16], uint32_t (&u)[8]) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint32_t addr = tile + tc::sw128(lane, 2 * j + q);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(tc::pack_bf16x2(f[8 * q], f[8 * q + 1])),
-                 "r"(tc::pack_bf16x2(f[8 * q + 2], f[8 * q + 3])), "r"(tc::pack_bf16x2(f[8 * q + 4], f[8 * q + 5])),
-                 "r"(tc::pack_bf16x2(f[8 * q + 6], f[8 * q + 7]))
-                 : "memory");
-  }
+  for (int i = 0; i < 8; ++i) u[i] = tc::pack_bf16x2(f[2 * i], f[2 * i + 1]);
 }
+// 16 bf16 into columns 16 j .. 16 j + 15 of row `lane` of a staged 32 x 64 piece.
+__device__ __forceinline__ void stage16(uint32_t piece, int lane, int j, const uint32_t (&u)[8]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece + tc::sw128(lane, 2 * j + q)), "r"(u[4 * q]),
+                 "r"(u[4 * q + 1]), "r"(u[4 * q + 2]), "r"(u[4 * q + 3])
+                 : "memory");
+}
+// Until all but the newest `N` of this warp's stores have read their buffers.
+template <int N>
 __device__ __forceinline__ void stage_free(int lane) {
-  if (lane == 0) tc::bulk_wait_read0();
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
   __syncwarp();
 }
-// Stores the staged tile at column x, row y; TMA clips what lies past an edge of the [rows, cols] output.
-__device__ __forceinline__ void stage_store(uint32_t tile, int lane, const CUtensorMap* map, int x, int y,
+// Stores the staged piece at column x, row y; TMA clips what lies past an edge of the [rows, cols] output.
+__device__ __forceinline__ void stage_store(uint32_t piece, int lane, const CUtensorMap* map, int x, int y,
                                             const GemmArgs& a) {
   tc::fence_async_smem();
   __syncwarp();
-  if (lane == 0 && x < a.cols && y < a.rows) {
-    tcp::tma_store_2d(map, tile, x, y);
+  if (lane == 0) {
+    if (x < a.cols && y < a.rows) tcp::tma_store_2d(map, piece, x, y);
     tc::bulk_commit();
   }
 }
+// 16 bf16 straight to columns col .. col + 15 of a row (cols is a multiple of eight).
+__device__ __forceinline__ void put16(__nv_bfloat16* out, int row, int col, const uint32_t (&u)[8], const GemmArgs& a) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if (row < a.rows && col + 8 * q < a.cols)
+      *reinterpret_cast<uint4*>(out + static_cast<long>(row) * a.cols + col + 8 * q) =
+          make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+}
 
-template <Use USE, int G>
+template <Use USE>
 __global__ void __launch_bounds__(kThreads, 1)
     block_gemm_kernel(const GemmArgs a, const __grid_constant__ Maps maps) {
-  using C = Cfg<G>;
   constexpr bool kGlu = USE == Use::Glu || USE == Use::GluGrad;
   constexpr bool kAMn = USE == Use::Dw, kBMn = !kGlu;
-  constexpr int kTileN = kGlu ? 128 : 256;  // output columns of a tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = G == 1 ? 0 : tcp::cluster_rank();
-  const int units = a.tiles_m * a.tiles_n * a.products * a.parts;
-  const int first = blockIdx.x / G, stride = gridDim.x / G;
+  const int rank = static_cast<int>(tcp::cluster_rank());
+  const int first = blockIdx.x / 2, stride = gridDim.x / 2;
+  const int half = kGlu ? a.width : a.width / 2;  // columns of B that a CTA holds
 
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = tc::smem_u32(smem);
-  const uint32_t bar_full = base + C::kBar, bar_empty = bar_full + 8 * C::kStages;
-  const uint32_t bar_accf = bar_empty + 8 * C::kStages, bar_acce = bar_accf + 16;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kMisc);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
-  const bool misaligned = (base & 1023u) != 0;  // uniform; the swizzled layout needs 1 KB
+  const uint32_t bar_full = base + kBar, bar_empty = bar_full + 8 * kStages;
+  const uint32_t bar_accf = bar_empty + 8 * kStages, bar_acce = bar_accf + 16, bar_dh = bar_acce + 16;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kMisc + 4);
+  const bool run = (base & 1023u) == 0;  // uniform; the swizzled layout needs 1 KB
 
-  if (warp == 1 && !misaligned) tcp::tmem_alloc<G>(tc::smem_u32(s_tmem), 2 * kBN);
+  if (warp == 1 && run) tcp::tmem_alloc<2>(tc::smem_u32(s_tmem), 2 * kAccCols);
   if (tid == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(bar_full + 8 * s, 1);
       tc::mbar_init(bar_empty + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(bar_accf + 8 * b, 1);
-      tc::mbar_init(bar_acce + 8 * b, G * kEpiWarps);
+      tc::mbar_init(bar_acce + 8 * b, 2 * kEpiWarps);
     }
+    for (int e = 0; e < kEpiWarps; ++e) tc::mbar_init(bar_dh + 8 * e, 1);
     tc::mbar_fence_init();
-    *s_abort = misaligned ? 1 : 0;
+    *s_abort = run ? 0 : 1;
   }
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (G == 2) tcp::cluster_sync();  // the other CTA's barriers are ready, too
+  tcp::cluster_sync();  // the other CTA's barriers are ready, too
   tc::fence_after_sync();
   const uint32_t tmem = *s_tmem;
-  const bool run = !misaligned;
+  tc::grid_launch_dependents();
+  tc::grid_dep_wait();  // what the launch before this one in the same call wrote
 
   if (warp == 0) {
     if (lane == 0 && run) {  // TMA producer: this CTA's rows of A and its columns of B
-      const uint32_t full0 = G == 1 ? bar_full : tcp::map_rank(bar_full, 0);
+      const uint32_t full0 = tcp::map_rank(bar_full, 0);
+      // boxes of 64 columns hold an MN-major half, one box of `half` rows a K-major one
+      const int boxes = (half + 63) / 64;
+      const uint32_t bytes = 2 * (kA + (kBMn ? boxes * kBox : half * kBK * 2));
       long g = 0;
       bool ok = true;
-      for (int u = first; u < units && ok; u += stride) {
-        const Unit w = unit_at(a, u);
-        const int m0 = (w.m * G + static_cast<int>(rank)) * kBM, n0 = w.n * kTileN;
+      for (Walk w(a, first, stride); ok && w.step();) {
+        const Tile t = tile_at(w.tile, a.tiles_m, a.tiles_n);
+        const int m0 = (t.m * 2 + rank) * kBM, n0 = t.n * a.width;
         for (int kb = w.k0; kb < w.k1; ++kb, ++g) {
-          const int s = static_cast<int>(g % C::kStages);
-          if (g >= C::kStages && !tcp::wait(bar_empty + 8 * s, ((g / C::kStages) - 1) & 1, kWait)) {
+          const int s = static_cast<int>(g % kStages);
+          if (g >= kStages && !tcp::wait(bar_empty + 8 * s, ((g / kStages) - 1) & 1, kWait)) {
             ok = false;
             break;
           }
-          if (rank == 0) tc::mbar_arrive_expect_tx(bar_full + 8 * s, G * C::kStage);
-          const uint32_t st = base + s * C::kStage, bar = full0 + 8 * s;
+          if (rank == 0) tc::mbar_arrive_expect_tx(bar_full + 8 * s, bytes);
+          const uint32_t st = base + s * kStage, bar = full0 + 8 * s;
           const int term = kb >= a.nk[0] ? 1 : 0, k = (kb - (term ? a.nk[0] : 0)) * kBK;
           if constexpr (kAMn) {
-            const CUtensorMap* ta = &maps.a[w.product];
-            tcp::tma_load_2d<G>(st, ta, m0, k, bar);
-            tcp::tma_load_2d<G>(st + kBox, ta, m0 + 64, k, bar);
+            const CUtensorMap* ta = &maps.a[t.product];
+            tcp::tma_load_2d<2>(st, ta, m0, k, bar);
+            tcp::tma_load_2d<2>(st + kBox, ta, m0 + 64, k, bar);
           } else {
-            tcp::tma_load_2d<G>(st, &maps.a[term], k, m0, bar);
+            tcp::tma_load_2d<2>(st, &maps.a[term], k, m0, bar);
           }
-          const uint32_t sb = st + C::kA;
           if constexpr (kGlu) {
-            if constexpr (G == 1) {
-              tcp::tma_load_2d<G>(sb, &maps.b[0], k, n0, bar);
-              tcp::tma_load_2d<G>(sb + kHalf, &maps.b[1], k, n0, bar);
-            } else {
-              tcp::tma_load_2d<G>(sb, &maps.b[rank], k, n0, bar);
-            }
+            tcp::tma_load_2d<2>(st + kA, &maps.b[rank], k, n0, bar);
           } else {
-            const CUtensorMap* tb = &maps.b[term];
-            const int nb = n0 + static_cast<int>(rank) * 128;
-#pragma unroll
-            for (int q = 0; q < (G == 1 ? 4 : 2); ++q) tcp::tma_load_2d<G>(sb + q * kBox, tb, nb + 64 * q, k, bar);
+            for (int q = 0; q < boxes; ++q)
+              tcp::tma_load_2d<2>(st + kA + q * kBox, &maps.b[term], n0 + rank * half + 64 * q, k, bar);
           }
         }
       }
@@ -218,198 +267,244 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && run && rank == 0) {  // issuer of the products
-      constexpr uint32_t ID = tc::idesc_bf16(kBM * G, kBN, kAMn, kBMn);
+      const uint32_t id = tc::idesc_bf16(kPairRows, 2 * half, kAMn, kBMn);
       long g = 0;
       int i = 0;
       bool ok = true;
-      for (int u = first; u < units && ok; u += stride, ++i) {
-        const Unit w = unit_at(a, u);
+      for (Walk w(a, first, stride); ok && w.step(); ++i) {
         const int buf = i & 1;
         if (i >= 2 && !tcp::wait(bar_acce + 8 * buf, ((i / 2) - 1) & 1, kWait)) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
-        const uint32_t acc = tmem + buf * kBN;
+        const uint32_t acc = tmem + buf * kAccCols;
         for (int kb = w.k0; kb < w.k1; ++kb, ++g) {
-          const int s = static_cast<int>(g % C::kStages);
-          if (!tcp::wait(bar_full + 8 * s, (g / C::kStages) & 1, kWait)) {
+          const int s = static_cast<int>(g % kStages);
+          if (!tcp::wait(bar_full + 8 * s, (g / kStages) & 1, kWait)) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint32_t st = base + s * C::kStage;
+          const uint32_t st = base + s * kStage;
           // 16 k are 32 bytes of a K-major row, 16 rows (2 KB) of an MN-major block
           const uint64_t da = tc::desc_sw128(st, kAMn ? kBox : 16, 1024);
-          const uint64_t db = tc::desc_sw128(st + C::kA, kBMn ? kBox : 16, 1024);
+          const uint64_t db = tc::desc_sw128(st + kA, kBMn ? kBox : 16, 1024);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            tcp::mma_bf16<G>(acc, da + (kAMn ? 128 : 2) * k, db + (kBMn ? 128 : 2) * k, ID,
+            tcp::mma_bf16<2>(acc, da + (kAMn ? 128 : 2) * k, db + (kBMn ? 128 : 2) * k, id,
                              (kb > w.k0 || k > 0) ? 1u : 0u);
-          tcp::mma_commit<G>(bar_empty + 8 * s);
+          tcp::mma_commit<2>(bar_empty + 8 * s);
         }
-        if (ok) tcp::mma_commit<G>(bar_accf + 8 * buf);
+        if (ok) tcp::mma_commit<2>(bar_accf + 8 * buf);
       }
       if (!ok) *s_abort = 1;
     }
   } else if (run) {  // epilogue warps
-    const int e = warp - 2, quarter = warp & 3, half = e >> 2;
+    const int e = warp - 2, quarter = warp & 3, side = e >> 2;
     const uint32_t tl = static_cast<uint32_t>(32 * quarter) << 16;
-    const uint32_t tile = base + C::kOut + e * kStageOut;
+    const uint32_t piece[2] = {base + kOut + 2 * e * kStaged, base + kOut + (2 * e + 1) * kStaged};
+    const uint32_t my_dh = bar_dh + 8 * e;
+    const bool staged_dh = USE == Use::GluGrad && a.width == 128;
+    // GluGrad: dh of the unit after `w` into the second buffer, which the last store has read
+    const auto fetch_dh = [&](const Walk& w) {
+      const Tile t = tile_at(w.tile, a.tiles_m, a.tiles_n);
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(my_dh, kStaged);
+        tcp::tma_load_2d<1>(piece[1], &maps.dh, t.n * 128 + 64 * side, (t.m * 2 + rank) * kBM + 32 * quarter, my_dh);
+      }
+    };
     int i = 0;
-    for (int u = first; u < units; u += stride, ++i) {
-      const Unit w = unit_at(a, u);
+    [[maybe_unused]] uint32_t stores = 0;  // buffers in turn
+    Walk w(a, first, stride);
+    bool more = w.step();
+    if (staged_dh && more) fetch_dh(w);
+    for (; more; ++i) {
       const int buf = i & 1;
-      const bool ok = tcp::wait(bar_accf + 8 * buf, (i / 2) & 1, kWait);
+      const Tile t = tile_at(w.tile, a.tiles_m, a.tiles_n);
+      const int slot = w.slot;
+      const int m0 = (t.m * 2 + rank) * kBM + 32 * quarter, row = m0 + lane;
+      more = w.step();
+      bool ok = tcp::wait(bar_accf + 8 * buf, (i / 2) & 1, kWait);
+      if (staged_dh) ok = ok && tcp::wait(my_dh, i & 1, kWait);
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) *s_abort = 1;
         break;
       }
       tc::fence_after_sync();
-      const int m0 = (w.m * G + static_cast<int>(rank)) * kBM + 32 * quarter;
-      const uint32_t acc = tmem + buf * kBN + tl;
-      if constexpr (kGlu) {
-        const int col0 = w.n * kTileN + 64 * half;
-        [[maybe_unused]] uint32_t keep[32];  // GluGrad: du as bf16, staged after dg
-        stage_free(lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t ug[16], uu[16];
-          tc::tmem_ld16(acc + 64 * half + 16 * j, ug);
-          tc::tmem_ld16(acc + 128 + 64 * half + 16 * j, uu);
-          float d[16];
-          if constexpr (USE == Use::GluGrad) {
-            const int row = m0 + lane, col = col0 + 16 * j;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-              if (row < a.rows && col + 8 * q < a.cols)
-                RowLoad<__nv_bfloat16, 8>::run(a.dh + static_cast<long>(row) * a.cols + col + 8 * q, v);
-#pragma unroll
-              for (int x = 0; x < 8; ++x) d[8 * q + x] = v[x];
-            }
-          }
-          tc::tmem_wait_ld();
-          float gg[16], up[16], av[16], da[16];
-          to_float16(ug, gg);
-          to_float16(uu, up);
-          act_vec<16, USE == Use::GluGrad>(a.act, gg, av, da);
-          if constexpr (USE == Use::Glu) {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) up[x] *= av[x];
-            stage16(tile, lane, j, up);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              up[x] *= d[x] * da[x];  // dg
-              d[x] *= av[x];          // du
-            }
-            stage16(tile, lane, j, up);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) keep[8 * j + x] = tc::pack_bf16x2(d[2 * x], d[2 * x + 1]);
-          }
-        }
-        // the accumulator has been read: the next tile's products may overwrite it
+      const uint32_t acc = tmem + buf * kAccCols + tl;
+      // the accumulator has been read: the next but one tile's products may overwrite it
+      const auto release = [&]() {
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tcp::arrive_cluster(G == 1 ? bar_acce + 8 * buf : tcp::map_rank(bar_acce + 8 * buf, 0));
-        stage_store(tile, lane, &maps.out[0], col0, m0, a);
-        if constexpr (USE == Use::GluGrad) {
-          stage_free(lane);
+        if (lane == 0) tcp::arrive_cluster(tcp::map_rank(bar_acce + 8 * buf, 0));
+      };
+      if constexpr (kGlu) {
+        // this warp's columns: every other group of 64 of a full tile, of 16 of a narrow one
+        const int groups = a.width / 16, step = a.width == 128 ? 1 : 2, j0 = a.width == 128 ? 4 * side : side;
+        const int j1 = a.width == 128 ? j0 + 4 : groups;
+        uint32_t keep[4][8];  // full tiles: du as bf16, staged once dh has been read
+        if (staged_dh) stage_free<0>(lane);
+        if (USE == Use::Glu && a.width == 128) stage_free<1>(lane);
+        const uint32_t out = USE == Use::Glu ? piece[i & 1] : piece[0];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + tc::sw128(lane, j)),
-                         "r"(keep[4 * j]), "r"(keep[4 * j + 1]), "r"(keep[4 * j + 2]), "r"(keep[4 * j + 3])
-                         : "memory");
-          stage_store(tile, lane, &maps.out[1], col0, m0, a);
+        for (int q = 0; q < 4; ++q) {
+          const int j = j0 + q * step;
+          if (j < j1) {
+            const int col = t.n * a.width + 16 * j;
+            uint32_t ug[16], uu[16];
+            tc::tmem_ld16(acc + 16 * j, ug);
+            tc::tmem_ld16(acc + a.width + 16 * j, uu);
+            float d[16];
+            if constexpr (USE == Use::GluGrad) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t v[4] = {0, 0, 0, 0};
+                if (staged_dh)
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                               : "r"(piece[1] + tc::sw128(lane, 2 * q + x))
+                               : "memory");
+                else if (row < a.rows && col + 8 * x < a.cols)
+                  *reinterpret_cast<uint4*>(v) =
+                      *reinterpret_cast<const uint4*>(a.dh + static_cast<long>(row) * a.cols + col + 8 * x);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  d[8 * x + 2 * y] = __uint_as_float(v[y] << 16);
+                  d[8 * x + 2 * y + 1] = __uint_as_float(v[y] & 0xffff0000u);
+                }
+              }
+            }
+            tc::tmem_wait_ld();
+            float gg[16], up[16], av[16], da[16];
+            to_float16(ug, gg);
+            to_float16(uu, up);
+            act_vec<16, USE == Use::GluGrad>(a.act, gg, av, da);
+            uint32_t u[8];
+            if constexpr (USE == Use::Glu) {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) up[x] *= av[x];
+            } else {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                up[x] *= d[x] * da[x];  // dg
+                d[x] *= av[x];          // du
+              }
+              pack16(d, keep[q]);
+              if (a.width != 128) put16(a.out[1], row, col, keep[q], a);
+            }
+            pack16(up, u);
+            if (a.width == 128)
+              stage16(out, lane, q, u);
+            else
+              put16(a.out[0], row, col, u, a);
+          }
         }
-      } else if (a.parts == 1) {
+        release();
+        if (a.width == 128) {
+          const int col = t.n * 128 + 64 * side;
+          stage_store(out, lane, &maps.out[0], col, m0, a);
+          if constexpr (USE == Use::GluGrad) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) stage16(piece[1], lane, q, keep[q]);
+            stage_store(piece[1], lane, &maps.out[1], col, m0, a);
+            if (more) {
+              stage_free<0>(lane);
+              fetch_dh(w);
+            }
+          }
+        }
+      } else if (slot < 0) {
+        // groups of 64 columns in turn
+        const int groups = a.width / 64;
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const int col = 128 * half + 64 * c;
-          stage_free(lane);
+        for (int c = side; c < groups; c += 2) {
+          uint32_t v[4][16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc::tmem_ld16(acc + 64 * c + 16 * j, v[j]);
+          tc::tmem_wait_ld();
+          if (c + 2 >= groups) release();
+          stage_free<1>(lane);
+          const uint32_t out = piece[stores++ & 1];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t v[16];
             float f[16];
-            tc::tmem_ld16(acc + col + 16 * j, v);
-            tc::tmem_wait_ld();
-            to_float16(v, f);
-            stage16(tile, lane, j, f);
+            uint32_t u[8];
+            to_float16(v[j], f);
+            pack16(f, u);
+            stage16(out, lane, j, u);
           }
-          if (c == 1) {
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tcp::arrive_cluster(G == 1 ? bar_acce + 8 * buf : tcp::map_rank(bar_acce + 8 * buf, 0));
-          }
-          stage_store(tile, lane, &maps.out[w.product], w.n * kTileN + col, m0, a);
+          stage_store(out, lane, &maps.out[t.product], t.n * a.width + 64 * c, m0, a);
         }
+        if (side >= groups) release();
       } else {
-        float4* p = reinterpret_cast<float4*>(a.partial) + (static_cast<long>(u) * G + rank) * (kBM * kBN / 4);
+        float4* p = reinterpret_cast<float4*>(a.partial) + (static_cast<long>(slot) * 2 + rank) * (kBM * kAccCols / 4);
+        const int groups = a.width / 32;
 #pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
-          const int col = 128 * half + 16 * j;
-          uint32_t v[16];
-          tc::tmem_ld16(acc + col, v);
+        for (int c = side; c < groups; c += 2) {
+          uint32_t v[2][16];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tc::tmem_ld16(acc + 32 * c + 16 * j, v[j]);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            p[(col / 4 + q) * kBM + 32 * quarter + lane] =
-                make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
-                            __uint_as_float(v[4 * q + 3]));
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              p[(8 * c + 4 * j + q) * kBM + 32 * quarter + lane] =
+                  make_float4(__uint_as_float(v[j][4 * q]), __uint_as_float(v[j][4 * q + 1]),
+                              __uint_as_float(v[j][4 * q + 2]), __uint_as_float(v[j][4 * q + 3]));
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tcp::arrive_cluster(G == 1 ? bar_acce + 8 * buf : tcp::map_rank(bar_acce + 8 * buf, 0));
+        release();
       }
     }
     if (lane == 0) tc::bulk_wait0();  // the stores read this CTA's shared memory
   }
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (G == 2) tcp::cluster_sync();  // no CTA leaves while the other may still signal it
+  tcp::cluster_sync();  // no CTA leaves while the other may still signal it
   if (*s_abort && tid == 0 && a.dev_status != nullptr) atomicOr(a.dev_status, 2u);
   tc::fence_after_sync();
-  if (warp == 1 && !misaligned) tcp::tmem_dealloc<G>(tmem, 2 * kBN);
+  if (warp == 1 && run) tcp::tmem_dealloc<2>(tmem, 2 * kAccCols);
 }
 
-// Adds the parts of every tile's sum in order and rounds once. One thread: one row, 16 columns.
+// Adds the parts of every cut tile in order and rounds once. A CTA takes 128 rows x 16 columns of a tile:
+// a thread adds two quads of columns of a row (parts are stored for reading 32 rows of a quad at once),
+// and the rounded rows are stored through shared memory, 32 bytes each.
 struct SumArgs {
   const float4* partial;
-  int rows, cols, tiles_m, tiles_n, parts;
+  int rows, cols, tiles_m, tiles_n, width, direct, span, nk;
   __nv_bfloat16* out[2];
 };
-template <int G>
 __global__ void __launch_bounds__(256) part_sum_kernel(const SumArgs a) {
-  const int t = blockIdx.x;  // tile of a product, in unit order
-  const int seg = blockIdx.y * 2 + (threadIdx.x >> 7), r = threadIdx.x & 127;  // 16 columns, row of the CTA's 128
-  GemmArgs g{};
-  g.tiles_m = a.tiles_m;
-  g.tiles_n = a.tiles_n;
-  g.parts = 1;
-  const Unit w = unit_at(g, t);
+  __shared__ uint2 rowbuf[kBM][4 + 1];
+  const int cut = blockIdx.x, rank = blockIdx.z, col0 = 16 * blockIdx.y;  // which cut tile, CTA, columns
+  const Tile t = tile_at(a.direct + cut, a.tiles_m, a.tiles_n);
+  const long s0 = static_cast<long>(cut) * a.nk, s1 = s0 + a.nk - 1;
+  const int w0 = static_cast<int>(s0 / a.span), w1 = static_cast<int>(s1 / a.span);
+  const int r = threadIdx.x & (kBM - 1), q = threadIdx.x >> 7;  // row, quads q and q + 2
+  const float4* p = a.partial + static_cast<long>(rank) * (kBM * kAccCols / 4) + (col0 / 4 + q) * kBM + r;
+  float4 s[2] = {};
+  tc::grid_dep_wait();
+#pragma unroll 4
+  for (int w = w0; w <= w1; ++w) {
+    // the first pair's piece is its second one where its share began before this tile
+    const int slot = 2 * w + (static_cast<long>(w) * a.span < s0 ? 1 : 0);
 #pragma unroll
-  for (int rank = 0; rank < G; ++rank) {
-    const int row = (w.m * G + rank) * kBM + r, col = w.n * kBN + 16 * seg;
-    if (row >= a.rows || col >= a.cols) continue;
-    float4 s[4] = {};
-    for (int p = 0; p < a.parts; ++p) {
-      const float4* src = a.partial + ((static_cast<long>(t) * a.parts + p) * G + rank) * (kBM * kBN / 4);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 v = src[(4 * seg + q) * kBM + r];
-        s[q].x += v.x; s[q].y += v.y; s[q].z += v.z; s[q].w += v.w;
-      }
-    }
-    uint4* o = reinterpret_cast<uint4*>(a.out[w.product] + static_cast<long>(row) * a.cols + col);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if (col + 8 * q >= a.cols) break;
-      o[q] = make_uint4(tc::pack_bf16x2(s[2 * q].x, s[2 * q].y), tc::pack_bf16x2(s[2 * q].z, s[2 * q].w),
-                        tc::pack_bf16x2(s[2 * q + 1].x, s[2 * q + 1].y),
-                        tc::pack_bf16x2(s[2 * q + 1].z, s[2 * q + 1].w));
+    for (int i = 0; i < 2; ++i) {
+      const float4 v = p[static_cast<long>(slot) * 2 * (kBM * kAccCols / 4) + 2 * i * kBM];
+      s[i].x += v.x; s[i].y += v.y; s[i].z += v.z; s[i].w += v.w;
     }
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    rowbuf[r][q + 2 * i] = make_uint2(tc::pack_bf16x2(s[i].x, s[i].y), tc::pack_bf16x2(s[i].z, s[i].w));
+  __syncthreads();
+  const int r2 = threadIdx.x >> 1, q2 = threadIdx.x & 1;
+  const int row = (t.m * 2 + rank) * kBM + r2, col = t.n * a.width + col0 + 8 * q2;
+  if (row >= a.rows || col >= a.cols) return;
+  const uint2 lo = rowbuf[r2][2 * q2], hi = rowbuf[r2][2 * q2 + 1];
+  *reinterpret_cast<uint4*>(a.out[t.product] + static_cast<long>(row) * a.cols + col) =
+      make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
 int ceil_div(long a, long b) { return static_cast<int>((a + b - 1) / b); }
@@ -422,184 +517,224 @@ cudaError_t map_2d(CUtensorMap* m, const void* p, int rows, int cols, int box_ro
   return encode_bf16_map(m, p, 2, dims, strides, box);
 }
 
-// Parts of a tile's sum: what finishes first by a count of slices per SM (or pair), where a unit
-// costs kUnit slices beside its own and the second launch moves 8 bytes per partial value.
-constexpr int kPlanSms = 152;
-template <int G>
-int plan_parts(long tiles, int nk) {
-  constexpr double kUnit = 6.0, kLaunch = 14.0;
-  const int workers = kPlanSms / G;
-  double best = 0;
-  int parts = 1;
-  for (int p = 1; p <= 16 && p <= nk; ++p) {
-    double cost = static_cast<double>(ceil_div(tiles * p, workers)) * (ceil_div(nk, p) + kUnit);
-    // a slice is 512 cycles (0.27 us); all SMs together move about 6 KB of partials in a ns
-    if (p > 1) cost += kLaunch + static_cast<double>(tiles) * p * G * kBM * kBN * 8 / 6000.0 / 270.0;
-    if (p == 1 || cost < 0.97 * best) {
-      best = cost;
-      parts = p;
-    }
+// How a launch is dealt out. The unit of cost is a 64-deep slice of a full tile (512 cycles, 0.27 us).
+constexpr int kWorkers = 76;       // pairs of a GB300's 152 SMs
+constexpr double kUnit = 6.0;      // slices that a tile costs beside its own: the ends of its pipeline
+constexpr double kSumLaunch = 10;  // slices of the second launch of a cut plan
+struct Plan {
+  int width, tiles_m, tiles_n, tiles, direct, span;
+  double cost;
+  size_t bytes;
+};
+// Tiles of `width` output columns (`full` at most). A slice of a narrow tile costs more than its share of
+// the products: it still loads the 256 rows of A (half of a full slice's bytes), and the loads of all
+// pairs together keep L2 as busy as the tensor cores (64-column tiles ran at 290 TFLOP/s).
+Plan plan_width(int rows, int cols, int products, int nk, int width, int full, bool may_cut) {
+  const double part = static_cast<double>(width) / full, share = std::max(part, 0.9 * (0.5 + 0.5 * part));
+  Plan p{};
+  p.width = width;
+  p.tiles_m = ceil_div(rows, kPairRows);
+  p.tiles_n = ceil_div(cols, width);
+  p.tiles = p.tiles_m * p.tiles_n * products;
+  p.direct = p.tiles;
+  p.cost = static_cast<double>(ceil_div(p.tiles, kWorkers)) * (nk * share + kUnit);
+  const int left = p.tiles % kWorkers;
+  if (!may_cut || left == 0) return p;
+  // the tiles of the last round, cut: shares of at least four slices; every pair's part is written and
+  // read once, together about 6 KB in a ns
+  const long slices = static_cast<long>(left) * nk;
+  const int span = std::max(4, ceil_div(slices, kWorkers)), pairs = ceil_div(slices, span);
+  const double bytes = static_cast<double>(pairs + left) * kPairRows * width * 8;
+  const double cost = static_cast<double>(p.tiles / kWorkers) * (nk * share + kUnit) + span * share + 2 * kUnit +
+                      kSumLaunch + bytes / 6000.0 / 270.0;
+  if (cost < p.cost) {
+    p.direct = p.tiles - left;
+    p.span = span;
+    p.cost = cost;
+    p.bytes = static_cast<size_t>(2 * pairs) * kPairRows * kAccCols * 4;
   }
-  return parts;
+  return p;
+}
+// The gated products: 128 columns of g and of u a tile, or fewer (a multiple of 16) where that fills the
+// pairs better: M = 256, F = 5504: 43 tiles of 128, 69 of 80.
+Plan plan_glu(int M, int F, int K) {
+  Plan best{};
+  for (int width = 128; width >= 48; width -= 16) {
+    const Plan p = plan_width(M, F, 1, ceil_div(K, kBK), width, 128, false);
+    if (width == 128 || p.cost < 0.95 * best.cost) best = p;
+  }
+  return best;
+}
+// The others: 256 columns, or 192, 128 or 64.
+Plan plan_sum(int rows, int cols, int products, int nk) {
+  Plan best{};
+  for (int width = 256; width >= 64; width -= 64) {
+    const Plan p = plan_width(rows, cols, products, nk, width, 256, true);
+    if (width == 256 || p.cost < 0.97 * best.cost) best = p;
+  }
+  return best;
+}
+Plan plan_dx(int M, int N, int K, int terms) { return plan_sum(M, K, 1, terms * ceil_div(N, kBK)); }
+Plan plan_dw(int M, int N, int K, int products) { return plan_sum(N, K, products, ceil_div(M, kBK)); }
+
+void deal(GemmArgs* a, const Plan& p) {
+  a->width = p.width;
+  a->tiles_m = p.tiles_m;
+  a->tiles_n = p.tiles_n;
+  a->tiles = p.tiles;
+  a->direct = p.direct;
+  a->span = p.span;
+  a->workers = kWorkers;
 }
 
-template <Use USE, int G>
-cudaError_t launch(GemmArgs a, const Maps& maps, cudaStream_t stream) {
-  using C = Cfg<G>;
+// `after`: the launch follows another one of the same call, and may be made ready before that one ends.
+template <Use USE>
+cudaError_t launch(const GemmArgs& a, const Maps& maps, bool after, cudaStream_t stream) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = device_sms(&sms);
   if (e != cudaSuccess) return e;
-  const auto kernel = block_gemm_kernel<USE, G>;
+  const auto kernel = block_gemm_kernel<USE>;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms / G * G));
+  cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = G;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  static std::atomic<int> resident[64] = {};  // CTAs or pairs that run at once, per device
-  int workers = dev < 64 ? resident[dev].load(std::memory_order_relaxed) : 0;
-  if (workers == 0) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&workers, kernel, &cfg);
+  static std::atomic<int> resident[64] = {};  // pairs that run at once, per device
+  int pairs = dev < 64 ? resident[dev].load(std::memory_order_relaxed) : 0;
+  if (pairs == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
     if (e != cudaSuccess) return e;
-    if (workers < 1) return cudaErrorInvalidConfiguration;
-    if (dev < 64) resident[dev].store(workers, std::memory_order_relaxed);
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    if (dev < 64) resident[dev].store(pairs, std::memory_order_relaxed);
   }
-  const long units = static_cast<long>(a.tiles_m) * a.tiles_n * a.products * a.parts;
-  workers = static_cast<int>(std::min<long>(units, workers));
-  cfg.gridDim = dim3(static_cast<unsigned>(workers * G));
+  const int most = a.direct < a.tiles ? a.workers : std::min(a.workers, a.direct);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, most)));
+  cfg.numAttrs = after ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a, maps);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int G>
-cudaError_t sum_parts(const GemmArgs& a, void* out0, void* out1, cudaStream_t stream) {
+cudaError_t sum_parts(const GemmArgs& a, cudaStream_t stream) {
+  if (a.direct == a.tiles) return cudaSuccess;
   SumArgs s{};
   s.partial = reinterpret_cast<const float4*>(a.partial);
   s.rows = a.rows;
   s.cols = a.cols;
   s.tiles_m = a.tiles_m;
   s.tiles_n = a.tiles_n;
-  s.parts = a.parts;
-  s.out[0] = static_cast<__nv_bfloat16*>(out0);
-  s.out[1] = static_cast<__nv_bfloat16*>(out1);
-  part_sum_kernel<G><<<dim3(a.tiles_m * a.tiles_n * a.products, kBN / 32), 256, 0, stream>>>(s);
+  s.width = a.width;
+  s.direct = a.direct;
+  s.span = a.span;
+  s.nk = a.nk[0] + a.nk[1];
+  s.out[0] = a.out[0];
+  s.out[1] = a.out[1];
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.tiles - a.direct, a.width / 16, 2);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, part_sum_kernel, s);
   note_launches(1);
-  return cudaGetLastError();
-}
-
-constexpr int kG = 2;
-
-size_t partial_bytes(long tiles, int nk) {
-  const int parts = plan_parts<kG>(tiles, nk);
-  return parts == 1 ? 0 : static_cast<size_t>(tiles) * parts * kG * kBM * kBN * 4;
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // dx [M, K] = sum over terms of d_t [M, N] w_t [N, K].
 cudaError_t run_dx(const void* const* d, const void* const* w, int terms, void* dx, int M, int N, int K,
-                   float* partial, uint32_t* dev_status, cudaStream_t stream) {
+                   float* partial, uint32_t* dev_status, bool after, cudaStream_t stream) {
   Maps m{};
-  cudaError_t e = cudaSuccess;
-  for (int t = 0; t < 2 && e == cudaSuccess; ++t) {
-    e = map_2d(&m.a[t], d[t < terms ? t : 0], M, N, 128);
-    if (e == cudaSuccess) e = map_2d(&m.b[t], w[t < terms ? t : 0], N, K, 64);
-    if (e == cudaSuccess) e = map_2d(&m.out[t], dx, M, K, 32);
+  cudaError_t e = map_2d(&m.out[0], dx, M, K, 32);
+  for (int t = 0; t < terms && e == cudaSuccess; ++t) {
+    e = map_2d(&m.a[t], d[t], M, N, 128);
+    if (e == cudaSuccess) e = map_2d(&m.b[t], w[t], N, K, 64);
   }
   if (e != cudaSuccess) return e;
   GemmArgs a{};
   a.rows = M;
   a.cols = K;
-  a.tiles_m = ceil_div(M, kBM * kG);
-  a.tiles_n = ceil_div(K, kBN);
-  a.products = 1;
   a.nk[0] = ceil_div(N, kBK);
   a.nk[1] = terms == 2 ? a.nk[0] : 0;
-  a.parts = plan_parts<kG>(static_cast<long>(a.tiles_m) * a.tiles_n, a.nk[0] + a.nk[1]);
+  deal(&a, plan_dx(M, N, K, terms));
   a.partial = partial;
+  a.out[0] = static_cast<__nv_bfloat16*>(dx);
   a.dev_status = dev_status;
-  e = launch<Use::Dx, kG>(a, m, stream);
-  if (e != cudaSuccess || a.parts == 1) return e;
-  return sum_parts<kG>(a, dx, nullptr, stream);
+  e = launch<Use::Dx>(a, m, after, stream);
+  return e != cudaSuccess ? e : sum_parts(a, stream);
 }
 
 // dw_p [N, K] = d_p^T x for one or two d_p [M, N].
 cudaError_t run_dw(const void* const* d, int products, const void* x, void* const* dw, int M, int N, int K,
-                   float* partial, uint32_t* dev_status, cudaStream_t stream) {
+                   float* partial, uint32_t* dev_status, bool after, cudaStream_t stream) {
   Maps m{};
-  cudaError_t e = cudaSuccess;
-  for (int t = 0; t < 2 && e == cudaSuccess; ++t) {
-    const int p = t < products ? t : 0;
-    e = map_2d(&m.a[t], d[p], M, N, 64);
-    if (e == cudaSuccess) e = map_2d(&m.b[t], x, M, K, 64);
-    if (e == cudaSuccess) e = map_2d(&m.out[t], dw[p], N, K, 32);
+  cudaError_t e = map_2d(&m.b[0], x, M, K, 64);
+  GemmArgs a{};
+  for (int t = 0; t < products && e == cudaSuccess; ++t) {
+    e = map_2d(&m.a[t], d[t], M, N, 64);
+    if (e == cudaSuccess) e = map_2d(&m.out[t], dw[t], N, K, 32);
+    a.out[t] = static_cast<__nv_bfloat16*>(dw[t]);
   }
   if (e != cudaSuccess) return e;
-  GemmArgs a{};
   a.rows = N;
   a.cols = K;
-  a.tiles_m = ceil_div(N, kBM * kG);
-  a.tiles_n = ceil_div(K, kBN);
-  a.products = products;
   a.nk[0] = ceil_div(M, kBK);
-  a.parts = plan_parts<kG>(static_cast<long>(a.tiles_m) * a.tiles_n * products, a.nk[0]);
+  deal(&a, plan_dw(M, N, K, products));
   a.partial = partial;
   a.dev_status = dev_status;
-  e = launch<Use::Dw, kG>(a, m, stream);
-  if (e != cudaSuccess || a.parts == 1) return e;
-  return sum_parts<kG>(a, dw[0], products == 2 ? dw[1] : nullptr, stream);
+  e = launch<Use::Dw>(a, m, after, stream);
+  return e != cudaSuccess ? e : sum_parts(a, stream);
 }
 
 template <Use USE>
 cudaError_t run_glu(const GluArgs& g, const void* dh, void* out0, void* out1, cudaStream_t stream) {
-  Maps m{};
-  cudaError_t e = map_2d(&m.a[0], g.x, g.M, g.K, 128);
-  m.a[1] = m.a[0];
-  if (e == cudaSuccess) e = map_2d(&m.b[0], g.w_gate, g.F, g.K, 128);
-  if (e == cudaSuccess) e = map_2d(&m.b[1], g.w_up, g.F, g.K, 128);
-  if (e == cudaSuccess) e = map_2d(&m.out[0], out0, g.M, g.F, 32);
-  if (e == cudaSuccess) e = map_2d(&m.out[1], out1, g.M, g.F, 32);
-  if (e != cudaSuccess) return e;
   GemmArgs a{};
   a.rows = g.M;
   a.cols = g.F;
-  a.tiles_m = ceil_div(g.M, kBM * kG);
-  a.tiles_n = ceil_div(g.F, 128);
-  a.products = 1;
   a.nk[0] = ceil_div(g.K, kBK);
-  a.parts = 1;
+  deal(&a, plan_glu(g.M, g.F, g.K));
   a.dh = static_cast<const __nv_bfloat16*>(dh);
+  a.out[0] = static_cast<__nv_bfloat16*>(out0);
+  a.out[1] = static_cast<__nv_bfloat16*>(out1);
   a.act = g.act;
   a.dev_status = g.dev_status;
-  return launch<USE, kG>(a, m, stream);
+  Maps m{};
+  cudaError_t e = map_2d(&m.a[0], g.x, g.M, g.K, 128);
+  if (e == cudaSuccess) e = map_2d(&m.b[0], g.w_gate, g.F, g.K, a.width);
+  if (e == cudaSuccess) e = map_2d(&m.b[1], g.w_up, g.F, g.K, a.width);
+  if (e == cudaSuccess && a.width == 128) {  // narrower tiles are stored by the threads
+    e = map_2d(&m.out[0], out0, g.M, g.F, 32);
+    if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.out[1], out1, g.M, g.F, 32);
+    if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.dh, dh, g.M, g.F, 32);
+  }
+  return e != cudaSuccess ? e : launch<USE>(a, m, false, stream);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
-size_t dx_bytes(int M, int N, int K, int terms) {
-  return partial_bytes(static_cast<long>(ceil_div(M, kBM * kG)) * ceil_div(K, kBN), terms * ceil_div(N, kBK));
-}
-size_t dw_bytes(int M, int N, int K, int products) {
-  return partial_bytes(static_cast<long>(ceil_div(N, kBM * kG)) * ceil_div(K, kBN) * products, ceil_div(M, kBK));
-}
 
 }  // namespace
 
 cudaError_t launch_glu_fwd(const GluArgs& g, void* h, cudaStream_t stream) {
   if (g.M <= kGluDecodeRows) return launch_glu_decode(g, h, stream);
-  return run_glu<Use::Glu>(g, nullptr, h, h, stream);
+  return run_glu<Use::Glu>(g, nullptr, h, nullptr, stream);
 }
 
 size_t glu_bwd_ws_bytes(int M, int F, int K, bool dx, bool dw) {
   const size_t act = up256(static_cast<size_t>(M) * F * 2);
-  return 2 * act + std::max(dx ? dx_bytes(M, F, K, 2) : 0, dw ? dw_bytes(M, F, K, 2) : 0);
+  return 2 * act + std::max(dx ? plan_dx(M, F, K, 2).bytes : 0, dw ? plan_dw(M, F, K, 2).bytes : 0);
 }
 
 cudaError_t launch_glu_bwd(const GluArgs& g, const void* dh, void* dx, void* dw_gate, void* dw_up, void* ws,
@@ -612,17 +747,17 @@ cudaError_t launch_glu_bwd(const GluArgs& g, const void* dh, void* dx, void* dw_
   const void* d[2] = {dg, du};
   if (e == cudaSuccess && dx != nullptr) {
     const void* w[2] = {g.w_gate, g.w_up};
-    e = run_dx(d, w, 2, dx, g.M, g.F, g.K, partial, g.dev_status, stream);
+    e = run_dx(d, w, 2, dx, g.M, g.F, g.K, partial, g.dev_status, true, stream);
   }
   if (e == cudaSuccess && dw_gate != nullptr) {
     void* dw[2] = {dw_gate, dw_up};
-    e = run_dw(d, 2, g.x, dw, g.M, g.F, g.K, partial, g.dev_status, stream);
+    e = run_dw(d, 2, g.x, dw, g.M, g.F, g.K, partial, g.dev_status, true, stream);
   }
   return e;
 }
 
 size_t linear_bwd_ws_bytes(int M, int N, int K, bool dx, bool dw) {
-  return std::max(dx ? dx_bytes(M, N, K, 1) : 0, dw ? dw_bytes(M, N, K, 1) : 0);
+  return std::max(dx ? plan_dx(M, N, K, 1).bytes : 0, dw ? plan_dw(M, N, K, 1).bytes : 0);
 }
 
 cudaError_t launch_linear_bwd(const void* dy, const void* x, const void* w, void* dx, void* dw, int M, int N, int K,
@@ -631,9 +766,9 @@ cudaError_t launch_linear_bwd(const void* dy, const void* x, const void* w, void
   const void* d[2] = {dy, dy};
   const void* ww[2] = {w, w};
   void* o[2] = {dw, dw};
-  if (dx != nullptr) e = run_dx(d, ww, 1, dx, M, N, K, static_cast<float*>(ws), dev_status, stream);
+  if (dx != nullptr) e = run_dx(d, ww, 1, dx, M, N, K, static_cast<float*>(ws), dev_status, false, stream);
   if (e == cudaSuccess && dw != nullptr)
-    e = run_dw(d, 1, x, o, M, N, K, static_cast<float*>(ws), dev_status, stream);
+    e = run_dw(d, 1, x, o, M, N, K, static_cast<float*>(ws), dev_status, dx != nullptr, stream);
   return e;
 }
 
