@@ -72,14 +72,14 @@ struct Maps {
 
 // Pairs are numbered 0 .. workers - 1 in the plan; a GPU with fewer resident pairs takes several
 // numbers each. Tile t < direct is pair (t mod workers)'s, whole. The slices of the other tiles, in
-// order, are dealt out `span` to a pair.
+// order and `padded` for each tile (its last ones may be none), are dealt out `span` to a pair.
 struct GemmArgs {
   int rows, cols;            // of an output: M and F (Glu), M and K (Dx), N and K (Dw)
   int tiles_m, tiles_n;      // output tiles of one product
   int tiles;                 // of all products
   int width;                 // output columns of a tile
   int nk[2];                 // slices of the terms of one tile's sum
-  int workers, direct, span;
+  int workers, direct, span, padded;
   float* partial;            // parts of cut sums: [2 pair + piece][CTA][column / 4][row][4] fp32
   const __nv_bfloat16* dh;
   __nv_bfloat16* out[2];
@@ -117,7 +117,7 @@ struct Walk {
     start();
   }
   __device__ __forceinline__ void start() {
-    const long all = static_cast<long>(a.tiles - a.direct) * nk;
+    const long all = static_cast<long>(a.tiles - a.direct) * a.padded;
     next = worker;
     piece = 0;
     at = min(static_cast<long>(worker) * a.span, all);
@@ -134,12 +134,13 @@ struct Walk {
         return true;
       }
       if (at < end) {
-        tile = a.direct + static_cast<int>(at / nk);
-        k0 = static_cast<int>(at % nk);
-        k1 = static_cast<int>(min(static_cast<long>(nk), k0 + (end - at)));
+        const int of = static_cast<int>(at / a.padded);
+        tile = a.direct + of;
+        k0 = static_cast<int>(at - static_cast<long>(of) * a.padded);
+        at = min(end, static_cast<long>(of + 1) * a.padded);
+        k1 = static_cast<int>(min(static_cast<long>(nk), at - static_cast<long>(of) * a.padded));
         slot = 2 * worker + piece;
         ++piece;
-        at += k1 - k0;
         return true;
       }
     }
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kMisc + 4);
   const bool run = (base & 1023u) == 0;  // uniform; the swizzled layout needs 1 KB
 
-  if (warp == 1 && run) tcp::tmem_alloc<2>(tc::smem_u32(s_tmem), 2 * kAccCols);
+  if (warp == 1 && run) tcp::tmem_alloc(tc::smem_u32(s_tmem), 2 * kAccCols);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(bar_full + 8 * s, 1);
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int m0 = (t.m * 2 + rank) * kBM, n0 = t.n * a.width;
         for (int kb = w.k0; kb < w.k1; ++kb, ++g) {
           const int s = static_cast<int>(g % kStages);
-          if (g >= kStages && !tcp::wait(bar_empty + 8 * s, ((g / kStages) - 1) & 1, kWait)) {
+          if (g >= kStages && !tc::mbar_wait(bar_empty + 8 * s, ((g / kStages) - 1) & 1, kWait)) {
             ok = false;
             break;
           }
@@ -250,16 +251,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int term = kb >= a.nk[0] ? 1 : 0, k = (kb - (term ? a.nk[0] : 0)) * kBK;
           if constexpr (kAMn) {
             const CUtensorMap* ta = &maps.a[t.product];
-            tcp::tma_load_2d<2>(st, ta, m0, k, bar);
-            tcp::tma_load_2d<2>(st + kBox, ta, m0 + 64, k, bar);
+            tcp::tma_load_2d(st, ta, m0, k, bar);
+            tcp::tma_load_2d(st + kBox, ta, m0 + 64, k, bar);
           } else {
-            tcp::tma_load_2d<2>(st, &maps.a[term], k, m0, bar);
+            tcp::tma_load_2d(st, &maps.a[term], k, m0, bar);
           }
           if constexpr (kGlu) {
-            tcp::tma_load_2d<2>(st + kA, &maps.b[rank], k, n0, bar);
+            tcp::tma_load_2d(st + kA, &maps.b[rank], k, n0, bar);
           } else {
             for (int q = 0; q < boxes; ++q)
-              tcp::tma_load_2d<2>(st + kA + q * kBox, &maps.b[term], n0 + rank * half + 64 * q, k, bar);
+              tcp::tma_load_2d(st + kA + q * kBox, &maps.b[term], n0 + rank * half + 64 * q, k, bar);
           }
         }
       }
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (Walk w(a, first, stride); ok && w.step(); ++i) {
         const int buf = i & 1;
-        if (i >= 2 && !tcp::wait(bar_acce + 8 * buf, ((i / 2) - 1) & 1, kWait)) {
+        if (i >= 2 && !tc::mbar_wait(bar_acce + 8 * buf, ((i / 2) - 1) & 1, kWait)) {
           ok = false;
           break;
         }
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t acc = tmem + buf * kAccCols;
         for (int kb = w.k0; kb < w.k1; ++kb, ++g) {
           const int s = static_cast<int>(g % kStages);
-          if (!tcp::wait(bar_full + 8 * s, (g / kStages) & 1, kWait)) {
+          if (!tc::mbar_wait(bar_full + 8 * s, (g / kStages) & 1, kWait)) {
             ok = false;
             break;
           }
@@ -292,11 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t db = tc::desc_sw128(st + kA, kBMn ? kBox : 16, 1024);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            tcp::mma_bf16<2>(acc, da + (kAMn ? 128 : 2) * k, db + (kBMn ? 128 : 2) * k, id,
+            tcp::mma_bf16(acc, da + (kAMn ? 128 : 2) * k, db + (kBMn ? 128 : 2) * k, id,
                              (kb > w.k0 || k > 0) ? 1u : 0u);
-          tcp::mma_commit<2>(bar_empty + 8 * s);
+          tcp::mma_commit(bar_empty + 8 * s);
         }
-        if (ok) tcp::mma_commit<2>(bar_accf + 8 * buf);
+        if (ok) tcp::mma_commit(bar_accf + 8 * buf);
       }
       if (!ok) *s_abort = 1;
     }
@@ -311,11 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile_at(w.tile, a.tiles_m, a.tiles_n);
       if (lane == 0) {
         tc::mbar_arrive_expect_tx(my_dh, kStaged);
-        tcp::tma_load_2d<1>(piece[1], &maps.dh, t.n * 128 + 64 * side, (t.m * 2 + rank) * kBM + 32 * quarter, my_dh);
+        tcp::tma_load_2d(piece[1], &maps.dh, t.n * 128 + 64 * side, (t.m * 2 + rank) * kBM + 32 * quarter, my_dh);
       }
     };
     int i = 0;
-    [[maybe_unused]] uint32_t stores = 0;  // buffers in turn
     Walk w(a, first, stride);
     bool more = w.step();
     if (staged_dh && more) fetch_dh(w);
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = w.slot;
       const int m0 = (t.m * 2 + rank) * kBM + 32 * quarter, row = m0 + lane;
       more = w.step();
-      bool ok = tcp::wait(bar_accf + 8 * buf, (i / 2) & 1, kWait);
-      if (staged_dh) ok = ok && tcp::wait(my_dh, i & 1, kWait);
+      bool ok = tc::mbar_wait(bar_accf + 8 * buf, (i / 2) & 1, kWait);
+      if (staged_dh) ok = ok && tc::mbar_wait(my_dh, i & 1, kWait);
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) *s_abort = 1;
         break;
@@ -415,28 +415,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else if (slot < 0) {
-        // groups of 64 columns in turn
+        // groups of 64 columns in turn, at most two a warp; one fence covers both pieces (with one each,
+        // the fences took a third of the epilogue's time)
         const int groups = a.width / 64;
-#pragma unroll 1
-        for (int c = side; c < groups; c += 2) {
-          uint32_t v[4][16];
+        stage_free<0>(lane);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tc::tmem_ld16(acc + 64 * c + 16 * j, v[j]);
-          tc::tmem_wait_ld();
-          if (c + 2 >= groups) release();
-          stage_free<1>(lane);
-          const uint32_t out = piece[stores++ & 1];
+        for (int q = 0; q < 2; ++q) {
+          const int c = side + 2 * q;
+          if (c < groups) {
+            uint32_t v[4][16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float f[16];
-            uint32_t u[8];
-            to_float16(v[j], f);
-            pack16(f, u);
-            stage16(out, lane, j, u);
+            for (int j = 0; j < 4; ++j) tc::tmem_ld16(acc + 64 * c + 16 * j, v[j]);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float f[16];
+              uint32_t u[8];
+              to_float16(v[j], f);
+              pack16(f, u);
+              stage16(piece[q], lane, j, u);
+            }
           }
-          stage_store(out, lane, &maps.out[t.product], t.n * a.width + 64 * c, m0, a);
         }
-        if (side >= groups) release();
+        release();
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int c = side + 2 * q, x = t.n * a.width + 64 * c;
+            if (c < groups && x < a.cols && m0 < a.rows) tcp::tma_store_2d(&maps.out[t.product], piece[q], x, m0);
+          }
+          tc::bulk_commit();
+        }
       } else {
         float4* p = reinterpret_cast<float4*>(a.partial) + (static_cast<long>(slot) * 2 + rank) * (kBM * kAccCols / 4);
         const int groups = a.width / 32;
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tcp::cluster_sync();  // no CTA leaves while the other may still signal it
   if (*s_abort && tid == 0 && a.dev_status != nullptr) atomicOr(a.dev_status, 2u);
   tc::fence_after_sync();
-  if (warp == 1 && run) tcp::tmem_dealloc<2>(tmem, 2 * kAccCols);
+  if (warp == 1 && run) tcp::tmem_dealloc(tmem, 2 * kAccCols);
 }
 
 // Adds the parts of every cut tile in order and rounds once. A CTA takes 128 rows x 16 columns of a tile:
@@ -472,14 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // and the rounded rows are stored through shared memory, 32 bytes each.
 struct SumArgs {
   const float4* partial;
-  int rows, cols, tiles_m, tiles_n, width, direct, span, nk;
+  int rows, cols, tiles_m, tiles_n, width, direct, span, padded;
   __nv_bfloat16* out[2];
 };
 __global__ void __launch_bounds__(256) part_sum_kernel(const SumArgs a) {
   __shared__ uint2 rowbuf[kBM][4 + 1];
   const int cut = blockIdx.x, rank = blockIdx.z, col0 = 16 * blockIdx.y;  // which cut tile, CTA, columns
   const Tile t = tile_at(a.direct + cut, a.tiles_m, a.tiles_n);
-  const long s0 = static_cast<long>(cut) * a.nk, s1 = s0 + a.nk - 1;
+  const long s0 = static_cast<long>(cut) * a.padded, s1 = s0 + a.padded - 1;
   const int w0 = static_cast<int>(s0 / a.span), w1 = static_cast<int>(s1 / a.span);
   const int r = threadIdx.x & (kBM - 1), q = threadIdx.x >> 7;  // row, quads q and q + 2
   const float4* p = a.partial + static_cast<long>(rank) * (kBM * kAccCols / 4) + (col0 / 4 + q) * kBM + r;
@@ -522,7 +533,7 @@ constexpr int kWorkers = 76;       // pairs of a GB300's 152 SMs
 constexpr double kUnit = 6.0;      // slices that a tile costs beside its own: the ends of its pipeline
 constexpr double kSumLaunch = 10;  // slices of the second launch of a cut plan
 struct Plan {
-  int width, tiles_m, tiles_n, tiles, direct, span;
+  int width, tiles_m, tiles_n, tiles, direct, span, padded;
   double cost;
   size_t bytes;
 };
@@ -537,19 +548,26 @@ Plan plan_width(int rows, int cols, int products, int nk, int width, int full, b
   p.tiles_n = ceil_div(cols, width);
   p.tiles = p.tiles_m * p.tiles_n * products;
   p.direct = p.tiles;
+  p.span = p.padded = 1;
   p.cost = static_cast<double>(ceil_div(p.tiles, kWorkers)) * (nk * share + kUnit);
   const int left = p.tiles % kWorkers;
   if (!may_cut || left == 0) return p;
-  // the tiles of the last round, cut: shares of at least four slices; every pair's part is written and
-  // read once, together about 6 KB in a ns
-  const long slices = static_cast<long>(left) * nk;
-  const int span = std::max(4, ceil_div(slices, kWorkers)), pairs = ceil_div(slices, span);
+  // the tiles of the last round, cut: shares of at least four slices. Where a tile takes two pairs or
+  // more, all tiles are cut at the same places: pairs then read the same slices of A and B at the same
+  // time, and they meet in L2. Every pair's part is written and read once, together about 6 KB in a ns.
+  int span = std::max(4, ceil_div(static_cast<long>(left) * nk, kWorkers)), padded = nk;
+  if (2 * left <= kWorkers) {
+    span = std::max(4, ceil_div(nk, kWorkers / left));
+    padded = ceil_div(nk, span) * span;
+  }
+  const int pairs = ceil_div(static_cast<long>(left) * padded, span);
   const double bytes = static_cast<double>(pairs + left) * kPairRows * width * 8;
   const double cost = static_cast<double>(p.tiles / kWorkers) * (nk * share + kUnit) + span * share + 2 * kUnit +
                       kSumLaunch + bytes / 6000.0 / 270.0;
   if (cost < p.cost) {
     p.direct = p.tiles - left;
     p.span = span;
+    p.padded = padded;
     p.cost = cost;
     p.bytes = static_cast<size_t>(2 * pairs) * kPairRows * kAccCols * 4;
   }
@@ -584,6 +602,7 @@ void deal(GemmArgs* a, const Plan& p) {
   a->tiles = p.tiles;
   a->direct = p.direct;
   a->span = p.span;
+  a->padded = p.padded;
   a->workers = kWorkers;
 }
 
@@ -637,7 +656,7 @@ cudaError_t sum_parts(const GemmArgs& a, cudaStream_t stream) {
   s.width = a.width;
   s.direct = a.direct;
   s.span = a.span;
-  s.nk = a.nk[0] + a.nk[1];
+  s.padded = a.padded;
   s.out[0] = a.out[0];
   s.out[1] = a.out[1];
   cudaLaunchConfig_t cfg{};

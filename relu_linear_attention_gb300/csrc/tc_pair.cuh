@@ -1,7 +1,6 @@
-// Inline-PTX helpers for kernels whose tensor-core products run on one CTA (G = 1) or on a CTA pair
-// (G = 2: two SMs, one 256-row product, each CTA holding its half of A, of B and of the accumulator
-// rows). The pair is a cluster of two; its even CTA issues the products. Written from the PTX ISA
-// description of the instructions.
+// Inline-PTX helpers for kernels whose tensor-core products run on a CTA pair (two SMs, one 256-row
+// product, each CTA holding its half of A, of B and of the accumulator rows). The pair is a cluster of
+// two; its even CTA issues the products. Written from the PTX ISA description of the instructions.
 #pragma once
 
 #include <stdint.h>
@@ -27,63 +26,31 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Bounded wait that also acquires what the other CTA of the pair released.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, long long max_cycles) {
-  const long long t0 = clock64();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
-    if (clock64() - t0 > max_cycles) return false;
-  }
-}
-// One arrival on an mbarrier of any CTA of the cluster (an address from map_rank).
+// One arrival on an mbarrier of any CTA of the cluster (an address from map_rank). What it announces here
+// is that TMEM has been read, which tcgen05.fence::before_thread_sync orders before it; a release at
+// cluster scope, which would wait for the thread's shared-memory stores as well, took 40 % of the
+// epilogue's time.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <int G>
+// One warp of each CTA of the pair executes them.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t ncols) {
-  if constexpr (G == 1) {
-    tc::tmem_alloc(dst, ncols);
-    tc::tmem_relinquish();
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
-template <int G>
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  if constexpr (G == 1) {
-    tc::tmem_dealloc(taddr, ncols);
-  } else {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-  }
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// A box of a 2-D tensor map into this CTA's shared memory; its bytes count on `bar`, which may lie
-// in the pair's other CTA where G = 2. x (the innermost coordinate) is a multiple of 8 elements.
-template <int G>
+// A box of a 2-D tensor map into this CTA's shared memory; its bytes count on `bar`, which may lie in
+// the pair's other CTA. x (the innermost coordinate) is a multiple of 8 elements.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
-  if constexpr (G == 1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-        "%3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  }
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
@@ -92,33 +59,22 @@ __device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int
                : "memory");
 }
 
-// D[tmem] (+)= A B; for G = 2 the descriptors' offsets hold in both CTAs.
-template <int G>
+// D[tmem] (+)= A B; the descriptors' offsets hold in both CTAs.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
-  if constexpr (G == 1) {
-    tc::mma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
-  } else {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  }
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
-// One arrival, once every product issued so far by this thread is done, on `bar` here and (G = 2) at
-// the same place in the pair's other CTA.
-template <int G>
+// One arrival, once every product issued so far by this thread is done, on `bar` here and at the same
+// place in the pair's other CTA.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  if constexpr (G == 1) {
-    tc::mma_commit(bar);
-  } else {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-  }
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
 }  // namespace tcp
