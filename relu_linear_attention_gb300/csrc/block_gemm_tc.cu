@@ -79,6 +79,7 @@ struct GemmArgs {
   int tiles;                 // of all products
   int width;                 // output columns of a tile
   int nk[2];                 // slices of the terms of one tile's sum
+  bool solid_a, solid_b;     // whether an MN-major operand's map is one of blocks
   int workers, direct, span, padded;
   float* partial;            // parts of cut sums: [2 pair + piece][CTA][column / 4][row][4] fp32
   const __nv_bfloat16* dh;
@@ -235,6 +236,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // boxes of 64 columns hold an MN-major half, one box of `half` rows a K-major one
       const int boxes = (half + 63) / 64;
       const uint32_t bytes = 2 * (kA + (kBMn ? boxes * kBox : half * kBK * 2));
+      // columns c .. of an MN-major operand: one box of the block map, or a box for every block
+      const auto load_blocks = [&](const CUtensorMap* map, bool solid, int blocks, uint32_t dst, int c, int k,
+                                   uint32_t bar) {
+        if (solid) {
+          tcp::tma_load_3d(dst, map, 0, k, c / 64, bar);
+        } else {
+          for (int q = 0; q < blocks; ++q) tcp::tma_load_2d(dst + q * kBox, map, c + 64 * q, k, bar);
+        }
+      };
       long g = 0;
       bool ok = true;
       for (Walk w(a, first, stride); ok && w.step();) {
@@ -249,19 +259,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) tc::mbar_arrive_expect_tx(bar_full + 8 * s, bytes);
           const uint32_t st = base + s * kStage, bar = full0 + 8 * s;
           const int term = kb >= a.nk[0] ? 1 : 0, k = (kb - (term ? a.nk[0] : 0)) * kBK;
-          if constexpr (kAMn) {
-            const CUtensorMap* ta = &maps.a[t.product];
-            tcp::tma_load_2d(st, ta, m0, k, bar);
-            tcp::tma_load_2d(st + kBox, ta, m0 + 64, k, bar);
-          } else {
+          if constexpr (kAMn)
+            load_blocks(&maps.a[t.product], a.solid_a, 2, st, m0, k, bar);
+          else
             tcp::tma_load_2d(st, &maps.a[term], k, m0, bar);
-          }
-          if constexpr (kGlu) {
+          if constexpr (kGlu)
             tcp::tma_load_2d(st + kA, &maps.b[rank], k, n0, bar);
-          } else {
-            for (int q = 0; q < boxes; ++q)
-              tcp::tma_load_2d(st + kA + q * kBox, &maps.b[term], n0 + rank * half + 64 * q, k, bar);
-          }
+          else
+            load_blocks(&maps.b[term], a.solid_b, boxes, st + kA, n0 + rank * half, k, bar);
         }
       }
       if (!ok) *s_abort = 1;
@@ -528,6 +533,19 @@ cudaError_t map_2d(CUtensorMap* m, const void* p, int rows, int cols, int box_ro
   return encode_bf16_map(m, p, 2, dims, strides, box);
 }
 
+// An MN-major operand: a row-major bf16 [rows, cols] matrix in boxes of 64 rows (the sum's index) and
+// `blocks` blocks of 64 columns, block by block as the tensor core reads them. Where the columns are
+// whole blocks, they are a dimension of their own and one box brings them all: TMA takes about as long
+// to start a box as to copy 4 KB. Otherwise a box is one block, so that what lies past a row's end is
+// zeros and not the next row.
+cudaError_t map_mn(CUtensorMap* m, const void* p, int rows, int cols, int blocks, bool solid) {
+  if (!solid) return map_2d(m, p, rows, cols, 64);
+  const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols / 64)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(cols) * 2, 128};
+  const uint32_t box[3] = {64, 64, static_cast<uint32_t>(blocks)};
+  return encode_bf16_map(m, p, 3, dims, strides, box);
+}
+
 // How a launch is dealt out. The unit of cost is a 64-deep slice of a full tile (512 cycles, 0.27 us).
 constexpr int kWorkers = 76;       // pairs of a GB300's 152 SMs
 constexpr double kUnit = 6.0;      // slices that a tile costs beside its own: the ends of its pipeline
@@ -676,19 +694,20 @@ cudaError_t sum_parts(const GemmArgs& a, cudaStream_t stream) {
 // dx [M, K] = sum over terms of d_t [M, N] w_t [N, K].
 cudaError_t run_dx(const void* const* d, const void* const* w, int terms, void* dx, int M, int N, int K,
                    float* partial, uint32_t* dev_status, bool after, cudaStream_t stream) {
-  Maps m{};
-  cudaError_t e = map_2d(&m.out[0], dx, M, K, 32);
-  for (int t = 0; t < terms && e == cudaSuccess; ++t) {
-    e = map_2d(&m.a[t], d[t], M, N, 128);
-    if (e == cudaSuccess) e = map_2d(&m.b[t], w[t], N, K, 64);
-  }
-  if (e != cudaSuccess) return e;
   GemmArgs a{};
   a.rows = M;
   a.cols = K;
   a.nk[0] = ceil_div(N, kBK);
   a.nk[1] = terms == 2 ? a.nk[0] : 0;
   deal(&a, plan_dx(M, N, K, terms));
+  a.solid_b = K % 64 == 0 && a.width % 128 == 0;
+  Maps m{};
+  cudaError_t e = map_2d(&m.out[0], dx, M, K, 32);
+  for (int t = 0; t < terms && e == cudaSuccess; ++t) {
+    e = map_2d(&m.a[t], d[t], M, N, 128);
+    if (e == cudaSuccess) e = map_mn(&m.b[t], w[t], N, K, a.width / 128, a.solid_b);
+  }
+  if (e != cudaSuccess) return e;
   a.partial = partial;
   a.out[0] = static_cast<__nv_bfloat16*>(dx);
   a.dev_status = dev_status;
@@ -699,19 +718,21 @@ cudaError_t run_dx(const void* const* d, const void* const* w, int terms, void* 
 // dw_p [N, K] = d_p^T x for one or two d_p [M, N].
 cudaError_t run_dw(const void* const* d, int products, const void* x, void* const* dw, int M, int N, int K,
                    float* partial, uint32_t* dev_status, bool after, cudaStream_t stream) {
-  Maps m{};
-  cudaError_t e = map_2d(&m.b[0], x, M, K, 64);
   GemmArgs a{};
-  for (int t = 0; t < products && e == cudaSuccess; ++t) {
-    e = map_2d(&m.a[t], d[t], M, N, 64);
-    if (e == cudaSuccess) e = map_2d(&m.out[t], dw[t], N, K, 32);
-    a.out[t] = static_cast<__nv_bfloat16*>(dw[t]);
-  }
-  if (e != cudaSuccess) return e;
   a.rows = N;
   a.cols = K;
   a.nk[0] = ceil_div(M, kBK);
   deal(&a, plan_dw(M, N, K, products));
+  a.solid_a = N % 64 == 0;
+  a.solid_b = K % 64 == 0 && a.width % 128 == 0;
+  Maps m{};
+  cudaError_t e = map_mn(&m.b[0], x, M, K, a.width / 128, a.solid_b);
+  for (int t = 0; t < products && e == cudaSuccess; ++t) {
+    e = map_mn(&m.a[t], d[t], M, N, 2, a.solid_a);
+    if (e == cudaSuccess) e = map_2d(&m.out[t], dw[t], N, K, 32);
+    a.out[t] = static_cast<__nv_bfloat16*>(dw[t]);
+  }
+  if (e != cudaSuccess) return e;
   a.partial = partial;
   a.dev_status = dev_status;
   e = launch<Use::Dw>(a, m, after, stream);

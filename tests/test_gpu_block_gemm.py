@@ -71,7 +71,8 @@ def test_glu_every_activation(cuda_device, lib, act, M):
 
 @pytest.mark.parametrize("M,N,K", [(1, 8, 8), (1, 1024, 64), (5, 24, 40), (64, 64, 64), (65, 72, 56), (130, 264, 520),
                                    (128, 256, 256), (129, 257 * 8, 264), (1000, 40, 1000), (3000, 256, 136),
-                                   (20000, 64, 72), (4099, 520, 264)])
+                                   (20000, 64, 72), (4099, 520, 264),
+                                   (300, 192, 320), (200, 128, 1088)])
 def test_linear_backward_matches_the_oracle(cuda_device, lib, M, N, K):
     dy, x, w = (_normal(s, 40 + i, cuda_device) for i, s in enumerate(((M, N), (M, K), (N, K))))
     st = _status(cuda_device)
