@@ -373,7 +373,7 @@ def _scratch(need, workspace, like):
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = like.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
     elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -488,7 +488,7 @@ def rapt_glu_fwd(x, w_gate, w_up, *, act="silu", h=None, dev_status=None, stream
     code, lib, sp = _act_code(act), _lib.load(), _status_ptr(dev_status, di)
 
     def call(s):
-        o = x.new_empty(shape) if h is None else h
+        o = torch.empty(shape, dtype=bf16, device=x.device) if h is None else h
         st = lib.rapt_glu_fwd(xp, gp, up, x.numel() // K if K else 0, F, K, code,
                               o.data_ptr() if h is None else hp, sp, s)
         if st:
@@ -552,8 +552,12 @@ def rapt_linear_bwd(dy, x, w, *, need_dx=True, need_dw=True, dx=None, dw=None, d
     lib, sp = _lib.load(), _status_ptr(dev_status, di)
 
     def call(s):
-        ox = dy.new_empty(xs) if dx is None and need_dx else dx
-        ow = dy.new_empty(ws) if dw is None and need_dw else dw
+        ox = dx
+        if dx is None and need_dx:
+            ox = torch.empty(xs, dtype=bf16, device=dy.device)
+        ow = dw
+        if dw is None and need_dw:
+            ow = torch.empty(ws, dtype=bf16, device=dy.device)
         wsp, wsb, _keep = _scratch(lib.rapt_linear_bwd_workspace_size(M, N, K), workspace, dy)
         st = lib.rapt_linear_bwd(yp, xp, wp, M, N, K,
                                  ox.data_ptr() if need_dx and dx is None else dxp,
