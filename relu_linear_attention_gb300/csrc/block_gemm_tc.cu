@@ -1,6 +1,6 @@
 // The matrix products of a block's gated feed-forward and of a projection's gradients on the
 // 5th-generation tensor cores (tcgen05 + TMEM), sm_103a: bf16 operands, fp32 accumulation, one
-// rounding of every result to bf16. D[m, n] = sum_k A[m, k] B[n, k], four uses of one kernel:
+// rounding of every result to bf16. D[m, n] = sum_k A[m, k] B[n, k], in four forms:
 //
 //   Glu      A = x, B = the rows of w_gate and w_up: 128 columns of g = x w_gate^T and the same 128 of
 //            u = x w_up^T are the two halves of one 256-column accumulator, so act(g) u is formed in
@@ -10,6 +10,9 @@
 //   Dx       D = sum over one or two pairs (A, W): dy W, or dg w_gate + du w_up. W [n, k] is read as it
 //            lies: its rows are the sum's index, so it is an MN-major operand.
 //   Dw       D = dy^T x, one or two products over the tokens that share x: both operands MN-major.
+//
+// Dx and Dw are the two problems of one launch: its pairs go from the one to the other without a
+// pause (1531 x 1032 x 2744: XX us a launch each, YY together).
 //
 // A pair of CTAs on two SMs forms one tile of 256 rows x up to 256 accumulator columns (cta_group::2):
 // each CTA loads its 128 rows of A and its half of B, and holds its 128 rows of the accumulator; an SM
@@ -32,6 +35,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "kernels.h"
@@ -41,7 +45,7 @@
 namespace rapt {
 namespace {
 
-enum class Use { Glu, GluGrad, Dx, Dw };
+enum class Use { Glu, GluGrad, Grads };  // Grads: problem 0 is Dx, problem 1 Dw
 
 constexpr int kBM = 128, kBK = 64;         // rows of a CTA, depth of a slice
 constexpr int kPairRows = 2 * kBM;         // rows of a tile
@@ -62,28 +66,35 @@ constexpr uint32_t kSmem = kMisc + 16;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kRaster = 8;  // tile rows taken together
 
-// The tensor maps of one launch: A and B of up to two terms or products, outputs, dh.
+// The tensor maps of one launch: A and B of up to two terms or products of each problem, outputs, dh.
 struct Maps {
-  CUtensorMap a[2];
-  CUtensorMap b[2];
-  CUtensorMap out[2];
+  CUtensorMap a[2][2];
+  CUtensorMap b[2][2];
+  CUtensorMap out[2][2];
   CUtensorMap dh;
 };
 
-// Pairs are numbered 0 .. workers - 1 in the plan; a GPU with fewer resident pairs takes several
-// numbers each. Tile t < direct is pair (t mod workers)'s, whole. The slices of the other tiles, in
-// order and `padded` for each tile (its last ones may be none), are dealt out `span` to a pair.
-struct GemmArgs {
-  int rows, cols;            // of an output: M and F (Glu), M and K (Dx), N and K (Dw)
-  int tiles_m, tiles_n;      // output tiles of one product
-  int tiles;                 // of all products
-  int width;                 // output columns of a tile
-  int nk[2];                 // slices of the terms of one tile's sum
-  bool solid_a, solid_b;     // whether an MN-major operand's map is one of blocks
-  int workers, direct, span, padded;
-  float* partial;            // parts of cut sums: [2 pair + piece][CTA][column / 4][row][4] fp32
-  const __nv_bfloat16* dh;
+// One matrix product, or two of the same shape. Pairs are numbered 0 .. workers - 1 in the plan; a GPU
+// with fewer resident pairs takes several numbers each. Tile t < direct is pair (t mod workers)'s, whole.
+// The slices of the other tiles, in order and `padded` for each tile (its last ones may be none), are
+// dealt out `span` to a pair. The second problem's pairs are numbered from pair `turn`, where the
+// first's last round ended.
+struct Problem {
+  int rows, cols;        // of an output: M and F (Glu), M and K (Dx), N and K (Dw)
+  int tiles_m, tiles_n;  // output tiles of one product
+  int tiles;             // of all products
+  int width;             // output columns of a tile
+  int nk0, nk;           // slices of a tile's sum: of its first term, in all
+  int direct, span, padded, turn;
+  int slot0;             // first of its parts' places in the workspace
+  bool solid_a, solid_b;  // whether an MN-major operand's map is one of blocks
   __nv_bfloat16* out[2];
+};
+struct GemmArgs {
+  Problem p[2];
+  int workers;
+  float* partial;  // parts of cut sums: [slot0 + 2 pair + piece][CTA][column / 4][row][4] fp32
+  const __nv_bfloat16* dh;
   Act act;
   uint32_t* dev_status;
 };
@@ -105,45 +116,56 @@ __device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n) {
   return r;
 }
 
-// Walks the units of a pair: whole tiles, then pieces of cut tiles.
+// Walks the units of a pair: of each problem its whole tiles, then its pieces of cut tiles.
 struct Walk {
   const GemmArgs& a;
-  const int stride, nk;
-  int worker, next, piece;
+  const int stride;
+  int worker, q, next, piece, number;
   long at, end;  // slices of the cut tiles
   // the unit
   int tile, k0, k1, slot;  // slot: -1 whole, else where its part goes
-  __device__ __forceinline__ Walk(const GemmArgs& a_, int first, int stride_)
-      : a(a_), stride(stride_), nk(a_.nk[0] + a_.nk[1]), worker(first), next(first), piece(0) {
-    start();
+  __device__ __forceinline__ Walk(const GemmArgs& a_, int first, int stride_) : a(a_), stride(stride_), worker(first), q(0) {
+    open();
   }
-  __device__ __forceinline__ void start() {
-    const long all = static_cast<long>(a.tiles - a.direct) * a.padded;
-    next = worker;
+  __device__ __forceinline__ const Problem& problem() const { return a.p[q]; }
+  __device__ __forceinline__ void open() {
+    const Problem& p = a.p[q];
+    number = worker - p.turn + (worker < p.turn ? a.workers : 0);
+    const long all = static_cast<long>(p.tiles - p.direct) * p.padded;
+    next = number;
     piece = 0;
-    at = min(static_cast<long>(worker) * a.span, all);
-    end = min(at + a.span, all);
+    at = min(static_cast<long>(number) * p.span, all);
+    end = min(at + p.span, all);
   }
   __device__ __forceinline__ bool step() {
-    for (; worker < a.workers; worker += stride, start()) {
-      if (next < a.direct) {
+    while (worker < a.workers) {
+      const Problem& p = a.p[q];
+      if (next < p.direct) {
         tile = next;
         k0 = 0;
-        k1 = nk;
+        k1 = p.nk;
         slot = -1;
         next += a.workers;
         return true;
       }
       if (at < end) {
-        const int of = static_cast<int>(at / a.padded);
-        tile = a.direct + of;
-        k0 = static_cast<int>(at - static_cast<long>(of) * a.padded);
-        at = min(end, static_cast<long>(of + 1) * a.padded);
-        k1 = static_cast<int>(min(static_cast<long>(nk), at - static_cast<long>(of) * a.padded));
-        slot = 2 * worker + piece;
+        const int of = static_cast<int>(at / p.padded);
+        tile = p.direct + of;
+        k0 = static_cast<int>(at - static_cast<long>(of) * p.padded);
+        at = min(end, static_cast<long>(of + 1) * p.padded);
+        k1 = static_cast<int>(min(static_cast<long>(p.nk), at - static_cast<long>(of) * p.padded));
+        slot = p.slot0 + 2 * number + piece;
         ++piece;
         return true;
       }
+      if (q == 0) {
+        q = 1;
+      } else {
+        q = 0;
+        worker += stride;
+        if (worker >= a.workers) return false;
+      }
+      open();
     }
     return false;
   }
@@ -173,32 +195,30 @@ __device__ __forceinline__ void stage_free(int lane) {
 }
 // Stores the staged piece at column x, row y; TMA clips what lies past an edge of the [rows, cols] output.
 __device__ __forceinline__ void stage_store(uint32_t piece, int lane, const CUtensorMap* map, int x, int y,
-                                            const GemmArgs& a) {
+                                            const Problem& p) {
   tc::fence_async_smem();
   __syncwarp();
   if (lane == 0) {
-    if (x < a.cols && y < a.rows) tcp::tma_store_2d(map, piece, x, y);
+    if (x < p.cols && y < p.rows) tcp::tma_store_2d(map, piece, x, y);
     tc::bulk_commit();
   }
 }
 // 16 bf16 straight to columns col .. col + 15 of a row (cols is a multiple of eight).
-__device__ __forceinline__ void put16(__nv_bfloat16* out, int row, int col, const uint32_t (&u)[8], const GemmArgs& a) {
+__device__ __forceinline__ void put16(__nv_bfloat16* out, int row, int col, const uint32_t (&u)[8], const Problem& p) {
 #pragma unroll
   for (int q = 0; q < 2; ++q)
-    if (row < a.rows && col + 8 * q < a.cols)
-      *reinterpret_cast<uint4*>(out + static_cast<long>(row) * a.cols + col + 8 * q) =
+    if (row < p.rows && col + 8 * q < p.cols)
+      *reinterpret_cast<uint4*>(out + static_cast<long>(row) * p.cols + col + 8 * q) =
           make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
 }
 
 template <Use USE>
 __global__ void __launch_bounds__(kThreads, 1)
-    block_gemm_kernel(const GemmArgs a, const __grid_constant__ Maps maps) {
+    block_gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ Maps maps) {
   constexpr bool kGlu = USE == Use::Glu || USE == Use::GluGrad;
-  constexpr bool kAMn = USE == Use::Dw, kBMn = !kGlu;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(tcp::cluster_rank());
   const int first = blockIdx.x / 2, stride = gridDim.x / 2;
-  const int half = kGlu ? a.width : a.width / 2;  // columns of B that a CTA holds
 
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = tc::smem_u32(smem);
@@ -233,76 +253,104 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0 && run) {  // TMA producer: this CTA's rows of A and its columns of B
       const uint32_t full0 = tcp::map_rank(bar_full, 0);
-      // boxes of 64 columns hold an MN-major half, one box of `half` rows a K-major one
-      const int boxes = (half + 63) / 64;
-      const uint32_t bytes = 2 * (kA + (kBMn ? boxes * kBox : half * kBK * 2));
-      // columns c .. of an MN-major operand: one box of the block map, or a box for every block
-      const auto load_blocks = [&](const CUtensorMap* map, bool solid, int blocks, uint32_t dst, int c, int k,
-                                   uint32_t bar) {
-        if (solid) {
-          tcp::tma_load_3d(dst, map, 0, k, c / 64, bar);
-        } else {
-          for (int q = 0; q < blocks; ++q) tcp::tma_load_2d(dst + q * kBox, map, c + 64 * q, k, bar);
+      tcp::Ring<kStages> ring;
+      bool ok = true;
+      // one slice after another into the ring: load(stage, full barrier, slice) issues its copies
+      const auto stream = [&](int k0, int k1, uint32_t bytes, const auto& load) {
+        for (int kb = k0; kb < k1; ++kb, ring.step()) {
+          if (ring.round > 0 && !tcp::wait(bar_empty + 8 * ring.s, (ring.round - 1) & 1, kWait)) {
+            ok = false;
+            return;
+          }
+          if (rank == 0) tc::mbar_arrive_expect_tx(bar_full + 8 * ring.s, bytes);
+          load(base + ring.s * kStage, full0 + 8 * ring.s, kb);
         }
       };
-      long g = 0;
-      bool ok = true;
       for (Walk w(a, first, stride); ok && w.step();) {
-        const Tile t = tile_at(w.tile, a.tiles_m, a.tiles_n);
-        const int m0 = (t.m * 2 + rank) * kBM, n0 = t.n * a.width;
-        for (int kb = w.k0; kb < w.k1; ++kb, ++g) {
-          const int s = static_cast<int>(g % kStages);
-          if (g >= kStages && !tc::mbar_wait(bar_empty + 8 * s, ((g / kStages) - 1) & 1, kWait)) {
-            ok = false;
-            break;
+        const Problem& p = w.problem();
+        const Tile t = tile_at(w.tile, p.tiles_m, p.tiles_n);
+        const int m0 = (t.m * 2 + rank) * kBM, n0 = t.n * p.width;
+        if constexpr (kGlu) {
+          const CUtensorMap* mb = &maps.b[0][rank];
+          stream(w.k0, w.k1, 2 * (kA + p.width * kBK * 2), [&](uint32_t st, uint32_t bar, int kb) {
+            tcp::tma_load_2d(st, &maps.a[0][0], kb * kBK, m0, bar);
+            tcp::tma_load_2d(st + kA, mb, kb * kBK, n0, bar);
+          });
+        } else {
+          const int half = p.width / 2, blocks = (half + 63) / 64, nb = n0 + rank * half;
+          const uint32_t bytes = 2 * (kA + blocks * kBox);
+          const bool solid_a = p.solid_a, solid_b = p.solid_b;
+          // columns c .. of an MN-major operand: one box of the block map, or a box for every block
+          const auto load_mn = [&](const CUtensorMap* map, bool solid, int n, uint32_t dst, int c, int k, uint32_t bar) {
+            if (solid) {
+              tcp::tma_load_3d(dst, map, 0, k, c / 64, bar);
+            } else {
+              tcp::tma_load_2d(dst, map, c, k, bar);
+              if (n > 1) tcp::tma_load_2d(dst + kBox, map, c + 64, k, bar);
+            }
+          };
+          if (w.q == 0) {
+            const int nk0 = p.nk0;
+            for (int term = 0; term < 2 && ok; ++term) {
+              const CUtensorMap *ma = &maps.a[0][term], *mb = &maps.b[0][term];
+              const int skip = term * nk0;  // slices of the terms before
+              stream(max(w.k0, skip), min(w.k1, skip + nk0), bytes, [&](uint32_t st, uint32_t bar, int kb) {
+                const int k = (kb - skip) * kBK;
+                tcp::tma_load_2d(st, ma, k, m0, bar);
+                load_mn(mb, solid_b, blocks, st + kA, nb, k, bar);
+              });
+            }
+          } else {
+            const CUtensorMap *ma = &maps.a[1][t.product], *mb = &maps.b[1][0];
+            stream(w.k0, w.k1, bytes, [&](uint32_t st, uint32_t bar, int kb) {
+              load_mn(ma, solid_a, 2, st, m0, kb * kBK, bar);
+              load_mn(mb, solid_b, blocks, st + kA, nb, kb * kBK, bar);
+            });
           }
-          if (rank == 0) tc::mbar_arrive_expect_tx(bar_full + 8 * s, bytes);
-          const uint32_t st = base + s * kStage, bar = full0 + 8 * s;
-          const int term = kb >= a.nk[0] ? 1 : 0, k = (kb - (term ? a.nk[0] : 0)) * kBK;
-          if constexpr (kAMn)
-            load_blocks(&maps.a[t.product], a.solid_a, 2, st, m0, k, bar);
-          else
-            tcp::tma_load_2d(st, &maps.a[term], k, m0, bar);
-          if constexpr (kGlu)
-            tcp::tma_load_2d(st + kA, &maps.b[rank], k, n0, bar);
-          else
-            load_blocks(&maps.b[term], a.solid_b, boxes, st + kA, n0 + rank * half, k, bar);
         }
       }
       if (!ok) *s_abort = 1;
     }
   } else if (warp == 1) {
     if (lane == 0 && run && rank == 0) {  // issuer of the products
-      const uint32_t id = tc::idesc_bf16(kPairRows, 2 * half, kAMn, kBMn);
-      long g = 0;
-      int i = 0;
+      tcp::Ring<kStages> ring;
+      tcp::Ring<2> accs;
       bool ok = true;
-      for (Walk w(a, first, stride); ok && w.step(); ++i) {
-        const int buf = i & 1;
-        if (i >= 2 && !tc::mbar_wait(bar_acce + 8 * buf, ((i / 2) - 1) & 1, kWait)) {
+      // the slices of one unit; A_MN: A is MN-major (Dw)
+      const auto multiply = [&](int slices, uint32_t acc, uint32_t id, auto a_mn) {
+        constexpr bool kAMn = decltype(a_mn)::value, kBMn = !kGlu;
+        // 16 k are 32 bytes of a K-major row, 16 rows (2 KB) of an MN-major block
+        constexpr int kStepA = kAMn ? 128 : 2, kStepB = kBMn ? 128 : 2;
+        const uint64_t da0 = tc::desc_sw128(base, kAMn ? kBox : 16, 1024);
+        const uint64_t db0 = tc::desc_sw128(base + kA, kBMn ? kBox : 16, 1024);
+        for (int q = 0; q < slices; ++q, ring.step()) {
+          if (!tcp::wait(bar_full + 8 * ring.s, ring.round & 1, kWait)) {
+            ok = false;
+            return;
+          }
+          tc::fence_after_sync();
+          const uint64_t da = da0 + ring.s * (kStage / 16), db = db0 + ring.s * (kStage / 16);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k)
+            tcp::mma_bf16(acc, da + kStepA * k, db + kStepB * k, id, (q > 0 || k > 0) ? 1u : 0u);
+          tcp::mma_commit(bar_empty + 8 * ring.s);
+        }
+      };
+      for (Walk w(a, first, stride); ok && w.step(); accs.step()) {
+        const int width = w.problem().width;
+        const bool a_mn = !kGlu && w.q == 1;
+        const uint32_t id = tc::idesc_bf16(kPairRows, kGlu ? 2 * width : width, a_mn, !kGlu);
+        if (accs.round > 0 && !tcp::wait(bar_acce + 8 * accs.s, (accs.round - 1) & 1, kWait)) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
-        const uint32_t acc = tmem + buf * kAccCols;
-        for (int kb = w.k0; kb < w.k1; ++kb, ++g) {
-          const int s = static_cast<int>(g % kStages);
-          if (!tc::mbar_wait(bar_full + 8 * s, (g / kStages) & 1, kWait)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-          const uint32_t st = base + s * kStage;
-          // 16 k are 32 bytes of a K-major row, 16 rows (2 KB) of an MN-major block
-          const uint64_t da = tc::desc_sw128(st, kAMn ? kBox : 16, 1024);
-          const uint64_t db = tc::desc_sw128(st + kA, kBMn ? kBox : 16, 1024);
-#pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            tcp::mma_bf16(acc, da + (kAMn ? 128 : 2) * k, db + (kBMn ? 128 : 2) * k, id,
-                             (kb > w.k0 || k > 0) ? 1u : 0u);
-          tcp::mma_commit(bar_empty + 8 * s);
-        }
-        if (ok) tcp::mma_commit(bar_accf + 8 * buf);
+        const uint32_t acc = tmem + accs.s * kAccCols;
+        if (a_mn)
+          multiply(w.k1 - w.k0, acc, id, std::true_type{});
+        else
+          multiply(w.k1 - w.k0, acc, id, std::false_type{});
+        if (ok) tcp::mma_commit(bar_accf + 8 * accs.s);
       }
       if (!ok) *s_abort = 1;
     }
@@ -311,10 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t piece[2] = {base + kOut + 2 * e * kStaged, base + kOut + (2 * e + 1) * kStaged};
     const uint32_t my_dh = bar_dh + 8 * e;
-    const bool staged_dh = USE == Use::GluGrad && a.width == 128;
+    const bool staged_dh = USE == Use::GluGrad && a.p[0].width == 128;
     // GluGrad: dh of the unit after `w` into the second buffer, which the last store has read
     const auto fetch_dh = [&](const Walk& w) {
-      const Tile t = tile_at(w.tile, a.tiles_m, a.tiles_n);
+      const Tile t = tile_at(w.tile, a.p[0].tiles_m, a.p[0].tiles_n);
       if (lane == 0) {
         tc::mbar_arrive_expect_tx(my_dh, kStaged);
         tcp::tma_load_2d(piece[1], &maps.dh, t.n * 128 + 64 * side, (t.m * 2 + rank) * kBM + 32 * quarter, my_dh);
@@ -326,12 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (staged_dh && more) fetch_dh(w);
     for (; more; ++i) {
       const int buf = i & 1;
-      const Tile t = tile_at(w.tile, a.tiles_m, a.tiles_n);
+      const Problem& p = w.problem();
+      const Tile t = tile_at(w.tile, p.tiles_m, p.tiles_n);
       const int slot = w.slot;
+      [[maybe_unused]] const CUtensorMap* outs = maps.out[w.q];
       const int m0 = (t.m * 2 + rank) * kBM + 32 * quarter, row = m0 + lane;
       more = w.step();
-      bool ok = tc::mbar_wait(bar_accf + 8 * buf, (i / 2) & 1, kWait);
-      if (staged_dh) ok = ok && tc::mbar_wait(my_dh, i & 1, kWait);
+      bool ok = tcp::wait(bar_accf + 8 * buf, (i / 2) & 1, kWait);
+      if (staged_dh) ok = ok && tcp::wait(my_dh, i & 1, kWait);
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) *s_abort = 1;
         break;
@@ -346,20 +396,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if constexpr (kGlu) {
         // this warp's columns: every other group of 64 of a full tile, of 16 of a narrow one
-        const int groups = a.width / 16, step = a.width == 128 ? 1 : 2, j0 = a.width == 128 ? 4 * side : side;
-        const int j1 = a.width == 128 ? j0 + 4 : groups;
+        const int groups = p.width / 16, step = p.width == 128 ? 1 : 2, j0 = p.width == 128 ? 4 * side : side;
+        const int j1 = p.width == 128 ? j0 + 4 : groups;
         uint32_t keep[4][8];  // full tiles: du as bf16, staged once dh has been read
         if (staged_dh) stage_free<0>(lane);
-        if (USE == Use::Glu && a.width == 128) stage_free<1>(lane);
+        if (USE == Use::Glu && p.width == 128) stage_free<1>(lane);
         const uint32_t out = USE == Use::Glu ? piece[i & 1] : piece[0];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int j = j0 + q * step;
           if (j < j1) {
-            const int col = t.n * a.width + 16 * j;
+            const int col = t.n * p.width + 16 * j;
             uint32_t ug[16], uu[16];
             tc::tmem_ld16(acc + 16 * j, ug);
-            tc::tmem_ld16(acc + a.width + 16 * j, uu);
+            tc::tmem_ld16(acc + p.width + 16 * j, uu);
             float d[16];
             if constexpr (USE == Use::GluGrad) {
 #pragma unroll
@@ -370,9 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                                : "r"(piece[1] + tc::sw128(lane, 2 * q + x))
                                : "memory");
-                else if (row < a.rows && col + 8 * x < a.cols)
+                else if (row < p.rows && col + 8 * x < p.cols)
                   *reinterpret_cast<uint4*>(v) =
-                      *reinterpret_cast<const uint4*>(a.dh + static_cast<long>(row) * a.cols + col + 8 * x);
+                      *reinterpret_cast<const uint4*>(a.dh + static_cast<long>(row) * p.cols + col + 8 * x);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                   d[8 * x + 2 * y] = __uint_as_float(v[y] << 16);
@@ -396,23 +446,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 d[x] *= av[x];          // du
               }
               pack16(d, keep[q]);
-              if (a.width != 128) put16(a.out[1], row, col, keep[q], a);
+              if (p.width != 128) put16(p.out[1], row, col, keep[q], p);
             }
             pack16(up, u);
-            if (a.width == 128)
+            if (p.width == 128)
               stage16(out, lane, q, u);
             else
-              put16(a.out[0], row, col, u, a);
+              put16(p.out[0], row, col, u, p);
           }
         }
         release();
-        if (a.width == 128) {
+        if (p.width == 128) {
           const int col = t.n * 128 + 64 * side;
-          stage_store(out, lane, &maps.out[0], col, m0, a);
+          stage_store(out, lane, &outs[0], col, m0, p);
           if constexpr (USE == Use::GluGrad) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) stage16(piece[1], lane, q, keep[q]);
-            stage_store(piece[1], lane, &maps.out[1], col, m0, a);
+            stage_store(piece[1], lane, &outs[1], col, m0, p);
             if (more) {
               stage_free<0>(lane);
               fetch_dh(w);
@@ -422,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (slot < 0) {
         // groups of 64 columns in turn, at most two a warp; one fence covers both pieces (with one each,
         // the fences took a third of the epilogue's time)
-        const int groups = a.width / 64;
+        const int groups = p.width / 64;
         stage_free<0>(lane);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -448,14 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const int c = side + 2 * q, x = t.n * a.width + 64 * c;
-            if (c < groups && x < a.cols && m0 < a.rows) tcp::tma_store_2d(&maps.out[t.product], piece[q], x, m0);
+            const int c = side + 2 * q, x = t.n * p.width + 64 * c;
+            if (c < groups && x < p.cols && m0 < p.rows) tcp::tma_store_2d(&outs[t.product], piece[q], x, m0);
           }
           tc::bulk_commit();
         }
       } else {
-        float4* p = reinterpret_cast<float4*>(a.partial) + (static_cast<long>(slot) * 2 + rank) * (kBM * kAccCols / 4);
-        const int groups = a.width / 32;
+        float4* part = reinterpret_cast<float4*>(a.partial) + (static_cast<long>(slot) * 2 + rank) * (kBM * kAccCols / 4);
+        const int groups = p.width / 32;
 #pragma unroll 1
         for (int c = side; c < groups; c += 2) {
           uint32_t v[2][16];
@@ -466,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              p[(8 * c + 4 * j + q) * kBM + 32 * quarter + lane] =
+              part[(8 * c + 4 * j + q) * kBM + 32 * quarter + lane] =
                   make_float4(__uint_as_float(v[j][4 * q]), __uint_as_float(v[j][4 * q + 1]),
                               __uint_as_float(v[j][4 * q + 2]), __uint_as_float(v[j][4 * q + 3]));
         }
@@ -486,28 +536,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Adds the parts of every cut tile in order and rounds once. A CTA takes 128 rows x 16 columns of a tile:
 // a thread adds two quads of columns of a row (parts are stored for reading 32 rows of a quad at once),
 // and the rounded rows are stored through shared memory, 32 bytes each.
-struct SumArgs {
-  const float4* partial;
-  int rows, cols, tiles_m, tiles_n, width, direct, span, padded;
-  __nv_bfloat16* out[2];
-};
-__global__ void __launch_bounds__(256) part_sum_kernel(const SumArgs a) {
+__global__ void __launch_bounds__(256) part_sum_kernel(const __grid_constant__ GemmArgs a, int cut0) {
   __shared__ uint2 rowbuf[kBM][4 + 1];
-  const int cut = blockIdx.x, rank = blockIdx.z, col0 = 16 * blockIdx.y;  // which cut tile, CTA, columns
-  const Tile t = tile_at(a.direct + cut, a.tiles_m, a.tiles_n);
-  const long s0 = static_cast<long>(cut) * a.padded, s1 = s0 + a.padded - 1;
-  const int w0 = static_cast<int>(s0 / a.span), w1 = static_cast<int>(s1 / a.span);
+  const int q_ = static_cast<int>(blockIdx.x) >= cut0 ? 1 : 0;  // problem
+  const Problem& p = a.p[q_];
+  const int cut = blockIdx.x - (q_ ? cut0 : 0), rank = blockIdx.z, col0 = 16 * blockIdx.y;  // tile, CTA, columns
+  if (col0 >= p.width) return;
+  const Tile t = tile_at(p.direct + cut, p.tiles_m, p.tiles_n);
+  const long s0 = static_cast<long>(cut) * p.padded, s1 = s0 + p.padded - 1;
+  const int w0 = static_cast<int>(s0 / p.span), w1 = static_cast<int>(s1 / p.span);
   const int r = threadIdx.x & (kBM - 1), q = threadIdx.x >> 7;  // row, quads q and q + 2
-  const float4* p = a.partial + static_cast<long>(rank) * (kBM * kAccCols / 4) + (col0 / 4 + q) * kBM + r;
+  const float4* from = reinterpret_cast<const float4*>(a.partial) +
+                       (static_cast<long>(p.slot0) * 2 + rank) * (kBM * kAccCols / 4) + (col0 / 4 + q) * kBM + r;
   float4 s[2] = {};
   tc::grid_dep_wait();
 #pragma unroll 4
   for (int w = w0; w <= w1; ++w) {
     // the first pair's piece is its second one where its share began before this tile
-    const int slot = 2 * w + (static_cast<long>(w) * a.span < s0 ? 1 : 0);
+    const int slot = 2 * w + (static_cast<long>(w) * p.span < s0 ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 v = p[static_cast<long>(slot) * 2 * (kBM * kAccCols / 4) + 2 * i * kBM];
+      const float4 v = from[static_cast<long>(slot) * 2 * (kBM * kAccCols / 4) + 2 * i * kBM];
       s[i].x += v.x; s[i].y += v.y; s[i].z += v.z; s[i].w += v.w;
     }
   }
@@ -516,10 +565,10 @@ __global__ void __launch_bounds__(256) part_sum_kernel(const SumArgs a) {
     rowbuf[r][q + 2 * i] = make_uint2(tc::pack_bf16x2(s[i].x, s[i].y), tc::pack_bf16x2(s[i].z, s[i].w));
   __syncthreads();
   const int r2 = threadIdx.x >> 1, q2 = threadIdx.x & 1;
-  const int row = (t.m * 2 + rank) * kBM + r2, col = t.n * a.width + col0 + 8 * q2;
-  if (row >= a.rows || col >= a.cols) return;
+  const int row = (t.m * 2 + rank) * kBM + r2, col = t.n * p.width + col0 + 8 * q2;
+  if (row >= p.rows || col >= p.cols) return;
   const uint2 lo = rowbuf[r2][2 * q2], hi = rowbuf[r2][2 * q2 + 1];
-  *reinterpret_cast<uint4*>(a.out[t.product] + static_cast<long>(row) * a.cols + col) =
+  *reinterpret_cast<uint4*>((t.product ? p.out[1] : p.out[0]) + static_cast<long>(row) * p.cols + col) =
       make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
@@ -548,12 +597,12 @@ cudaError_t map_mn(CUtensorMap* m, const void* p, int rows, int cols, int blocks
 
 // How a launch is dealt out. The unit of cost is a 64-deep slice of a full tile (512 cycles, 0.27 us).
 constexpr int kWorkers = 76;       // pairs of a GB300's 152 SMs
+constexpr size_t kSlotBytes = static_cast<size_t>(kPairRows) * kAccCols * 4;
 constexpr double kUnit = 6.0;      // slices that a tile costs beside its own: the ends of its pipeline
 constexpr double kSumLaunch = 10;  // slices of the second launch of a cut plan
 struct Plan {
-  int width, tiles_m, tiles_n, tiles, direct, span, padded;
+  int width, tiles_m, tiles_n, tiles, direct, span, padded, slots;
   double cost;
-  size_t bytes;
 };
 // Tiles of `width` output columns (`full` at most). A slice of a narrow tile costs more than its share of
 // the products: it still loads the 256 rows of A (half of a full slice's bytes), and the loads of all
@@ -587,7 +636,7 @@ Plan plan_width(int rows, int cols, int products, int nk, int width, int full, b
     p.span = span;
     p.padded = padded;
     p.cost = cost;
-    p.bytes = static_cast<size_t>(2 * pairs) * kPairRows * kAccCols * 4;
+    p.slots = 2 * pairs;
   }
   return p;
 }
@@ -613,18 +662,34 @@ Plan plan_sum(int rows, int cols, int products, int nk) {
 Plan plan_dx(int M, int N, int K, int terms) { return plan_sum(M, K, 1, terms * ceil_div(N, kBK)); }
 Plan plan_dw(int M, int N, int K, int products) { return plan_sum(N, K, products, ceil_div(M, kBK)); }
 
-void deal(GemmArgs* a, const Plan& p) {
-  a->width = p.width;
-  a->tiles_m = p.tiles_m;
-  a->tiles_n = p.tiles_n;
-  a->tiles = p.tiles;
-  a->direct = p.direct;
-  a->span = p.span;
-  a->padded = p.padded;
-  a->workers = kWorkers;
+// A problem of rows x cols outputs; `turn`: the pair that its numbers begin with.
+Problem deal(const Plan& p, int rows, int cols, int nk0, int terms, int turn) {
+  Problem q{};
+  q.rows = rows;
+  q.cols = cols;
+  q.tiles_m = p.tiles_m;
+  q.tiles_n = p.tiles_n;
+  q.tiles = p.tiles;
+  q.width = p.width;
+  q.nk0 = nk0;
+  q.nk = nk0 * terms;
+  q.direct = p.direct;
+  q.span = p.span;
+  q.padded = p.padded;
+  q.turn = turn;
+  return q;
+}
+Problem no_problem() {
+  Problem q{};
+  q.span = q.padded = q.width = 1;
+  return q;
+}
+// Pairs that a problem's last round keeps busy.
+int last_round(const Plan& p) {
+  if (p.direct == p.tiles) return p.tiles % kWorkers;
+  return ceil_div(static_cast<long>(p.tiles - p.direct) * p.padded, p.span) % kWorkers;
 }
 
-// `after`: the launch follows another one of the same call, and may be made ready before that one ends.
 template <Use USE>
 cudaError_t launch(const GemmArgs& a, const Maps& maps, bool after, cudaStream_t stream) {
   int dev = 0, sms = 0;
@@ -655,7 +720,8 @@ cudaError_t launch(const GemmArgs& a, const Maps& maps, bool after, cudaStream_t
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     if (dev < 64) resident[dev].store(pairs, std::memory_order_relaxed);
   }
-  const int most = a.direct < a.tiles ? a.workers : std::min(a.workers, a.direct);
+  const bool cut = a.p[0].direct < a.p[0].tiles || a.p[1].direct < a.p[1].tiles;
+  const int most = cut || a.p[1].tiles > 0 ? a.workers : std::min(a.workers, a.p[0].tiles);
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, most)));
   cfg.numAttrs = after ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a, maps);
@@ -664,21 +730,10 @@ cudaError_t launch(const GemmArgs& a, const Maps& maps, bool after, cudaStream_t
 }
 
 cudaError_t sum_parts(const GemmArgs& a, cudaStream_t stream) {
-  if (a.direct == a.tiles) return cudaSuccess;
-  SumArgs s{};
-  s.partial = reinterpret_cast<const float4*>(a.partial);
-  s.rows = a.rows;
-  s.cols = a.cols;
-  s.tiles_m = a.tiles_m;
-  s.tiles_n = a.tiles_n;
-  s.width = a.width;
-  s.direct = a.direct;
-  s.span = a.span;
-  s.padded = a.padded;
-  s.out[0] = a.out[0];
-  s.out[1] = a.out[1];
+  const int cut0 = a.p[0].tiles - a.p[0].direct, cut1 = a.p[1].tiles - a.p[1].direct;
+  if (cut0 + cut1 == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.tiles - a.direct, a.width / 16, 2);
+  cfg.gridDim = dim3(cut0 + cut1, std::max(cut0 > 0 ? a.p[0].width : 0, cut1 > 0 ? a.p[1].width : 0) / 16, 2);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -686,84 +741,83 @@ cudaError_t sum_parts(const GemmArgs& a, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, part_sum_kernel, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, part_sum_kernel, a, cut0);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// dx [M, K] = sum over terms of d_t [M, N] w_t [N, K].
-cudaError_t run_dx(const void* const* d, const void* const* w, int terms, void* dx, int M, int N, int K,
-                   float* partial, uint32_t* dev_status, bool after, cudaStream_t stream) {
+// For one or two d_t [M, N] with w_t [N, K] and x [M, K]: dx [M, K] = sum_t d_t w_t and
+// dw_t [N, K] = d_t^T x, dx or all dw's null where not wanted.
+cudaError_t run_grads(const void* const* d, const void* const* w, int terms, const void* x, void* dx, void* const* dw,
+                      int M, int N, int K, float* partial, bool after, uint32_t* dev_status, cudaStream_t stream) {
   GemmArgs a{};
-  a.rows = M;
-  a.cols = K;
-  a.nk[0] = ceil_div(N, kBK);
-  a.nk[1] = terms == 2 ? a.nk[0] : 0;
-  deal(&a, plan_dx(M, N, K, terms));
-  a.solid_b = K % 64 == 0 && a.width % 128 == 0;
   Maps m{};
-  cudaError_t e = map_2d(&m.out[0], dx, M, K, 32);
-  for (int t = 0; t < terms && e == cudaSuccess; ++t) {
-    e = map_2d(&m.a[t], d[t], M, N, 128);
-    if (e == cudaSuccess) e = map_mn(&m.b[t], w[t], N, K, a.width / 128, a.solid_b);
+  cudaError_t e = cudaSuccess;
+  a.p[0] = a.p[1] = no_problem();
+  int turn = 0, slot0 = 0;
+  if (dx != nullptr) {
+    const Plan plan = plan_dx(M, N, K, terms);
+    Problem& p = a.p[0] = deal(plan, M, K, ceil_div(N, kBK), terms, 0);
+    turn = last_round(plan);
+    slot0 = plan.slots;
+    p.solid_b = K % 64 == 0 && p.width % 128 == 0;
+    p.out[0] = static_cast<__nv_bfloat16*>(dx);
+    e = map_2d(&m.out[0][0], dx, M, K, 32);
+    for (int t = 0; t < terms && e == cudaSuccess; ++t) {
+      e = map_2d(&m.a[0][t], d[t], M, N, 128);
+      if (e == cudaSuccess) e = map_mn(&m.b[0][t], w[t], N, K, p.width / 128, p.solid_b);
+    }
+  }
+  if (dw[0] != nullptr && e == cudaSuccess) {
+    Problem& p = a.p[1] = deal(plan_dw(M, N, K, terms), N, K, ceil_div(M, kBK), 1, turn);
+    p.slot0 = slot0;
+    p.solid_a = N % 64 == 0;
+    p.solid_b = K % 64 == 0 && p.width % 128 == 0;
+    e = map_mn(&m.b[1][0], x, M, K, p.width / 128, p.solid_b);
+    for (int t = 0; t < terms && e == cudaSuccess; ++t) {
+      p.out[t] = static_cast<__nv_bfloat16*>(dw[t]);
+      e = map_mn(&m.a[1][t], d[t], M, N, 2, p.solid_a);
+      if (e == cudaSuccess) e = map_2d(&m.out[1][t], dw[t], N, K, 32);
+    }
   }
   if (e != cudaSuccess) return e;
-  a.partial = partial;
-  a.out[0] = static_cast<__nv_bfloat16*>(dx);
-  a.dev_status = dev_status;
-  e = launch<Use::Dx>(a, m, after, stream);
-  return e != cudaSuccess ? e : sum_parts(a, stream);
-}
-
-// dw_p [N, K] = d_p^T x for one or two d_p [M, N].
-cudaError_t run_dw(const void* const* d, int products, const void* x, void* const* dw, int M, int N, int K,
-                   float* partial, uint32_t* dev_status, bool after, cudaStream_t stream) {
-  GemmArgs a{};
-  a.rows = N;
-  a.cols = K;
-  a.nk[0] = ceil_div(M, kBK);
-  deal(&a, plan_dw(M, N, K, products));
-  a.solid_a = N % 64 == 0;
-  a.solid_b = K % 64 == 0 && a.width % 128 == 0;
-  Maps m{};
-  cudaError_t e = map_mn(&m.b[0], x, M, K, a.width / 128, a.solid_b);
-  for (int t = 0; t < products && e == cudaSuccess; ++t) {
-    e = map_mn(&m.a[t], d[t], M, N, 2, a.solid_a);
-    if (e == cudaSuccess) e = map_2d(&m.out[t], dw[t], N, K, 32);
-    a.out[t] = static_cast<__nv_bfloat16*>(dw[t]);
-  }
-  if (e != cudaSuccess) return e;
+  a.workers = kWorkers;
   a.partial = partial;
   a.dev_status = dev_status;
-  e = launch<Use::Dw>(a, m, after, stream);
+  e = launch<Use::Grads>(a, m, after, stream);
   return e != cudaSuccess ? e : sum_parts(a, stream);
 }
 
 template <Use USE>
 cudaError_t run_glu(const GluArgs& g, const void* dh, void* out0, void* out1, cudaStream_t stream) {
   GemmArgs a{};
-  a.rows = g.M;
-  a.cols = g.F;
-  a.nk[0] = ceil_div(g.K, kBK);
-  deal(&a, plan_glu(g.M, g.F, g.K));
+  a.p[0] = deal(plan_glu(g.M, g.F, g.K), g.M, g.F, ceil_div(g.K, kBK), 1, 0);
+  a.p[1] = no_problem();
+  a.workers = kWorkers;
   a.dh = static_cast<const __nv_bfloat16*>(dh);
-  a.out[0] = static_cast<__nv_bfloat16*>(out0);
-  a.out[1] = static_cast<__nv_bfloat16*>(out1);
+  a.p[0].out[0] = static_cast<__nv_bfloat16*>(out0);
+  a.p[0].out[1] = static_cast<__nv_bfloat16*>(out1);
   a.act = g.act;
   a.dev_status = g.dev_status;
+  const int width = a.p[0].width;
   Maps m{};
-  cudaError_t e = map_2d(&m.a[0], g.x, g.M, g.K, 128);
-  if (e == cudaSuccess) e = map_2d(&m.b[0], g.w_gate, g.F, g.K, a.width);
-  if (e == cudaSuccess) e = map_2d(&m.b[1], g.w_up, g.F, g.K, a.width);
-  if (e == cudaSuccess && a.width == 128) {  // narrower tiles are stored by the threads
-    e = map_2d(&m.out[0], out0, g.M, g.F, 32);
-    if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.out[1], out1, g.M, g.F, 32);
+  cudaError_t e = map_2d(&m.a[0][0], g.x, g.M, g.K, 128);
+  if (e == cudaSuccess) e = map_2d(&m.b[0][0], g.w_gate, g.F, g.K, width);
+  if (e == cudaSuccess) e = map_2d(&m.b[0][1], g.w_up, g.F, g.K, width);
+  if (e == cudaSuccess && width == 128) {  // narrower tiles are stored by the threads
+    e = map_2d(&m.out[0][0], out0, g.M, g.F, 32);
+    if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.out[0][1], out1, g.M, g.F, 32);
     if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.dh, dh, g.M, g.F, 32);
   }
   return e != cudaSuccess ? e : launch<USE>(a, m, false, stream);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t grads_bytes(int M, int N, int K, int terms, bool dx, bool dw) {
+  return static_cast<size_t>((dx ? plan_dx(M, N, K, terms).slots : 0) + (dw ? plan_dw(M, N, K, terms).slots : 0)) *
+         kSlotBytes;
+}
 
 }  // namespace
 
@@ -773,8 +827,7 @@ cudaError_t launch_glu_fwd(const GluArgs& g, void* h, cudaStream_t stream) {
 }
 
 size_t glu_bwd_ws_bytes(int M, int F, int K, bool dx, bool dw) {
-  const size_t act = up256(static_cast<size_t>(M) * F * 2);
-  return 2 * act + std::max(dx ? plan_dx(M, F, K, 2).bytes : 0, dw ? plan_dw(M, F, K, 2).bytes : 0);
+  return 2 * up256(static_cast<size_t>(M) * F * 2) + grads_bytes(M, F, K, 2, dx, dw);
 }
 
 cudaError_t launch_glu_bwd(const GluArgs& g, const void* dh, void* dx, void* dw_gate, void* dw_up, void* ws,
@@ -783,33 +836,19 @@ cudaError_t launch_glu_bwd(const GluArgs& g, const void* dh, void* dx, void* dw_
   void* dg = ws;
   void* du = static_cast<uint8_t*>(ws) + act;
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2 * act);
-  cudaError_t e = run_glu<Use::GluGrad>(g, dh, dg, du, stream);
+  const cudaError_t e = run_glu<Use::GluGrad>(g, dh, dg, du, stream);
+  if (e != cudaSuccess) return e;
   const void* d[2] = {dg, du};
-  if (e == cudaSuccess && dx != nullptr) {
-    const void* w[2] = {g.w_gate, g.w_up};
-    e = run_dx(d, w, 2, dx, g.M, g.F, g.K, partial, g.dev_status, true, stream);
-  }
-  if (e == cudaSuccess && dw_gate != nullptr) {
-    void* dw[2] = {dw_gate, dw_up};
-    e = run_dw(d, 2, g.x, dw, g.M, g.F, g.K, partial, g.dev_status, true, stream);
-  }
-  return e;
+  const void* w[2] = {g.w_gate, g.w_up};
+  void* dw[2] = {dw_gate, dw_up};
+  return run_grads(d, w, 2, g.x, dx, dw, g.M, g.F, g.K, partial, true, g.dev_status, stream);
 }
 
-size_t linear_bwd_ws_bytes(int M, int N, int K, bool dx, bool dw) {
-  return std::max(dx ? plan_dx(M, N, K, 1).bytes : 0, dw ? plan_dw(M, N, K, 1).bytes : 0);
-}
+size_t linear_bwd_ws_bytes(int M, int N, int K, bool dx, bool dw) { return grads_bytes(M, N, K, 1, dx, dw); }
 
 cudaError_t launch_linear_bwd(const void* dy, const void* x, const void* w, void* dx, void* dw, int M, int N, int K,
                               void* ws, uint32_t* dev_status, cudaStream_t stream) {
-  cudaError_t e = cudaSuccess;
-  const void* d[2] = {dy, dy};
-  const void* ww[2] = {w, w};
-  void* o[2] = {dw, dw};
-  if (dx != nullptr) e = run_dx(d, ww, 1, dx, M, N, K, static_cast<float*>(ws), dev_status, false, stream);
-  if (e == cudaSuccess && dw != nullptr)
-    e = run_dw(d, 1, x, o, M, N, K, static_cast<float*>(ws), dev_status, dx != nullptr, stream);
-  return e;
+  return run_grads(&dy, &w, 1, x, dx, &dw, M, N, K, static_cast<float*>(ws), false, dev_status, stream);
 }
 
 }  // namespace rapt

@@ -26,6 +26,23 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// tc::mbar_wait, but a phase that is already complete costs one probe and no clock.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, long long max_cycles) {
+  return tc::mbar_try_wait(bar, parity) || tc::mbar_wait(bar, parity, max_cycles);
+}
+// A place in a ring of N stages and how often the ring has been round, for a single thread's loop.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == N) {
+      s = 0;
+      ++round;
+    }
+  }
+};
+
 // One arrival on an mbarrier of any CTA of the cluster (an address from map_rank). What it announces here
 // is that TMEM has been read, which tcgen05.fence::before_thread_sync orders before it; a release at
 // cluster scope, which would wait for the thread's shared-memory stores as well, took 40 % of the
