@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tcp::tma_load_2d(st + kA, mb, kb * kBK, n0, bar);
           });
         } else {
-          const int half = p.width / 2, blocks = (half + 63) / 64, nb = n0 + rank * half;
+          const int half = p.width / 2, blocks = half / 64, nb = n0 + rank * half;
           const uint32_t bytes = 2 * (kA + blocks * kBox);
           const bool solid_a = p.solid_a, solid_b = p.solid_b;
           // columns c .. of an MN-major operand: one box of the block map, or a box for every block
@@ -604,11 +604,12 @@ struct Plan {
   int width, tiles_m, tiles_n, tiles, direct, span, padded, slots;
   double cost;
 };
-// Tiles of `width` output columns (`full` at most). A slice of a narrow tile costs more than its share of
-// the products: it still loads the 256 rows of A (half of a full slice's bytes), and the loads of all
-// pairs together keep L2 as busy as the tensor cores (64-column tiles ran at 290 TFLOP/s).
+// Tiles of `width` output columns (`full` at most). A slice of a narrow tile saves little: it still loads
+// the 256 rows of A and goes round the ring. Measured against a full tile's: 0.84 at 80 of 128 columns,
+// 0.90 at 112 of 128, 0.85 at 128 of 256 (1.05 at 192 and 1.0 at 64 of 256, where the halves of B do not
+// start at a block: those widths are not offered).
 Plan plan_width(int rows, int cols, int products, int nk, int width, int full, bool may_cut) {
-  const double part = static_cast<double>(width) / full, share = std::max(part, 0.9 * (0.5 + 0.5 * part));
+  const double share = 0.65 + 0.35 * width / full;
   Plan p{};
   p.width = width;
   p.tiles_m = ceil_div(rows, kPairRows);
@@ -621,7 +622,7 @@ Plan plan_width(int rows, int cols, int products, int nk, int width, int full, b
   if (!may_cut || left == 0) return p;
   // the tiles of the last round, cut: shares of at least four slices. Where a tile takes two pairs or
   // more, all tiles are cut at the same places: pairs then read the same slices of A and B at the same
-  // time, and they meet in L2. Every pair's part is written and read once, together about 6 KB in a ns.
+  // time, and they meet in L2. Every pair's part is written and read once, together about 9 KB in a ns.
   int span = std::max(4, ceil_div(static_cast<long>(left) * nk, kWorkers)), padded = nk;
   if (2 * left <= kWorkers) {
     span = std::max(4, ceil_div(nk, kWorkers / left));
@@ -630,7 +631,7 @@ Plan plan_width(int rows, int cols, int products, int nk, int width, int full, b
   const int pairs = ceil_div(static_cast<long>(left) * padded, span);
   const double bytes = static_cast<double>(pairs + left) * kPairRows * width * 8;
   const double cost = static_cast<double>(p.tiles / kWorkers) * (nk * share + kUnit) + span * share + 2 * kUnit +
-                      kSumLaunch + bytes / 6000.0 / 270.0;
+                      kSumLaunch + bytes / 9000.0 / 270.0;
   if (cost < p.cost) {
     p.direct = p.tiles - left;
     p.span = span;
@@ -650,14 +651,11 @@ Plan plan_glu(int M, int F, int K) {
   }
   return best;
 }
-// The others: 256 columns, or 192, 128 or 64.
+// The others: 256 columns, or 128 where that saves a round.
 Plan plan_sum(int rows, int cols, int products, int nk) {
-  Plan best{};
-  for (int width = 256; width >= 64; width -= 64) {
-    const Plan p = plan_width(rows, cols, products, nk, width, 256, true);
-    if (width == 256 || p.cost < 0.97 * best.cost) best = p;
-  }
-  return best;
+  const Plan wide = plan_width(rows, cols, products, nk, 256, 256, true);
+  const Plan narrow = plan_width(rows, cols, products, nk, 128, 256, true);
+  return narrow.cost < 0.97 * wide.cost ? narrow : wide;
 }
 Plan plan_dx(int M, int N, int K, int terms) { return plan_sum(M, K, 1, terms * ceil_div(N, kBK)); }
 Plan plan_dw(int M, int N, int K, int products) { return plan_sum(N, K, products, ceil_div(M, kBK)); }
@@ -760,7 +758,7 @@ cudaError_t run_grads(const void* const* d, const void* const* w, int terms, con
     Problem& p = a.p[0] = deal(plan, M, K, ceil_div(N, kBK), terms, 0);
     turn = last_round(plan);
     slot0 = plan.slots;
-    p.solid_b = K % 64 == 0 && p.width % 128 == 0;
+    p.solid_b = K % 64 == 0;
     p.out[0] = static_cast<__nv_bfloat16*>(dx);
     e = map_2d(&m.out[0][0], dx, M, K, 32);
     for (int t = 0; t < terms && e == cudaSuccess; ++t) {
@@ -772,7 +770,7 @@ cudaError_t run_grads(const void* const* d, const void* const* w, int terms, con
     Problem& p = a.p[1] = deal(plan_dw(M, N, K, terms), N, K, ceil_div(M, kBK), 1, turn);
     p.slot0 = slot0;
     p.solid_a = N % 64 == 0;
-    p.solid_b = K % 64 == 0 && p.width % 128 == 0;
+    p.solid_b = K % 64 == 0;
     e = map_mn(&m.b[1][0], x, M, K, p.width / 128, p.solid_b);
     for (int t = 0; t < terms && e == cudaSuccess; ++t) {
       p.out[t] = static_cast<__nv_bfloat16*>(dw[t]);
