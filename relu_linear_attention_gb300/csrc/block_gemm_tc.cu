@@ -66,10 +66,11 @@ constexpr uint32_t kSmem = kMisc + 16;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kRaster = 8;  // tile rows taken together
 
-// The tensor maps of one launch: A and B of up to two terms or products of each problem, outputs, dh.
+// The tensor maps of one launch: A and B of up to two terms or products of each problem (the MN-major ones
+// also block by block), outputs, dh.
 struct Maps {
-  CUtensorMap a[2][2];
-  CUtensorMap b[2][2];
+  CUtensorMap a[2][2], a_blocks[2];
+  CUtensorMap b[2][2], b_blocks[2][2];
   CUtensorMap out[2][2];
   CUtensorMap dh;
 };
@@ -87,8 +88,9 @@ struct Problem {
   int nk0, nk;           // slices of a tile's sum: of its first term, in all
   int direct, span, padded, turn;
   int slot0;             // first of its parts' places in the workspace
-  bool solid_a, solid_b;  // whether an MN-major operand's map is one of blocks
+  int solid_a, solid_b;  // columns of the MN-major A (Dw) and B that their block maps have
   __nv_bfloat16* out[2];
+  int pitch;  // elements of an output's row (Glu)
 };
 struct GemmArgs {
   Problem p[2];
@@ -208,7 +210,7 @@ __device__ __forceinline__ void put16(__nv_bfloat16* out, int row, int col, cons
 #pragma unroll
   for (int q = 0; q < 2; ++q)
     if (row < p.rows && col + 8 * q < p.cols)
-      *reinterpret_cast<uint4*>(out + static_cast<long>(row) * p.cols + col + 8 * q) =
+      *reinterpret_cast<uint4*>(out + static_cast<long>(row) * p.pitch + col + 8 * q) =
           make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
 }
 
@@ -279,11 +281,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const int half = p.width / 2, blocks = half / 64, nb = n0 + rank * half;
           const uint32_t bytes = 2 * (kA + blocks * kBox);
-          const bool solid_a = p.solid_a, solid_b = p.solid_b;
-          // columns c .. of an MN-major operand: one box of the block map, or a box for every block
-          const auto load_mn = [&](const CUtensorMap* map, bool solid, int n, uint32_t dst, int c, int k, uint32_t bar) {
+          const bool solid_a = m0 + kBM <= p.solid_a, solid_b = nb + half <= p.solid_b;
+          // columns c .. of an MN-major operand: one box of the block map where it has them all, or a box
+          // for every block
+          const auto load_mn = [&](const CUtensorMap* map, const CUtensorMap* by_block, bool solid, int n, uint32_t dst,
+                                   int c, int k, uint32_t bar) {
             if (solid) {
-              tcp::tma_load_3d(dst, map, 0, k, c / 64, bar);
+              tcp::tma_load_3d(dst, by_block, 0, k, c / 64, bar);
             } else {
               tcp::tma_load_2d(dst, map, c, k, bar);
               if (n > 1) tcp::tma_load_2d(dst + kBox, map, c + 64, k, bar);
@@ -292,19 +296,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (w.q == 0) {
             const int nk0 = p.nk0;
             for (int term = 0; term < 2 && ok; ++term) {
-              const CUtensorMap *ma = &maps.a[0][term], *mb = &maps.b[0][term];
+              const CUtensorMap *ma = &maps.a[0][term], *mb = &maps.b[0][term], *bb = &maps.b_blocks[0][term];
               const int skip = term * nk0;  // slices of the terms before
               stream(max(w.k0, skip), min(w.k1, skip + nk0), bytes, [&](uint32_t st, uint32_t bar, int kb) {
                 const int k = (kb - skip) * kBK;
                 tcp::tma_load_2d(st, ma, k, m0, bar);
-                load_mn(mb, solid_b, blocks, st + kA, nb, k, bar);
+                load_mn(mb, bb, solid_b, blocks, st + kA, nb, k, bar);
               });
             }
           } else {
             const CUtensorMap *ma = &maps.a[1][t.product], *mb = &maps.b[1][0];
+            const CUtensorMap *ab = &maps.a_blocks[t.product], *bb = &maps.b_blocks[1][0];
             stream(w.k0, w.k1, bytes, [&](uint32_t st, uint32_t bar, int kb) {
-              load_mn(ma, solid_a, 2, st, m0, kb * kBK, bar);
-              load_mn(mb, solid_b, blocks, st + kA, nb, kb * kBK, bar);
+              load_mn(ma, ab, solid_a, 2, st, m0, kb * kBK, bar);
+              load_mn(mb, bb, solid_b, blocks, st + kA, nb, kb * kBK, bar);
             });
           }
         }
@@ -574,25 +579,33 @@ __global__ void __launch_bounds__(256) part_sum_kernel(const __grid_constant__ G
 
 int ceil_div(long a, long b) { return static_cast<int>((a + b - 1) / b); }
 
-// A row-major bf16 [rows, cols] matrix in boxes of box_rows x 64 columns.
-cudaError_t map_2d(CUtensorMap* m, const void* p, int rows, int cols, int box_rows) {
+// A row-major bf16 [rows, cols] matrix, `pitch` elements a row, in boxes of box_rows x 64 columns.
+cudaError_t map_2d(CUtensorMap* m, const void* p, int rows, int cols, int pitch, int box_rows) {
   const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
-  const uint64_t strides[1] = {static_cast<uint64_t>(cols) * 2};
+  const uint64_t strides[1] = {static_cast<uint64_t>(pitch) * 2};
   const uint32_t box[2] = {64, static_cast<uint32_t>(box_rows)};
   return encode_bf16_map(m, p, 2, dims, strides, box);
 }
 
-// An MN-major operand: a row-major bf16 [rows, cols] matrix in boxes of 64 rows (the sum's index) and
-// `blocks` blocks of 64 columns, block by block as the tensor core reads them. Where the columns are
-// whole blocks, they are a dimension of their own and one box brings them all: TMA takes about as long
-// to start a box as to copy 4 KB. Otherwise a box is one block, so that what lies past a row's end is
-// zeros and not the next row.
-cudaError_t map_mn(CUtensorMap* m, const void* p, int rows, int cols, int blocks, bool solid) {
-  if (!solid) return map_2d(m, p, rows, cols, 64);
-  const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols / 64)};
-  const uint64_t strides[2] = {static_cast<uint64_t>(cols) * 2, 128};
+// An MN-major operand: such a matrix in boxes of 64 rows (the sum's index) and 64 columns and, as far as
+// whole blocks of 64 columns go (*solid columns), in boxes of `blocks` of them, block by block as the
+// tensor core reads them: TMA takes about as long to start a box as to copy 4 KB. What follows the whole
+// blocks is left to the first map, which has zeros past a row's end where the block map would read on.
+// A row whose pitch has room for its last block may count it as whole: what it reads there ends in
+// columns that are not stored.
+cudaError_t map_mn(CUtensorMap* m, CUtensorMap* by_block, const void* p, int rows, int cols, int pitch, int blocks,
+                   int* solid) {
+  const int whole = pitch > cols ? (cols + 63) / 64 : cols / 64;
+  *solid = 64 * whole;
+  cudaError_t e = map_2d(m, p, rows, cols, pitch, 64);
+  if (e != cudaSuccess || whole < blocks) {
+    *solid = 0;
+    return e;
+  }
+  const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(whole)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(pitch) * 2, 128};
   const uint32_t box[3] = {64, 64, static_cast<uint32_t>(blocks)};
-  return encode_bf16_map(m, p, 3, dims, strides, box);
+  return encode_bf16_map(by_block, p, 3, dims, strides, box);
 }
 
 // How a launch is dealt out. The unit of cost is a 64-deep slice of a full tile (512 cycles, 0.27 us).
@@ -745,8 +758,8 @@ cudaError_t sum_parts(const GemmArgs& a, cudaStream_t stream) {
 }
 
 // For one or two d_t [M, N] with w_t [N, K] and x [M, K]: dx [M, K] = sum_t d_t w_t and
-// dw_t [N, K] = d_t^T x, dx or all dw's null where not wanted.
-cudaError_t run_grads(const void* const* d, const void* const* w, int terms, const void* x, void* dx, void* const* dw,
+// dw_t [N, K] = d_t^T x, dx or all dw's null where not wanted. d_t's rows are `pitch` elements apart.
+cudaError_t run_grads(const void* const* d, int pitch, const void* const* w, int terms, const void* x, void* dx, void* const* dw,
                       int M, int N, int K, float* partial, bool after, uint32_t* dev_status, cudaStream_t stream) {
   GemmArgs a{};
   Maps m{};
@@ -758,24 +771,22 @@ cudaError_t run_grads(const void* const* d, const void* const* w, int terms, con
     Problem& p = a.p[0] = deal(plan, M, K, ceil_div(N, kBK), terms, 0);
     turn = last_round(plan);
     slot0 = plan.slots;
-    p.solid_b = K % 64 == 0;
     p.out[0] = static_cast<__nv_bfloat16*>(dx);
-    e = map_2d(&m.out[0][0], dx, M, K, 32);
+    e = map_2d(&m.out[0][0], dx, M, K, K, 32);
     for (int t = 0; t < terms && e == cudaSuccess; ++t) {
-      e = map_2d(&m.a[0][t], d[t], M, N, 128);
-      if (e == cudaSuccess) e = map_mn(&m.b[0][t], w[t], N, K, p.width / 128, p.solid_b);
+      e = map_2d(&m.a[0][t], d[t], M, N, pitch, 128);
+      if (e == cudaSuccess)
+        e = map_mn(&m.b[0][t], &m.b_blocks[0][t], w[t], N, K, K, p.width / 128, &p.solid_b);
     }
   }
   if (dw[0] != nullptr && e == cudaSuccess) {
     Problem& p = a.p[1] = deal(plan_dw(M, N, K, terms), N, K, ceil_div(M, kBK), 1, turn);
     p.slot0 = slot0;
-    p.solid_a = N % 64 == 0;
-    p.solid_b = K % 64 == 0;
-    e = map_mn(&m.b[1][0], x, M, K, p.width / 128, p.solid_b);
+    e = map_mn(&m.b[1][0], &m.b_blocks[1][0], x, M, K, K, p.width / 128, &p.solid_b);
     for (int t = 0; t < terms && e == cudaSuccess; ++t) {
       p.out[t] = static_cast<__nv_bfloat16*>(dw[t]);
-      e = map_mn(&m.a[1][t], d[t], M, N, 2, p.solid_a);
-      if (e == cudaSuccess) e = map_2d(&m.out[1][t], dw[t], N, K, 32);
+      e = map_mn(&m.a[1][t], &m.a_blocks[t], d[t], M, N, pitch, 2, &p.solid_a);
+      if (e == cudaSuccess) e = map_2d(&m.out[1][t], dw[t], N, K, K, 32);
     }
   }
   if (e != cudaSuccess) return e;
@@ -786,8 +797,9 @@ cudaError_t run_grads(const void* const* d, const void* const* w, int terms, con
   return e != cudaSuccess ? e : sum_parts(a, stream);
 }
 
+// Outputs of `pitch` elements a row.
 template <Use USE>
-cudaError_t run_glu(const GluArgs& g, const void* dh, void* out0, void* out1, cudaStream_t stream) {
+cudaError_t run_glu(const GluArgs& g, const void* dh, void* out0, void* out1, int pitch, cudaStream_t stream) {
   GemmArgs a{};
   a.p[0] = deal(plan_glu(g.M, g.F, g.K), g.M, g.F, ceil_div(g.K, kBK), 1, 0);
   a.p[1] = no_problem();
@@ -795,17 +807,18 @@ cudaError_t run_glu(const GluArgs& g, const void* dh, void* out0, void* out1, cu
   a.dh = static_cast<const __nv_bfloat16*>(dh);
   a.p[0].out[0] = static_cast<__nv_bfloat16*>(out0);
   a.p[0].out[1] = static_cast<__nv_bfloat16*>(out1);
+  a.p[0].pitch = pitch;
   a.act = g.act;
   a.dev_status = g.dev_status;
   const int width = a.p[0].width;
   Maps m{};
-  cudaError_t e = map_2d(&m.a[0][0], g.x, g.M, g.K, 128);
-  if (e == cudaSuccess) e = map_2d(&m.b[0][0], g.w_gate, g.F, g.K, width);
-  if (e == cudaSuccess) e = map_2d(&m.b[0][1], g.w_up, g.F, g.K, width);
+  cudaError_t e = map_2d(&m.a[0][0], g.x, g.M, g.K, g.K, 128);
+  if (e == cudaSuccess) e = map_2d(&m.b[0][0], g.w_gate, g.F, g.K, g.K, width);
+  if (e == cudaSuccess) e = map_2d(&m.b[0][1], g.w_up, g.F, g.K, g.K, width);
   if (e == cudaSuccess && width == 128) {  // narrower tiles are stored by the threads
-    e = map_2d(&m.out[0][0], out0, g.M, g.F, 32);
-    if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.out[0][1], out1, g.M, g.F, 32);
-    if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.dh, dh, g.M, g.F, 32);
+    e = map_2d(&m.out[0][0], out0, g.M, g.F, pitch, 32);
+    if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.out[0][1], out1, g.M, g.F, pitch, 32);
+    if (e == cudaSuccess && USE == Use::GluGrad) e = map_2d(&m.dh, dh, g.M, g.F, g.F, 32);
   }
   return e != cudaSuccess ? e : launch<USE>(a, m, false, stream);
 }
@@ -821,32 +834,35 @@ size_t grads_bytes(int M, int N, int K, int terms, bool dx, bool dw) {
 
 cudaError_t launch_glu_fwd(const GluArgs& g, void* h, cudaStream_t stream) {
   if (g.M <= kGluDecodeRows) return launch_glu_decode(g, h, stream);
-  return run_glu<Use::Glu>(g, nullptr, h, nullptr, stream);
+  return run_glu<Use::Glu>(g, nullptr, h, nullptr, g.F, stream);
 }
 
+// dg and du lie in rows of whole 64-column blocks: every box of them is aligned, and one brings two blocks.
+int grad_pitch(int F) { return (F + 63) / 64 * 64; }
 size_t glu_bwd_ws_bytes(int M, int F, int K, bool dx, bool dw) {
-  return 2 * up256(static_cast<size_t>(M) * F * 2) + grads_bytes(M, F, K, 2, dx, dw);
+  return 2 * up256(static_cast<size_t>(M) * grad_pitch(F) * 2) + grads_bytes(M, F, K, 2, dx, dw);
 }
 
 cudaError_t launch_glu_bwd(const GluArgs& g, const void* dh, void* dx, void* dw_gate, void* dw_up, void* ws,
                            cudaStream_t stream) {
-  const size_t act = up256(static_cast<size_t>(g.M) * g.F * 2);
+  const int pitch = grad_pitch(g.F);
+  const size_t act = up256(static_cast<size_t>(g.M) * pitch * 2);
   void* dg = ws;
   void* du = static_cast<uint8_t*>(ws) + act;
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2 * act);
-  const cudaError_t e = run_glu<Use::GluGrad>(g, dh, dg, du, stream);
+  const cudaError_t e = run_glu<Use::GluGrad>(g, dh, dg, du, pitch, stream);
   if (e != cudaSuccess) return e;
   const void* d[2] = {dg, du};
   const void* w[2] = {g.w_gate, g.w_up};
   void* dw[2] = {dw_gate, dw_up};
-  return run_grads(d, w, 2, g.x, dx, dw, g.M, g.F, g.K, partial, true, g.dev_status, stream);
+  return run_grads(d, pitch, w, 2, g.x, dx, dw, g.M, g.F, g.K, partial, true, g.dev_status, stream);
 }
 
 size_t linear_bwd_ws_bytes(int M, int N, int K, bool dx, bool dw) { return grads_bytes(M, N, K, 1, dx, dw); }
 
 cudaError_t launch_linear_bwd(const void* dy, const void* x, const void* w, void* dx, void* dw, int M, int N, int K,
                               void* ws, uint32_t* dev_status, cudaStream_t stream) {
-  return run_grads(&dy, &w, 1, x, dx, &dw, M, N, K, static_cast<float*>(ws), false, dev_status, stream);
+  return run_grads(&dy, N, &w, 1, x, dx, &dw, M, N, K, static_cast<float*>(ws), false, dev_status, stream);
 }
 
 }  // namespace rapt
