@@ -355,17 +355,25 @@ def _act_code(act):
     return code
 
 
-def _launch(index, stream, call):
-    """call(stream handle) with CUDA device `index` current; what it allocates belongs to the stream it
-    launches on."""
-    if stream is None and index == torch.cuda.current_device():
-        # the handle alone: a stream object costs 3 us on the host, as much as the launch
-        return call(torch._C._cuda_getCurrentRawStream(index))
+def _here(index, stream):
+    """Whether a call goes to the current stream of the current device, CUDA device `index`."""
+    _need(index >= 0, "the tensors must be CUDA tensors")
+    return stream is None and index == torch.cuda.current_device()
+
+
+def _elsewhere(call, index, stream, *args, **kwargs):
+    """call(*args, **kwargs) with CUDA device `index` and `stream` made current: what it allocates belongs
+    to the stream that it launches on."""
     with torch.cuda.device(index):
         s = torch.cuda.current_stream() if stream is None else stream
         _need(s.device_index == index, "stream and tensors are on different devices")
         with torch.cuda.stream(s):
-            return call(s.cuda_stream)
+            return call(*args, **kwargs)
+
+
+def _handle(index):
+    """The current stream's handle alone: a stream object costs 3 us on the host, as much as a launch."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _scratch(need, workspace, like):
@@ -392,35 +400,42 @@ def rapt_residual_norm_fwd(x, y=None, *, gate=None, w_post=None, scale=None, w_p
     x, y, gate [..., D] (fp32 or bf16), gains fp32 [D]; each of y, gate, w_post and scale may be
     missing (see include/rapt.h). Returns (r, h): r is x itself without y unless an r is passed, h is
     None without w_pre. r and h may be passed to be written, and may be x, y or gate themselves."""
-    di, dt, shape = x.get_device(), x.dtype, x.shape
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_residual_norm_fwd, di, stream, x, y, gate=gate, w_post=w_post,
+                          scale=scale, w_pre=w_pre, act=act, eps=eps, r=r, h=h)
+    dt, shape = x.dtype, x.shape
     _need(dt in _DT, "dtype must be float32 or bfloat16")
     _need(len(shape) >= 1, "x must be [..., D]")
+    _need(h is None or w_pre is not None, "h needs w_pre")
     D = shape[-1]
+    f32, row = torch.float32, shape[-1:]
     xp, yp = _like("x", x, dt, shape, di), _opt_like("y", y, dt, shape, di)
     gp = _opt_like("gate", gate, dt, shape, di)
-    f32, row = torch.float32, shape[-1:]
     wp, sp = _opt_like("w_post", w_post, f32, row, di), _opt_like("scale", scale, f32, row, di)
     pp = _opt_like("w_pre", w_pre, f32, row, di)
     rp, hp = _opt_like("r", r, dt, shape, di), _opt_like("h", h, dt, shape, di)
-    _need(h is None or w_pre is not None, "h needs w_pre")
-    T = x.numel() // D if D else 0
-    code, lib = _act_code(act), _lib.load()
+    if r is None and y is not None:
+        r = torch.empty_like(x)
+        rp = r.data_ptr()
+    if h is None and w_pre is not None:
+        h = torch.empty_like(x)
+        hp = h.data_ptr()
+    st = _lib.load().rapt_residual_norm_fwd(xp, yp, gp, _DT[dt], x.numel() // D if D else 0, D,
+                                            _act_code(act), wp, sp, pp, eps, rp, hp, _handle(di))
+    if st:
+        _lib.check("rapt_residual_norm_fwd", st)
+    return (x if r is None else r), h
 
-    def call(s):
-        ro, ho = r, h
-        if ro is None and y is not None:
-            ro = torch.empty_like(x)
-        if ho is None and w_pre is not None:
-            ho = torch.empty_like(x)
-        st = lib.rapt_residual_norm_fwd(
-            xp, yp, gp, _DT[dt], T, D, code, wp, sp, pp, eps,
-            rp if ro is None or rp is not None else ro.data_ptr(),
-            hp if ho is None or hp is not None else ho.data_ptr(), s)
-        if st:
-            _lib.check("rapt_residual_norm_fwd", st)
-        return (x if ro is None else ro), ho
 
-    return _launch(di, stream, call)
+def _out(name, t, like, wanted, index):
+    """(tensor, address) of an output like `like`: the caller's t, a new one if wanted, or none."""
+    if t is not None:
+        return t, _like(name, t, like.dtype, like.shape, index)
+    if not wanted:
+        return None, None
+    t = torch.empty_like(like)
+    return t, t.data_ptr()
 
 
 def rapt_residual_norm_bwd(dr, dh, x, y=None, *, gate=None, w_post=None, scale=None, w_pre=None,
@@ -432,7 +447,13 @@ def rapt_residual_norm_bwd(dr, dh, x, y=None, *, gate=None, w_post=None, scale=N
     [..., D] inputs."""
     first = dr if dr is not None else dh
     _need(first is not None, "one of dr and dh is needed")
-    di, dt, shape = first.get_device(), first.dtype, first.shape
+    di = first.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_residual_norm_bwd, di, stream, dr, dh, x, y, gate=gate, w_post=w_post,
+                          scale=scale, w_pre=w_pre, act=act, eps=eps, need_dx=need_dx,
+                          need_dy=need_dy, need_dgate=need_dgate, need_dw=need_dw, dx=dx, dy=dy,
+                          dgate=dgate, workspace=workspace)
+    dt, shape = first.dtype, first.shape
     _need(dt in _DT, "dtype must be float32 or bfloat16")
     _need(len(shape) >= 1, "dr and dh must be [..., D]")
     D = shape[-1]
@@ -443,93 +464,73 @@ def rapt_residual_norm_bwd(dr, dh, x, y=None, *, gate=None, w_post=None, scale=N
     gains = (_opt_like("w_post", w_post, f32, row, di), _opt_like("scale", scale, f32, row, di),
              _opt_like("w_pre", w_pre, f32, row, di))
     T = first.numel() // D if D else 0
-    code, lib = _act_code(act), _lib.load()
+    lib = _lib.load()
+    dx, dxp = _out("dx", dx, first, need_dx, di)
+    dy, dyp = _out("dy", dy, first, need_dy and y is not None, di)
+    dgate, dgp = _out("dgate", dgate, first, need_dgate and gate is not None, di)
+    sums, wsp, wsb, owner = [None] * 3, None, 0, None
+    if need_dw:
+        sums = [None if w is None else torch.empty_like(w)
+                for w in (w_post, scale, w_pre if dh is not None else None)]
+        if any(t is not None for t in sums):
+            need = lib.rapt_residual_norm_bwd_workspace_size(T, D, _DT[dt])
+            wsp, wsb, owner = _scratch(need, workspace, first)
+    st = lib.rapt_residual_norm_bwd(*ins, _DT[dt], T, D, _act_code(act), *gains, eps, dxp, dyp, dgp,
+                                    *[None if t is None else t.data_ptr() for t in sums], wsp, wsb,
+                                    _handle(di))
+    if st:
+        _lib.check("rapt_residual_norm_bwd", st)
+    return (dx, dy, dgate, *sums)
 
-    def call(s):
-        def out(name, t, wanted):
-            if t is not None:
-                return t, _like(name, t, dt, shape, di)
-            if not wanted:
-                return None, None
-            t = torch.empty_like(first)
-            return t, t.data_ptr()
 
-        ox, oxp = out("dx", dx, need_dx)
-        oy, oyp = out("dy", dy, need_dy and y is not None)
-        og, ogp = out("dgate", dgate, need_dgate and gate is not None)
-        sums = [None] * 3
-        wsp, wsb, _keep = None, 0, None
-        if need_dw:
-            sums = [None if w is None else torch.empty_like(w)
-                    for w in (w_post, scale, w_pre if dh is not None else None)]
-            if any(t is not None for t in sums):
-                need = lib.rapt_residual_norm_bwd_workspace_size(T, D, _DT[dt])
-                wsp, wsb, _keep = _scratch(need, workspace, first)
-        st = lib.rapt_residual_norm_bwd(*ins, _DT[dt], T, D, code, *gains, eps, oxp, oyp, ogp,
-                                        *[None if t is None else t.data_ptr() for t in sums],
-                                        wsp, wsb, s)
-        if st:
-            _lib.check("rapt_residual_norm_bwd", st)
-        return (ox, oy, og, *sums)
-
-    return _launch(di, stream, call)
+def _glu_inputs(x, w_gate, w_up, index):
+    """(K, F, shape of h, addresses of x, w_gate, w_up) of a gated feed-forward."""
+    bf16, xs, ws = torch.bfloat16, x.shape, w_gate.shape
+    _need(len(xs) >= 1 and len(ws) == 2 and ws[1] == xs[-1], "x [..., K], w_gate and w_up [F, K]")
+    return (ws[1], ws[0], xs[:-1] + ws[:1], _like("x", x, bf16, xs, index),
+            _like("w_gate", w_gate, bf16, ws, index), _like("w_up", w_up, bf16, ws, index))
 
 
 def rapt_glu_fwd(x, w_gate, w_up, *, act="silu", h=None, dev_status=None, stream=None):
     """Gated feed-forward h = act(x w_gate^T) (x w_up^T): x [..., K], w_gate and w_up [F, K], bf16.
     Returns h [..., F] bf16."""
-    di, bf16, xs, ws = x.get_device(), torch.bfloat16, x.shape, w_gate.shape
-    _need(len(xs) >= 1 and len(ws) == 2 and ws[1] == xs[-1], "x [..., K], w_gate and w_up [F, K]")
-    F, K = ws
-    xp = _like("x", x, bf16, xs, di)
-    gp, up = _like("w_gate", w_gate, bf16, ws, di), _like("w_up", w_up, bf16, ws, di)
-    shape = xs[:-1] + ws[:1]
-    hp = _opt_like("h", h, bf16, shape, di)
-    code, lib, sp = _act_code(act), _lib.load(), _status_ptr(dev_status, di)
-
-    def call(s):
-        o = torch.empty(shape, dtype=bf16, device=x.device) if h is None else h
-        st = lib.rapt_glu_fwd(xp, gp, up, x.numel() // K if K else 0, F, K, code,
-                              o.data_ptr() if h is None else hp, sp, s)
-        if st:
-            _lib.check("rapt_glu_fwd", st)
-        return o
-
-    return _launch(di, stream, call)
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_glu_fwd, di, stream, x, w_gate, w_up, act=act, h=h, dev_status=dev_status)
+    K, F, shape, xp, gp, up = _glu_inputs(x, w_gate, w_up, di)
+    if h is None:
+        h = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        hp = h.data_ptr()
+    else:
+        hp = _like("h", h, torch.bfloat16, shape, di)
+    st = _lib.load().rapt_glu_fwd(xp, gp, up, x.numel() // K if K else 0, F, K, _act_code(act), hp,
+                                  _status_ptr(dev_status, di), _handle(di))
+    if st:
+        _lib.check("rapt_glu_fwd", st)
+    return h
 
 
 def rapt_glu_bwd(dh, x, w_gate, w_up, *, act="silu", need_dx=True, need_dw=True, dx=None,
                  dw_gate=None, dw_up=None, dev_status=None, workspace=None, stream=None):
     """Gradients of sum(dh h) for rapt_glu_fwd: dh [..., F]. Returns (dx, dw_gate, dw_up), None for
     what is not needed."""
-    di, bf16, xs, ws = x.get_device(), torch.bfloat16, x.shape, w_gate.shape
-    _need(len(xs) >= 1 and len(ws) == 2 and ws[1] == xs[-1], "x [..., K], w_gate and w_up [F, K]")
-    F, K = ws
-    hp = _like("dh", dh, bf16, xs[:-1] + ws[:1], di)
-    xp = _like("x", x, bf16, xs, di)
-    gp, up = _like("w_gate", w_gate, bf16, ws, di), _like("w_up", w_up, bf16, ws, di)
-    M = x.numel() // K if K else 0
-    code, lib, sp = _act_code(act), _lib.load(), _status_ptr(dev_status, di)
-
-    def call(s):
-        def out(name, t, like, wanted):
-            if t is not None:
-                return t, _like(name, t, bf16, like.shape, di)
-            if not wanted:
-                return None, None
-            t = torch.empty_like(like)
-            return t, t.data_ptr()
-
-        ox, oxp = out("dx", dx, x, need_dx)
-        og, ogp = out("dw_gate", dw_gate, w_gate, need_dw)
-        ou, oup = out("dw_up", dw_up, w_up, need_dw)
-        wsp, wsb, _keep = _scratch(lib.rapt_glu_bwd_workspace_size(M, F, K), workspace, x)
-        st = lib.rapt_glu_bwd(hp, xp, gp, up, M, F, K, code, oxp, ogp, oup, sp, wsp, wsb, s)
-        if st:
-            _lib.check("rapt_glu_bwd", st)
-        return ox, og, ou
-
-    return _launch(di, stream, call)
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_glu_bwd, di, stream, dh, x, w_gate, w_up, act=act, need_dx=need_dx,
+                          need_dw=need_dw, dx=dx, dw_gate=dw_gate, dw_up=dw_up,
+                          dev_status=dev_status, workspace=workspace)
+    K, F, shape, xp, gp, up = _glu_inputs(x, w_gate, w_up, di)
+    hp = _like("dh", dh, torch.bfloat16, shape, di)
+    M, lib = x.numel() // K if K else 0, _lib.load()
+    dx, dxp = _out("dx", dx, x, need_dx, di)
+    dw_gate, dgp = _out("dw_gate", dw_gate, w_gate, need_dw, di)
+    dw_up, dup = _out("dw_up", dw_up, w_up, need_dw, di)
+    wsp, wsb, owner = _scratch(lib.rapt_glu_bwd_workspace_size(M, F, K), workspace, x)
+    st = lib.rapt_glu_bwd(hp, xp, gp, up, M, F, K, _act_code(act), dxp, dgp, dup,
+                          _status_ptr(dev_status, di), wsp, wsb, _handle(di))
+    if st:
+        _lib.check("rapt_glu_bwd", st)
+    return dx, dw_gate, dw_up
 
 
 def rapt_linear_bwd(dy, x, w, *, need_dx=True, need_dw=True, dx=None, dw=None, dev_status=None,
@@ -537,36 +538,34 @@ def rapt_linear_bwd(dy, x, w, *, need_dx=True, need_dw=True, dx=None, dw=None, d
     """Gradients of y = x W^T (rapt_linear_fwd): dx = dy W, dw = dy^T x; dy [..., N], x [..., K],
     w [N, K], bf16. x may be None without dw, w without dx. Returns (dx, dw), None for what is not
     needed."""
-    di, bf16, ys = dy.get_device(), torch.bfloat16, dy.shape
-    _need(len(ys) >= 1, "dy must be [..., N]")
     need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
     _need(not need_dx or w is not None, "dx needs w")
     _need(not need_dw or x is not None, "dw needs x")
     _need(need_dx or need_dw, "one of dx and dw must be needed")
+    di = dy.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_linear_bwd, di, stream, dy, x, w, need_dx=need_dx, need_dw=need_dw,
+                          dx=dx, dw=dw, dev_status=dev_status, workspace=workspace)
+    bf16, ys = torch.bfloat16, dy.shape
+    _need(len(ys) >= 1, "dy must be [..., N]")
     K = x.shape[-1] if x is not None else w.shape[-1]
     N, xs, ws = ys[-1], ys[:-1] + (K,), (ys[-1], K)
     yp = _like("dy", dy, bf16, ys, di)
     xp, wp = _opt_like("x", x, bf16, xs, di), _opt_like("w", w, bf16, ws, di)
     dxp, dwp = _opt_like("dx", dx, bf16, xs, di), _opt_like("dw", dw, bf16, ws, di)
-    M = dy.numel() // N if N else 0
-    lib, sp = _lib.load(), _status_ptr(dev_status, di)
-
-    def call(s):
-        ox = dx
-        if dx is None and need_dx:
-            ox = torch.empty(xs, dtype=bf16, device=dy.device)
-        ow = dw
-        if dw is None and need_dw:
-            ow = torch.empty(ws, dtype=bf16, device=dy.device)
-        wsp, wsb, _keep = _scratch(lib.rapt_linear_bwd_workspace_size(M, N, K), workspace, dy)
-        st = lib.rapt_linear_bwd(yp, xp, wp, M, N, K,
-                                 ox.data_ptr() if need_dx and dx is None else dxp,
-                                 ow.data_ptr() if need_dw and dw is None else dwp, sp, wsp, wsb, s)
-        if st:
-            _lib.check("rapt_linear_bwd", st)
-        return ox, ow
-
-    return _launch(di, stream, call)
+    M, lib = dy.numel() // N if N else 0, _lib.load()
+    if need_dx and dx is None:
+        dx = torch.empty(xs, dtype=bf16, device=dy.device)
+        dxp = dx.data_ptr()
+    if need_dw and dw is None:
+        dw = torch.empty(ws, dtype=bf16, device=dy.device)
+        dwp = dw.data_ptr()
+    wsp, wsb, owner = _scratch(lib.rapt_linear_bwd_workspace_size(M, N, K), workspace, dy)
+    st = lib.rapt_linear_bwd(yp, xp, wp, M, N, K, dxp, dwp, _status_ptr(dev_status, di), wsp, wsb,
+                             _handle(di))
+    if st:
+        _lib.check("rapt_linear_bwd", st)
+    return dx, dw
 
 
 def rapt_layer_fwd(x, w_qkv, w_o, gamma_q, gamma_k, *, heads, eps_norm=1e-6, rope_base=1e4,
