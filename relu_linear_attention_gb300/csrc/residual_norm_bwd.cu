@@ -1,5 +1,6 @@
 // Backward of the residual norm; the mathematics and the layout of the work are in residual_norm.cuh.
 #include "residual_norm.cuh"
+#include "tc_utils.cuh"
 
 namespace rapt {
 namespace {
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
     s = next;
   }
   if (a.part == nullptr) return;
+  tc::grid_launch_dependents();  // the sum over the CTAs may be made ready
   float* out = a.part + static_cast<long>(blockIdx.x) * 2 * D;
   if (slots == 1) {
     in.put_sums(out, gg);
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const GainGrads
   __shared__ float s[32][33];
   const int k = blockIdx.y, c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
+  tc::grid_dep_wait();  // the partials of the launch before this one
   if (c < a.D) {
 #pragma unroll 8
     for (int b = threadIdx.y; b < a.nparts; b += 32) v += a.part[(static_cast<long>(b) * 2 + k) * a.D + c];
@@ -236,9 +239,18 @@ cudaError_t launch_residual_norm_bwd(DType dt, const ResidualNormArgs& a, float*
   }
   if (dw_post == nullptr && dscale == nullptr && dw_pre == nullptr) return cudaSuccess;
   const GainGrads g{a.part, a.w_post, a.scale, dw_post, dscale, dw_pre, grid, a.D};
-  residual_norm_sum_kernel<<<dim3((a.D + 31) / 32, 2), dim3(32, 32), 0, stream>>>(g);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a.D + 31) / 32, 2);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.T > 0 ? 1 : 0;  // not before what another call launched
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, residual_norm_sum_kernel, g);
   note_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace rapt
