@@ -57,11 +57,13 @@ __device__ __forceinline__ Quad fma4(Quad a, Quad b, Quad c) {
 __device__ __forceinline__ float2 dot4(Quad a, Quad b, float2 s) { return fma2(a.p[1], b.p[1], fma2(a.p[0], b.p[0], s)); }
 
 // How rows lie: in 16-byte vectors; in 4-byte words (one fp32, two bf16); or (bf16 of odd D) with every
-// other row starting in the middle of a word.
+// other row starting in the middle of a word. A thread's rows are then all even or all odd (a launch has
+// an even number of CTAs), and on odd ones its words start one column earlier: column -1 is the row
+// before's, and not looked at.
 enum class Rows { Vec, Word, HalfWord };
 
 // Thread tx of a row's tpr owns 4 NC columns, as pieces of a vector or a word: piece i starts at column
-// (i tpr + tx) kPer, so that a warp's accesses are contiguous. RING false: no ring (the rows are too
+// (i tpr + tx) kPer - shift, so that a warp's accesses are contiguous. RING false: no ring (the rows are too
 // wide for one); what would be read there is read from the row itself.
 template <typename T, Rows R, int NC, bool RING>
 struct Cols {
@@ -69,28 +71,27 @@ struct Cols {
   static constexpr int kPer = kBytes / sizeof(T);             // columns of a piece
   static constexpr int kPieces = 4 * NC / kPer;
   static constexpr int kWords = kBytes / 4;
-  static constexpr int kCopies = R == Rows::HalfWord ? 2 : 1;  // ring places of a piece
-  int tx, tpr, D;
+  int tx, tpr, D, shift;
   uint32_t pitch;  // ring bytes of one piece of every thread
 
-  __device__ __forceinline__ Cols(int tx_, int tpr_, int D_)
-      : tx(tx_), tpr(tpr_), D(D_), pitch(blockDim.x * kBytes) {}
+  // row0: the first of this thread's rows.
+  __device__ __forceinline__ Cols(int tx_, int tpr_, int D_, long row0)
+      : tx(tx_), tpr(tpr_), D(D_), shift(R == Rows::HalfWord ? static_cast<int>(row0 & 1) : 0),
+        pitch(blockDim.x * kBytes) {}
   // Ring bytes of a thread in one stage of `tensors` rows. The threads' places lie side by side, piece
   // by piece: a warp's copies then arrive as whole lines (a thread's places together made the copies
   // 16-byte writes and the fp32 forward a third slower).
-  static __host__ __device__ constexpr int stride(int tensors) { return tensors * kPieces * kCopies * kBytes; }
-  __device__ __forceinline__ int col(int i) const { return (i * tpr + tx) * kPer; }
-  // Place `copy` of piece i of tensor slot k, given this thread's first place in a stage.
-  __device__ __forceinline__ uint8_t* at(uint8_t* stage, int k, int i, int copy) const {
-    return stage + ((k * kPieces + i) * kCopies + copy) * pitch;
-  }
+  static __host__ __device__ constexpr int stride(int tensors) { return tensors * kPieces * kBytes; }
+  __device__ __forceinline__ int col(int i) const { return (i * tpr + tx) * kPer - shift; }
+  // Place of piece i of tensor slot k, given this thread's first place in a stage.
+  __device__ __forceinline__ uint8_t* at(uint8_t* stage, int k, int i) const { return stage + (k * kPieces + i) * pitch; }
   // Zeros in a tensor slot that nothing is copied to.
   __device__ __forceinline__ void clear(uint8_t* stage, int k) const {
     if constexpr (RING) {
 #pragma unroll
-      for (int i = 0; i < kPieces * kCopies; ++i)
+      for (int i = 0; i < kPieces; ++i)
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) reinterpret_cast<uint32_t*>(at(stage, k, 0, i))[w] = 0;
+        for (int w = 0; w < kWords; ++w) reinterpret_cast<uint32_t*>(at(stage, k, i))[w] = 0;
     }
   }
   // Starts the copies of this thread's columns of the row at `row` into a tensor slot (columns past the
@@ -100,21 +101,16 @@ struct Cols {
     for (int i = 0; i < (RING ? kPieces : 0); ++i) {
       const int e = col(i);
       if (e >= D) continue;
-      const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(at(stage, k, i, 0)));
+      const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(at(stage, k, i)));
       if constexpr (R == Rows::Vec) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + e) : "memory");
       } else if constexpr (R == Rows::Word) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(row + e) : "memory");
       } else {
-        // the words that hold columns e and e + 1; of the second only its first half, and that only
-        // where the row starts in the middle of a word and has the column
-        const uintptr_t p = reinterpret_cast<uintptr_t>(row + e), word = p & ~uintptr_t{3};
-        const bool odd = (p & 2) != 0, pair = e + 1 < D, two = odd && pair;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(word), "r"(odd || pair ? 4 : 2)
-                     : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + pitch), "l"(two ? word + 4 : word),
-                     "r"(two ? 2 : 0)
-                     : "memory");
+        if (e + 1 < D)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(row + e) : "memory");
+        else  // the last column alone: what follows may be no one's
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, 2;" ::"r"(dst), "l"(row + e) : "memory");
       }
     }
   }
@@ -126,13 +122,10 @@ struct Cols {
       uint32_t w[kWords] = {};
       if constexpr (RING) {
         if constexpr (kBytes == 16) {
-          *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at(stage, k, i, 0));
+          *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at(stage, k, i));
         } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(at(stage, k, i, 0));
-          if constexpr (R == Rows::HalfWord) {
-            if ((reinterpret_cast<uintptr_t>(row) & 2) != 0)
-              w[0] = (w[0] >> 16) | (*reinterpret_cast<const uint32_t*>(at(stage, k, i, 1)) << 16);
-          }
+          w[0] = *reinterpret_cast<const uint32_t*>(at(stage, k, i));
+          if (R == Rows::HalfWord && i == 0 && col(0) < 0) w[0] &= 0xffff0000u;
         }
       } else {
         const int e = col(i);
@@ -144,7 +137,7 @@ struct Cols {
             w[0] = *reinterpret_cast<const uint32_t*>(p);
           } else {
             const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-            w[0] = h[0] | (e + 1 < D ? static_cast<uint32_t>(h[1]) << 16 : 0u);
+            w[0] = (e >= 0 ? h[0] : 0u) | (e + 1 < D ? static_cast<uint32_t>(h[1]) << 16 : 0u);
           }
         }
       }
@@ -184,8 +177,10 @@ struct Cols {
         *reinterpret_cast<uint4*>(row + e) = *reinterpret_cast<const uint4*>(b);
       } else if constexpr (R == Rows::Word) {
         *reinterpret_cast<__nv_bfloat162*>(row + e) = __floats2bfloat162_rn(q[0], q[1]);
+      } else if (e >= 0 && e + 1 < D) {
+        *reinterpret_cast<__nv_bfloat162*>(row + e) = __floats2bfloat162_rn(q[0], q[1]);
       } else {
-        row[e] = __float2bfloat16_rn(q[0]);
+        if (e >= 0) row[e] = __float2bfloat16_rn(q[0]);
         if (e + 1 < D) row[e + 1] = __float2bfloat16_rn(q[1]);
       }
     }
@@ -207,7 +202,7 @@ struct Cols {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const int e = col(i) + k;
-        v[i * kPer + k] = w != nullptr && e < D ? w[e] : 1.f;
+        v[i * kPer + k] = w != nullptr && e >= 0 && e < D ? w[e] : 1.f;
       }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -221,7 +216,7 @@ struct Cols {
     for (int i = 0; i < kPieces; ++i)
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
-        if (col(i) + k < D) row[col(i) + k] = v[i * kPer + k];
+        if (col(i) + k >= 0 && col(i) + k < D) row[col(i) + k] = v[i * kPer + k];
   }
 };
 
@@ -399,8 +394,9 @@ size_t ring_bytes(const RowShape& s, int stages, int tensors) {
   return static_cast<size_t>(stages) * Cols<T, R, NC, true>::stride(tensors) * s.threads;
 }
 
+// `even`: an even number of CTAs, where there is more than one.
 template <auto KERNEL>
-cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t smem, int most, int* grid,
+cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t smem, int most, bool even, int* grid,
                         cudaStream_t stream) {
   const long slots = s.threads / s.tpr, ctas = (a.T + slots - 1) / slots;
   int per_sm = 1, sms = 0, dev = 0;
@@ -416,6 +412,7 @@ cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t sme
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERNEL, s.threads, smem);
   if (e != cudaSuccess) return e;
   *grid = static_cast<int>(std::min<long>({ctas, static_cast<long>(sms) * std::max(1, per_sm), most}));
+  if (even && *grid > 1) *grid &= ~1;
   KERNEL<<<*grid, s.threads, smem, stream>>>(a, s.tpr);
   note_launches(1);
   return cudaGetLastError();

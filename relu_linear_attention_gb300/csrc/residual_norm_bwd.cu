@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
   int half = 0;
   const int tx = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, D = a.D;
   const float inv_d = 1.f / static_cast<float>(D);
-  const C in(tx, tpr, D);
+  const C in(tx, tpr, D, static_cast<long>(blockIdx.x) * slots + threadIdx.x / tpr);
   Quad ws[NC], wpre[NC];
   load_gains(a, in, ws, wpre);
   const bool post = a.w_post != nullptr, gated = a.gate != nullptr, joined = a.y != nullptr, normed = a.dh != nullptr;
@@ -195,7 +195,7 @@ cudaError_t go(const ResidualNormArgs& a, const RowShape& s, int* grid, cudaStre
   if constexpr (STAGES > 0 && NC > 2) {  // eight columns a thread always fit
     if (smem > kSmemMost) return go<T, R, NC, 0, MAXT, MINB>(a, s, grid, stream);
   }
-  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, max_parts(s), grid, stream);
+  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, max_parts(s), R == Rows::HalfWord, grid, stream);
 }
 // Stages of the ring: what lies in flight decides the rate, up to a point. bf16, % of the copy rate with
 // 2 / 3 / 4 stages: D = 256: 74 / 92 / 82, D = 2048 (two CTAs of 256 threads an SM): 60 / 80 / 78,

@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_fwd_kernel(const Res
   int half = 0;
   const int tx = threadIdx.x % tpr, slots = blockDim.x / tpr, D = a.D;
   const float inv_d = 1.f / static_cast<float>(D);
-  const C in(tx, tpr, D);
+  const C in(tx, tpr, D, static_cast<long>(blockIdx.x) * slots + threadIdx.x / tpr);
   Quad ws[NC], wpre[NC];
   load_gains(a, in, ws, wpre);
   const bool post = a.w_post != nullptr, gated = a.gate != nullptr, joined = a.y != nullptr;
@@ -95,7 +95,7 @@ cudaError_t go(const ResidualNormArgs& a, const RowShape& s, cudaStream_t stream
     if (smem > kSmemMost) return go<T, R, NC, 0, MAXT, MINB>(a, s, stream);
   }
   int grid = 0;
-  return launch_rows<residual_norm_fwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, 1 << 30, &grid, stream);
+  return launch_rows<residual_norm_fwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, 1 << 30, R == Rows::HalfWord, &grid, stream);
 }
 // Eight columns a thread up to D = 8192, then sixteen. Two stages of the ring for the narrow rows, three
 // for the wide ones where they fit: bf16, % of the copy rate with 2 / 3 / 4 stages: D = 256: 92 / 81 /
