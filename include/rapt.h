@@ -476,8 +476,8 @@ typedef enum rapt_act {
  *                    read before any of them is overwritten), but not the other.
  * All arithmetic is fp32; outputs are rounded once. Requirements: T >= 0 (0 does nothing; the
  * [T, D] pointers are not looked at),
- * 1 <= D <= 16384 (RAPT_ERR_UNSUPPORTED beyond), eps finite and > 0. Rows of any length are taken;
- * those of a multiple of 16 bytes are read and written 16 bytes at a time. A row depends on no other.
+ * 1 <= D <= 16384 (RAPT_ERR_UNSUPPORTED beyond), eps finite and > 0. Rows of any length are taken
+ * (the tensors themselves 16-byte aligned). A row depends on no other.
  */
 rapt_status rapt_residual_norm_fwd(const void* x, const void* y, const void* gate, rapt_dtype dtype,
                                    int32_t T, int32_t D, rapt_act act, const float* w_post,

@@ -88,7 +88,7 @@ rapt_status rapt_residual_norm_fwd(const void* x, const void* y, const void* gat
 
 size_t rapt_residual_norm_bwd_workspace_size(int32_t T, int32_t D, rapt_dtype dtype) {
   if (check_norm(dtype, T, D, RAPT_ACT_NONE, 1.f) != RAPT_OK) return 0;
-  return rapt::residual_norm_ws_bytes(T, D);
+  return rapt::residual_norm_ws_bytes(T, D, to_dt(dtype));
 }
 
 rapt_status rapt_residual_norm_bwd(const void* dr, const void* dh, const void* x, const void* y,
@@ -115,7 +115,7 @@ rapt_status rapt_residual_norm_bwd(const void* dr, const void* dh, const void* x
       aliases({dw_post, dscale, dw_pre}, {w_post, scale, w_pre}))
     return RAPT_ERR_INVALID_ARG;
   const bool sums = dw_post != nullptr || dscale != nullptr || dw_pre != nullptr;
-  const size_t need = sums ? rapt::residual_norm_ws_bytes(T, D) : 0;
+  const size_t need = sums ? rapt::residual_norm_ws_bytes(T, D, to_dt(dtype)) : 0;
   if (workspace_bytes < need || (need > 0 && (workspace == nullptr || off16(workspace)))) return RAPT_ERR_WORKSPACE;
   rapt::ResidualNormArgs a{};
   a.x = dh != nullptr ? x : nullptr;

@@ -334,7 +334,7 @@ struct ResidualNormArgs {
   float eps;
 };
 constexpr int kResidualNormMaxD = 16384;
-size_t residual_norm_ws_bytes(long T, int D);
+size_t residual_norm_ws_bytes(long T, int D, DType dt);
 cudaError_t launch_residual_norm_fwd(DType dt, const ResidualNormArgs& a, cudaStream_t stream);
 cudaError_t launch_residual_norm_bwd(DType dt, const ResidualNormArgs& a, float* dw_post, float* dscale,
                                      float* dw_pre, cudaStream_t stream);

@@ -36,7 +36,6 @@
 namespace rapt {
 namespace rn {
 
-
 // ---------------------------------------------------------------- two fp32 values per instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
@@ -56,93 +55,91 @@ __device__ __forceinline__ Quad fma4(Quad a, Quad b, Quad c) {
 // s + a . b, the two halves of a pair apart
 __device__ __forceinline__ float2 dot4(Quad a, Quad b, float2 s) { return fma2(a.p[1], b.p[1], fma2(a.p[0], b.p[0], s)); }
 
-// How rows lie: in 16-byte vectors; in 4-byte words (one fp32, two bf16); or (bf16 of odd D) with every
-// other row starting in the middle of a word. A thread's rows are then all even or all odd (a launch has
-// an even number of CTAs), and on odd ones its words start one column earlier: column -1 is the row
-// before's, and not looked at.
-enum class Rows { Vec, Word, HalfWord };
+// How rows lie: in whole 16-byte vectors, or (D not a multiple of a vector) starting somewhere inside
+// one. In the second case all rows of a thread start at the same place in a vector (a launch's rows of a
+// thread lie a multiple of a vector's elements apart), `shift` columns into it, and the thread's vectors
+// begin that much earlier: the first of a row holds the end of the row before, which is not looked at.
+// So every row moves in 16-byte pieces, and only a row's ends are stored otherwise. Forward / backward,
+// us, D = 1001, 128 MiB a tensor: bf16 151 / 286, fp32 109 / 198 (copies of a word each: 198 / 334 and
+// 153 / 219; D = 1000: 116 / 204 and 118 / 179).
+enum class Rows { Whole, Shifted };
 
-// Thread tx of a row's tpr owns 4 NC columns, as pieces of a vector or a word: piece i starts at column
-// (i tpr + tx) kPer - shift, so that a warp's accesses are contiguous. RING false: no ring (the rows are too
-// wide for one); what would be read there is read from the row itself.
+// Thread tx of a row's tpr owns 4 NC columns, as 16-byte pieces: piece i starts at column
+// (i tpr + tx) kPer - shift, so that a warp's accesses are contiguous. RING false: no ring (the rows are
+// too wide for one); what would be read there is read from the row itself. Rows are given by the address
+// of column 0.
 template <typename T, Rows R, int NC, bool RING>
 struct Cols {
-  static constexpr int kBytes = R == Rows::Vec ? 16 : 4;      // of a piece
-  static constexpr int kPer = kBytes / sizeof(T);             // columns of a piece
+  static constexpr int kBytes = 16;                // of a piece
+  static constexpr int kPer = kBytes / sizeof(T);  // columns of a piece
   static constexpr int kPieces = 4 * NC / kPer;
-  static constexpr int kWords = kBytes / 4;
   int tx, tpr, D, shift;
   uint32_t pitch;  // ring bytes of one piece of every thread
 
   // row0: the first of this thread's rows.
   __device__ __forceinline__ Cols(int tx_, int tpr_, int D_, long row0)
-      : tx(tx_), tpr(tpr_), D(D_), shift(R == Rows::HalfWord ? static_cast<int>(row0 & 1) : 0),
+      : tx(tx_), tpr(tpr_), D(D_), shift(R == Rows::Shifted ? static_cast<int>(row0 * D_ & (kPer - 1)) : 0),
         pitch(blockDim.x * kBytes) {}
   // Ring bytes of a thread in one stage of `tensors` rows. The threads' places lie side by side, piece
   // by piece: a warp's copies then arrive as whole lines (a thread's places together made the copies
   // 16-byte writes and the fp32 forward a third slower).
   static __host__ __device__ constexpr int stride(int tensors) { return tensors * kPieces * kBytes; }
   __device__ __forceinline__ int col(int i) const { return (i * tpr + tx) * kPer - shift; }
+  // Whether piece i lies in the row from end to end.
+  __device__ __forceinline__ bool whole(int i) const {
+    return R == Rows::Whole || (col(i) >= 0 && col(i) + kPer <= D);
+  }
+  __device__ __forceinline__ bool has(int e) const { return (R == Rows::Whole || e >= 0) && e < D; }
   // Place of piece i of tensor slot k, given this thread's first place in a stage.
   __device__ __forceinline__ uint8_t* at(uint8_t* stage, int k, int i) const { return stage + (k * kPieces + i) * pitch; }
   // Zeros in a tensor slot that nothing is copied to.
   __device__ __forceinline__ void clear(uint8_t* stage, int k) const {
     if constexpr (RING) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) reinterpret_cast<uint32_t*>(at(stage, k, i))[w] = 0;
+      for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(at(stage, k, i)) = make_uint4(0, 0, 0, 0);
     }
   }
-  // Starts the copies of this thread's columns of the row at `row` into a tensor slot (columns past the
-  // end keep the zeros of `clear`).
+  // Starts the copies of this thread's columns of a row into a tensor slot (columns past the end keep the
+  // zeros of `clear`).
   __device__ __forceinline__ void fetch(uint8_t* stage, int k, const T* row) const {
 #pragma unroll
     for (int i = 0; i < (RING ? kPieces : 0); ++i) {
       const int e = col(i);
       if (e >= D) continue;
       const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(at(stage, k, i)));
-      if constexpr (R == Rows::Vec) {
+      if (R == Rows::Whole || e + kPer <= D)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + e) : "memory");
-      } else if constexpr (R == Rows::Word) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(row + e) : "memory");
-      } else {
-        if (e + 1 < D)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(row + e) : "memory");
-        else  // the last column alone: what follows may be no one's
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, 2;" ::"r"(dst), "l"(row + e) : "memory");
-      }
+      else  // no further than the row: what follows the last one may be no one's
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(row + e),
+                     "r"((D - e) * static_cast<int>(sizeof(T)))
+                     : "memory");
     }
   }
-  // This thread's columns of the row at `row` (null: zeros), from its tensor slot.
+  // This thread's columns of a row (null: zeros), from its tensor slot; zeros where there is no column.
   __device__ __forceinline__ void read(uint8_t* stage, int k, const T* row, Quad (&f)[NC]) const {
     float v[4 * NC];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      uint32_t w[kWords] = {};
+      uint32_t w[4] = {};
+      const int e = col(i);
       if constexpr (RING) {
-        if constexpr (kBytes == 16) {
-          *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at(stage, k, i));
+        *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at(stage, k, i));
+      } else if (row != nullptr && e < D) {
+        if (whole(i)) {
+          *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(row + e);
         } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(at(stage, k, i));
-          if (R == Rows::HalfWord && i == 0 && col(0) < 0) w[0] &= 0xffff0000u;
-        }
-      } else {
-        const int e = col(i);
-        const T* p = row + e;
-        if (row != nullptr && e < D) {
-          if constexpr (kBytes == 16) {
-            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
-          } else if constexpr (R == Rows::Word) {
-            w[0] = *reinterpret_cast<const uint32_t*>(p);
-          } else {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-            w[0] = (e >= 0 ? h[0] : 0u) | (e + 1 < D ? static_cast<uint32_t>(h[1]) << 16 : 0u);
-          }
+#pragma unroll
+          for (int q = 0; q < kPer; ++q)
+            if (has(e + q)) {
+              if constexpr (sizeof(T) == 4)
+                w[q] = reinterpret_cast<const uint32_t*>(row)[e + q];
+              else
+                w[q / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[e + q]) << (16 * (q % 2));
+            }
         }
       }
 #pragma unroll
-      for (int q = 0; q < kWords; ++q) {
+      for (int q = 0; q < 4; ++q) {
         if constexpr (sizeof(T) == 4) {
           v[i * kPer + q] = __uint_as_float(w[q]);
         } else {
@@ -150,10 +147,22 @@ struct Cols {
           v[i * kPer + 2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
         }
       }
+      if (R == Rows::Shifted && RING && i == 0 && e < 0) {  // the end of the row before
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+          if (e + q < 0) v[q] = 0.f;
+      }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
       f[c] = {{make_float2(v[4 * c], v[4 * c + 1]), make_float2(v[4 * c + 2], v[4 * c + 3])}};
+  }
+  // q[k] without an address of its own.
+  static __device__ __forceinline__ float pick(const float* q, int k) {
+    float v = q[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) v = i == k ? q[i] : v;
+    return v;
   }
   // Stores this thread's columns to a row (none where it is null).
   __device__ __forceinline__ void write(T* row, const Quad (&f)[NC]) const {
@@ -165,23 +174,26 @@ struct Cols {
       const int e = col(i);
       if (e >= D) continue;
       const float* q = v + i * kPer;
-      if constexpr (sizeof(T) == 4) {
-        if constexpr (kPer == 4)
+      if (whole(i)) {
+        if constexpr (sizeof(T) == 4) {
           *reinterpret_cast<float4*>(row + e) = make_float4(q[0], q[1], q[2], q[3]);
-        else
-          row[e] = q[0];
-      } else if constexpr (kPer == 8) {
-        __nv_bfloat162 b[4];
+        } else {
+          __nv_bfloat162 b[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(q[2 * k], q[2 * k + 1]);
-        *reinterpret_cast<uint4*>(row + e) = *reinterpret_cast<const uint4*>(b);
-      } else if constexpr (R == Rows::Word) {
-        *reinterpret_cast<__nv_bfloat162*>(row + e) = __floats2bfloat162_rn(q[0], q[1]);
-      } else if (e >= 0 && e + 1 < D) {
-        *reinterpret_cast<__nv_bfloat162*>(row + e) = __floats2bfloat162_rn(q[0], q[1]);
-      } else {
-        if (e >= 0) row[e] = __float2bfloat16_rn(q[0]);
-        if (e + 1 < D) row[e + 1] = __float2bfloat16_rn(q[1]);
+          for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(q[2 * k], q[2 * k + 1]);
+          *reinterpret_cast<uint4*>(row + e) = *reinterpret_cast<const uint4*>(b);
+        }
+      } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (has(e + k)) row[e + k] = q[k];
+      } else {  // words, but for a first or last column that shares one with another row
+#pragma unroll
+        for (int k = 0; k < kPer; k += 2)
+          if (has(e + k) && has(e + k + 1))
+            *reinterpret_cast<__nv_bfloat162*>(row + e + k) = __floats2bfloat162_rn(q[k], q[k + 1]);
+        if (e < 0 && (e & 1)) row[0] = from_float<T>(pick(q, -e));
+        if (e + kPer > D && ((D - e) & 1)) row[D - 1] = from_float<T>(pick(q, D - 1 - e));
       }
     }
   }
@@ -202,7 +214,7 @@ struct Cols {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const int e = col(i) + k;
-        v[i * kPer + k] = w != nullptr && e >= 0 && e < D ? w[e] : 1.f;
+        v[i * kPer + k] = w != nullptr && has(e) ? w[e] : 1.f;
       }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -216,7 +228,7 @@ struct Cols {
     for (int i = 0; i < kPieces; ++i)
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
-        if (col(i) + k >= 0 && col(i) + k < D) row[col(i) + k] = v[i * kPer + k];
+        if (has(col(i) + k)) row[col(i) + k] = v[i * kPer + k];
   }
 };
 
@@ -366,22 +378,23 @@ __device__ __forceinline__ void load_gains(const ResidualNormArgs& a, const C& i
 
 constexpr int kFwdTensors = 3, kBwdTensors = 5;
 
-// Threads of a row (tpr: 8, 16 or 32 lanes of a warp, or a CTA of whole warps) and of a CTA, for EPT
-// columns a thread.
+// Threads of a row (tpr: 8, 16 or 32 lanes of a warp, or a CTA of whole warps) and of a CTA, for ept
+// columns a thread, where a row takes up to `more` columns of another one with it.
 struct RowShape {
   int tpr, threads;
 };
-inline RowShape row_shape(int D, int ept) {
-  const int need = (D + ept - 1) / ept;
+inline RowShape row_shape(int D, int ept, int more) {
+  const int need = (D + more + ept - 1) / ept;
   RowShape s;
   s.tpr = need <= 8 ? 8 : need <= 16 ? 16 : (need + 31) / 32 * 32;
   s.threads = s.tpr <= 32 ? 256 : s.tpr;
   return s;
 }
 // Columns a thread of the backward: eight up to 512 threads, then sixteen: a CTA of eight has too few
-// registers a thread beyond (D = 5120 in fp32: 242 us with eight, 204 with sixteen).
-inline int bwd_ept(int D) { return D <= 4096 ? 8 : 16; }
-inline RowShape bwd_shape(int D) { return row_shape(D, bwd_ept(D)); }
+// registers a thread beyond (D = 5120 in fp32: 242 us with eight, 204 with sixteen). Rows that take a few
+// columns of another one with them need twenty-four to fit 1024 threads at the widest.
+inline int bwd_ept(int D, int more) { return D + more <= 4096 ? 8 : more == 0 || D + more <= 8192 ? 16 : 24; }
+inline RowShape bwd_shape(int D, int more) { return row_shape(D, bwd_ept(D, more), more); }
 // CTAs of a backward launch at most (its registers hold an SM to 1024 threads): the workspace's rows
 // of partial sums.
 inline int max_parts(const RowShape& s) { return 160 * std::max(1, 1024 / s.threads); }
@@ -394,9 +407,9 @@ size_t ring_bytes(const RowShape& s, int stages, int tensors) {
   return static_cast<size_t>(stages) * Cols<T, R, NC, true>::stride(tensors) * s.threads;
 }
 
-// `even`: an even number of CTAs, where there is more than one.
+// `apart`: what the number of rows between a thread's rows is to be a multiple of.
 template <auto KERNEL>
-cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t smem, int most, bool even, int* grid,
+cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t smem, int most, int apart, int* grid,
                         cudaStream_t stream) {
   const long slots = s.threads / s.tpr, ctas = (a.T + slots - 1) / slots;
   int per_sm = 1, sms = 0, dev = 0;
@@ -412,17 +425,22 @@ cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t sme
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERNEL, s.threads, smem);
   if (e != cudaSuccess) return e;
   *grid = static_cast<int>(std::min<long>({ctas, static_cast<long>(sms) * std::max(1, per_sm), most}));
-  if (even && *grid > 1) *grid &= ~1;
+  if (slots == 1 && *grid < a.T)  // several slots are a multiple already
+    *grid = static_cast<int>(std::min<long>(a.T, std::max(*grid / apart, 1) * apart));
   KERNEL<<<*grid, s.threads, smem, stream>>>(a, s.tpr);
   note_launches(1);
   return cudaGetLastError();
 }
 
-// How the rows of a [T, D] tensor lie.
-inline Rows rows_of(DType dt, int D) {
-  if (D % (dt == DType::BF16 ? 8 : 4) == 0) return Rows::Vec;
-  return dt == DType::F32 || D % 2 == 0 ? Rows::Word : Rows::HalfWord;
+// How the rows of a [T, D] tensor lie, and the columns that one may take with it.
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+bool whole_rows(int D) {
+  return D % kVec<T> == 0;
 }
+template <typename T, Rows R>
+constexpr int kMore = R == Rows::Shifted ? kVec<T> - 1 : 0;
 
 }  // namespace rn
 }  // namespace rapt

@@ -195,28 +195,40 @@ cudaError_t go(const ResidualNormArgs& a, const RowShape& s, int* grid, cudaStre
   if constexpr (STAGES > 0 && NC > 2) {  // eight columns a thread always fit
     if (smem > kSmemMost) return go<T, R, NC, 0, MAXT, MINB>(a, s, grid, stream);
   }
-  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, max_parts(s), R == Rows::HalfWord, grid, stream);
+  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, max_parts(s), kMore<T, R> + 1,
+                                                                             grid, stream);
 }
 // Stages of the ring: what lies in flight decides the rate, up to a point. bf16, % of the copy rate with
 // 2 / 3 / 4 stages: D = 256: 74 / 92 / 82, D = 2048 (two CTAs of 256 threads an SM): 60 / 80 / 78,
-// D = 4096 (one of 512): 51 / - / 72. fp32 and split words fill the shared memory with two.
+// D = 4096 (one of 512): 51 / - / 72. fp32 fills the shared memory with two.
 template <typename T, Rows R>
 cudaError_t pick(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {
-  constexpr bool kNarrow = Cols<T, R, 2, true>::stride(1) == 16;  // ring bytes of eight columns
-  const RowShape s = bwd_shape(a.D);
-  if (bwd_ept(a.D) == 8) {
+  constexpr bool kNarrow = sizeof(T) == 2;
+  const RowShape s = bwd_shape(a.D, kMore<T, R>);
+  const int ept = bwd_ept(a.D, kMore<T, R>);
+  if (ept == 8) {
     if (s.threads <= 256) return go<T, R, 2, kNarrow ? 3 : 2, 256, 2>(a, s, grid, stream);
+    if constexpr (R == Rows::Shifted)  // nine warps twice an SM, at 96 registers a thread: D = 2047 462 -> 334 us
+      if (s.threads <= 288) return go<T, R, 2, kNarrow ? 3 : 2, 288, 2>(a, s, grid, stream);
     return go<T, R, 2, kNarrow ? 4 : 2, 512, 1>(a, s, grid, stream);
   }
-  if (s.threads <= 384) return go<T, R, 4, 2, 384, 1>(a, s, grid, stream);
-  if (s.threads <= 512) return go<T, R, 4, 2, 512, 1>(a, s, grid, stream);
-  return go<T, R, 4, 0, 1024, 1>(a, s, grid, stream);
+  if (ept == 16 && s.threads <= 384) return go<T, R, 4, 2, 384, 1>(a, s, grid, stream);
+  if (ept == 16 && s.threads <= 512) return go<T, R, 4, 2, 512, 1>(a, s, grid, stream);
+  if constexpr (R == Rows::Whole)
+    return go<T, R, 4, 0, 1024, 1>(a, s, grid, stream);
+  else
+    return go<T, R, 6, 0, 704, 1>(a, s, grid, stream);
+}
+template <typename T>
+cudaError_t pick_rows(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {
+  return whole_rows<T>(a.D) ? pick<T, Rows::Whole>(a, grid, stream) : pick<T, Rows::Shifted>(a, grid, stream);
 }
 
 }  // namespace
 
-size_t residual_norm_ws_bytes(long T, int D) {
-  const RowShape s = bwd_shape(D);
+size_t residual_norm_ws_bytes(long T, int D, DType dt) {
+  const int vec = dt == DType::F32 ? kVec<float> : kVec<__nv_bfloat16>;
+  const RowShape s = bwd_shape(D, D % vec == 0 ? 0 : vec - 1);
   const long slots = s.threads / s.tpr;
   return static_cast<size_t>(std::min<long>((T + slots - 1) / slots, max_parts(s))) * 2 * D * 4;
 }
@@ -225,16 +237,8 @@ cudaError_t launch_residual_norm_bwd(DType dt, const ResidualNormArgs& a, float*
                                      float* dw_pre, cudaStream_t stream) {
   int grid = 0;
   if (a.T > 0) {
-    const Rows r = rows_of(dt, a.D);
-    cudaError_t e;
-    if (dt == DType::F32)
-      e = r == Rows::Vec ? pick<float, Rows::Vec>(a, &grid, stream)
-                           : pick<float, Rows::Word>(a, &grid, stream);
-    else if (r == Rows::Vec)
-      e = pick<__nv_bfloat16, Rows::Vec>(a, &grid, stream);
-    else
-      e = r == Rows::Word ? pick<__nv_bfloat16, Rows::Word>(a, &grid, stream)
-                          : pick<__nv_bfloat16, Rows::HalfWord>(a, &grid, stream);
+    const cudaError_t e =
+        dt == DType::F32 ? pick_rows<float>(a, &grid, stream) : pick_rows<__nv_bfloat16>(a, &grid, stream);
     if (e != cudaSuccess) return e;
   }
   if (dw_post == nullptr && dscale == nullptr && dw_pre == nullptr) return cudaSuccess;

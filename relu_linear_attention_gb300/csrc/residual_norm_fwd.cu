@@ -95,31 +95,34 @@ cudaError_t go(const ResidualNormArgs& a, const RowShape& s, cudaStream_t stream
     if (smem > kSmemMost) return go<T, R, NC, 0, MAXT, MINB>(a, s, stream);
   }
   int grid = 0;
-  return launch_rows<residual_norm_fwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, 1 << 30, R == Rows::HalfWord, &grid, stream);
+  return launch_rows<residual_norm_fwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, 1 << 30, kMore<T, R> + 1,
+                                                                             &grid, stream);
 }
-// Eight columns a thread up to D = 8192, then sixteen. Two stages of the ring for the narrow rows, three
+// Eight columns a thread up to D = 8192, then sixteen, or twenty-four of rows that take a few columns of
+// another one with them (sixteen would need more than 1024 threads from D = 16378 on). Two stages of the ring for the narrow rows, three
 // for the wide ones where they fit: bf16, % of the copy rate with 2 / 3 / 4 stages: D = 256: 92 / 81 /
 // 79, D = 2048: 89 / 90 / 87, D = 4096: 88 / 92 / 90.
 template <typename T, Rows R>
 cudaError_t pick(const ResidualNormArgs& a, cudaStream_t stream) {
-  constexpr int kS = Cols<T, R, 2, true>::stride(1) == 16 ? 3 : 2;
-  const RowShape s = row_shape(a.D, a.D <= 8192 ? 8 : 16);
-  if (a.D > 8192) return go<T, R, 4, 2, 1024, 1>(a, s, stream);
+  constexpr int kS = sizeof(T) == 2 ? 3 : 2, kPlus = kMore<T, R>;
+  const bool eight = a.D + kPlus <= 8192;
+  constexpr int kWide = R == Rows::Whole ? 16 : 24;
+  const RowShape s = row_shape(a.D, eight ? 8 : kWide, kPlus);
+  if (!eight) return go<T, R, kWide / 4, 2, R == Rows::Whole ? 1024 : 704, 1>(a, s, stream);
   if (s.threads <= 256) return go<T, R, 2, 2, 256, 4>(a, s, stream);
   if (s.threads <= 512) return go<T, R, 2, kS, 512, 2>(a, s, stream);
   return go<T, R, 2, kS, 1024, 1>(a, s, stream);
+}
+template <typename T>
+cudaError_t pick_rows(const ResidualNormArgs& a, cudaStream_t stream) {
+  return whole_rows<T>(a.D) ? pick<T, Rows::Whole>(a, stream) : pick<T, Rows::Shifted>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_residual_norm_fwd(DType dt, const ResidualNormArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  const Rows r = rows_of(dt, a.D);
-  if (dt == DType::F32)
-    return r == Rows::Vec ? pick<float, Rows::Vec>(a, stream) : pick<float, Rows::Word>(a, stream);
-  if (r == Rows::Vec) return pick<__nv_bfloat16, Rows::Vec>(a, stream);
-  return r == Rows::Word ? pick<__nv_bfloat16, Rows::Word>(a, stream)
-                         : pick<__nv_bfloat16, Rows::HalfWord>(a, stream);
+  return dt == DType::F32 ? pick_rows<float>(a, stream) : pick_rows<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace rapt

@@ -195,3 +195,41 @@ def test_rows_past_32_bit_offsets(cuda_device, lib):
     _, h = R.rapt_residual_norm_fwd(x, w_pre=w)
     assert torch.equal(h[-4:], R.rapt_residual_norm_fwd(tail, w_pre=w)[1])
     assert not h[:-4].any()
+
+
+# Rows that start at different places of a 16-byte vector: a thread's rows have to start at the same one,
+# so that many more rows than CTAs (or rows of a CTA) are in question, and their neighbours' values.
+@pytest.mark.parametrize("T,D", [(9001, 1), (6001, 3), (5003, 65), (6001, 257), (3001, 1001), (1201, 1538), (701, 4093),
+                                 (353, 4099), (331, 8190), (331, 8195), (307, 16381)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows_of_odd_widths(cuda_device, lib, T, D, dtype):
+    kw, dr, dh = _inputs(T, D, dtype, T + D, cuda_device)
+    _check_fwd(kw, "silu", dtype)
+    got = _check_bwd(dr, dh, kw, "silu", dtype)
+    for a, b in zip(got, R.rapt_residual_norm_bwd(dr, dh, **kw, act="silu", eps=EPS)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,D", [(301, 257), (901, 1001), (170, 8195)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_row_leaves_its_neighbours(cuda_device, lib, T, D, dtype):
+    """NaN and infinite rows reach no other row, in place too: the pieces that rows share are split."""
+    kw, dr, dh = _inputs(T, D, dtype, 3, cuda_device)
+    r, h = R.rapt_residual_norm_fwd(**kw, act="gelu", eps=EPS)
+    grads = R.rapt_residual_norm_bwd(dr, dh, **kw, act="gelu", eps=EPS)[:3]
+    bad = torch.arange(1, T, 3, device=cuda_device)
+    rest = torch.ones(T, dtype=torch.bool, device=cuda_device)
+    rest[bad] = False
+    ill = {k: v.clone() if v.dim() == 2 else v for k, v in kw.items()}
+    for k in ("x", "y", "gate"):
+        ill[k][bad] = float("nan") if k != "y" else float("inf")
+    dri, dhi = dr.clone(), dh.clone()
+    dri[bad] = float("nan")
+    dhi[bad] = float("-inf")
+    gi = R.rapt_residual_norm_bwd(dri, dhi, **ill, act="gelu", eps=EPS)[:3]
+    for a, b in zip(grads, gi):
+        assert torch.equal(a[rest], b[rest])
+    ri, hi = R.rapt_residual_norm_fwd(**ill, act="gelu", eps=EPS, r=ill["x"], h=ill["y"])
+    assert ri.data_ptr() == ill["x"].data_ptr()
+    assert torch.equal(ri[rest], r[rest]) and torch.equal(hi[rest], h[rest])
+    assert torch.isnan(ri[bad]).all()
