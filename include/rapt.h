@@ -476,7 +476,7 @@ typedef enum rapt_act {
  *                    read before any of them is overwritten), but not the other.
  * All arithmetic is fp32; outputs are rounded once. Requirements: T >= 0 (0 does nothing; the
  * [T, D] pointers are not looked at),
- * 1 <= D <= 16384 (RAPT_ERR_UNSUPPORTED beyond), eps finite and > 0. Rows of any length are taken
+ * 1 <= D <= 16384 (RAPT_ERR_UNSUPPORTED beyond), eps a finite, normal float > 0. Rows of any length are taken
  * (the tensors themselves 16-byte aligned). A row depends on no other.
  */
 rapt_status rapt_residual_norm_fwd(const void* x, const void* y, const void* gate, rapt_dtype dtype,
@@ -511,8 +511,8 @@ rapt_status rapt_residual_norm_bwd(const void* dr, const void* dh, const void* x
  * product in one kernel (the down projection is a rapt_linear_fwd of h).
  *   x [M, K], w_gate, w_up [F, K] (a linear layer's weights), h [M, F], all bf16.
  * Tensor cores, fp32 accumulation; act and the product are formed in fp32 and rounded once.
- * Requirements: M >= 0 (0 does nothing), K % 8 == 0 and F % 8 == 0 (RAPT_ERR_UNSUPPORTED
- * otherwise); h must not alias an input. A row of h depends on the same row of x alone.
+ * Requirements: 0 <= M <= 2^26 (0 does nothing), K % 8 == 0 and F % 8 == 0 (RAPT_ERR_UNSUPPORTED
+ * otherwise), K and F at most 2^24, every matrix at most 2^38 elements; h must not alias an input. A row of h depends on the same row of x alone.
  * dev_status as for rapt_linear_fwd.
  */
 rapt_status rapt_glu_fwd(const void* x, const void* w_gate, const void* w_up, int32_t M, int32_t F,
@@ -540,7 +540,7 @@ rapt_status rapt_glu_bwd(const void* dh, const void* x, const void* w_gate, cons
  *   x may be NULL without dw, w without dx. dw is zeros for M = 0.
  *   workspace        rapt_linear_bwd_workspace_size() bytes, 16-byte aligned (may be 0).
  * Tensor cores, fp32 accumulation, results rounded once; long sums of few output tiles are split and
- * their fp32 parts added in a fixed order. Requirements: M >= 0, N % 8 == 0, K % 8 == 0; outputs
+ * their fp32 parts added in a fixed order. Requirements: sizes as for rapt_glu_fwd, with N for F; outputs
  * alias nothing. dev_status as for rapt_linear_fwd.
  */
 size_t rapt_linear_bwd_workspace_size(int32_t M, int32_t N, int32_t K);

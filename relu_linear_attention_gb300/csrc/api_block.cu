@@ -1,5 +1,6 @@
 // C ABI of the operators around the attention (declared in include/rapt.h): residual norms, gated
 // feed-forward, gradients of projections. Validation, workspace sizing and dispatch, as in api.cu.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -41,16 +42,19 @@ bool bad_status_word(const uint32_t* p) { return (reinterpret_cast<uintptr_t>(p)
 
 rapt_status check_norm(rapt_dtype dtype, int32_t T, int32_t D, rapt_act act, float eps) {
   if ((dtype != RAPT_F32 && dtype != RAPT_BF16) || !known_act(act)) return RAPT_ERR_UNSUPPORTED;
-  if (T < 0 || D < 1 || !std::isfinite(eps) || !(eps > 0.f)) return RAPT_ERR_INVALID_ARG;
+  // the root's instruction takes a subnormal for zero: a row of zeros would become NaN
+  if (T < 0 || D < 1 || !std::isfinite(eps) || !(eps >= FLT_MIN)) return RAPT_ERR_INVALID_ARG;
   if (D > rapt::kResidualNormMaxD) return RAPT_ERR_UNSUPPORTED;
   return RAPT_OK;
 }
 
-// M x N x K of a product in tiles: positive, rows of whole 16 bytes, and a count of tiles that
-// leaves room for the parts of a split sum in 31 bits.
+// M x N x K of a product in tiles: positive, rows of whole 16 bytes, a count of tiles that leaves room
+// for the parts of a split sum in 31 bits, and no tile whose sum takes longer than the kernel's waits (a
+// 64-deep slice of it takes 0.27 us: 2^26 are 0.3 s of 1 s).
 rapt_status check_gemm(int32_t M, int32_t N, int32_t K) {
   if (M < 0 || N < 1 || K < 1) return RAPT_ERR_INVALID_ARG;
   if (N % 8 != 0 || K % 8 != 0) return RAPT_ERR_UNSUPPORTED;
+  if (M > 1 << 26 || N > 1 << 24 || K > 1 << 24) return RAPT_ERR_INVALID_ARG;
   const long long most = 1LL << 38;  // 2^24 tiles of 128 x 128
   if (static_cast<long long>(M) * N > most || static_cast<long long>(M) * K > most ||
       static_cast<long long>(N) * K > most)

@@ -18,7 +18,7 @@ NAN, INF = float("nan"), float("inf")
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=2), UNSUP), (dict(act=5), UNSUP), (dict(act=-1), UNSUP), (dict(D=16385), UNSUP),
     (dict(T=-1), BAD), (dict(D=0), BAD), (dict(eps=0.0), BAD), (dict(eps=-1.0), BAD), (dict(eps=NAN), BAD),
-    (dict(eps=INF), BAD), (dict(x=None), BAD), (dict(r=None, h=None), BAD), (dict(w_pre=None), BAD),
+    (dict(eps=INF), BAD), (dict(eps=1e-39), BAD), (dict(x=None), BAD), (dict(r=None, h=None), BAD), (dict(w_pre=None), BAD),
     (dict(y=None), BAD), (dict(y=None, gate=None), BAD), (dict(y=None, gate=None, w_post=None), BAD),
     (dict(x=ODD), BAD), (dict(w_post=ODD), BAD), (dict(h=ODD), BAD), (dict(h=P[10]), BAD),
     (dict(T=0), OK), (dict(T=0, x=None, r=None, h=None), OK),
@@ -66,7 +66,8 @@ def test_workspace_queries(lib):
     (dict(M=-1), BAD), (dict(F=0), BAD), (dict(K=-8), BAD), (dict(F=60), UNSUP), (dict(K=20), UNSUP),
     (dict(act=5), UNSUP), (dict(x=None), BAD), (dict(wg=None), BAD), (dict(wu=None), BAD), (dict(h=None), BAD),
     (dict(x=ODD), BAD), (dict(h=ODD), BAD), (dict(h=P[1]), BAD), (dict(st=ctypes.c_void_p(0x7F0000001001)), BAD),
-    (dict(M=2 ** 31 - 1, F=2 ** 30), BAD), (dict(M=0), OK), (dict(M=0, x=None, h=None), OK),
+    (dict(M=2 ** 31 - 1, F=2 ** 30), BAD), (dict(K=2 ** 31 - 8), BAD), (dict(K=2 ** 24 + 8), BAD),
+    (dict(F=2 ** 24 + 8), BAD), (dict(M=2 ** 26 + 1), BAD), (dict(M=0), OK), (dict(M=0, x=None, h=None), OK),
 ])
 def test_glu_fwd_refuses(lib, kw, code):
     a = dict(x=P[0], wg=P[1], wu=P[2], M=4, F=64, K=64, act=1, h=P[3], st=None)
@@ -89,7 +90,7 @@ def test_glu_bwd_refuses(lib, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(M=-1), BAD), (dict(N=0), BAD), (dict(N=12), UNSUP), (dict(K=9), UNSUP), (dict(dy=None), BAD),
+    (dict(M=-1), BAD), (dict(N=0), BAD), (dict(M=2 ** 27, N=8, K=8), BAD), (dict(N=12), UNSUP), (dict(K=9), UNSUP), (dict(dy=None), BAD),
     (dict(x=None), BAD), (dict(w=None), BAD), (dict(dx=None, dw=None), BAD), (dict(dx=P[4]), BAD),
     (dict(dx=P[0]), BAD), (dict(dw=P[2]), BAD), (dict(dw=ODD), BAD), (dict(ws=None), WS), (dict(wsb=64), WS),
     (dict(st=ctypes.c_void_p(0x7F0000001002)), BAD),
