@@ -252,10 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::grid_launch_dependents();
   tc::grid_dep_wait();  // what the launch before this one in the same call wrote
 
+  tcp::Ring<kStages> ring;  // of the thread that loads, of the one that multiplies
   if (warp == 0) {
     if (lane == 0 && run) {  // TMA producer: this CTA's rows of A and its columns of B
       const uint32_t full0 = tcp::map_rank(bar_full, 0);
-      tcp::Ring<kStages> ring;
       bool ok = true;
       // one slice after another into the ring: load(stage, full barrier, slice) issues its copies
       const auto stream = [&](int k0, int k1, uint32_t bytes, const auto& load) {
@@ -318,7 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && run && rank == 0) {  // issuer of the products
-      tcp::Ring<kStages> ring;
       tcp::Ring<2> accs;
       bool ok = true;
       // the slices of one unit; A_MN: A is MN-major (Dw)
@@ -532,6 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (tid == 0 && rank == 0 && run && *s_abort) {  // given up: what is on its way to either CTA still lands
+    for (int s = 0; s < kStages; ++s) {
+      const uint32_t rounds = ring.round + (s < ring.s ? 1 : 0);
+      if (rounds > 0) tcp::wait(bar_full + 8 * s, (rounds - 1) & 1, kWait);
+    }
+  }
+  __syncwarp();
   tcp::cluster_sync();  // no CTA leaves while the other may still signal it
   if (*s_abort && tid == 0 && a.dev_status != nullptr) atomicOr(a.dev_status, 2u);
   tc::fence_after_sync();
@@ -645,7 +651,7 @@ Plan plan_width(int rows, int cols, int products, int nk, int width, int full, b
   const double bytes = static_cast<double>(pairs + left) * kPairRows * width * 8;
   const double cost = static_cast<double>(p.tiles / kWorkers) * (nk * share + kUnit) + span * share + 2 * kUnit +
                       kSumLaunch + bytes / 9000.0 / 270.0;
-  if (cost < p.cost) {
+  if (cost < p.cost) {  // then nk > span: a share spans two tiles at most
     p.direct = p.tiles - left;
     p.span = span;
     p.padded = padded;
