@@ -10,8 +10,8 @@
 //     dn = s a g,  dw_post = sum_rows dn yh,  u = w_post dn,  dy = sg (u - yh mean(u yh))
 // where mean(t rh) = rho mean(t r): the two sums over r need no rho, so they share one reduction.
 //
-// HBM bound: the forward moves 5 tensors, the backward 8, each once. A CTA takes a row at a time (or,
-// below 257 columns, 8 to 32 lanes take one) and keeps the rows ahead of it in flight in a ring in
+// HBM bound: the forward moves 5 tensors, the backward 8, each once. A CTA takes a row at a time (or 8 to
+// 32 lanes take a narrow one) and keeps the rows ahead of it in flight in a ring in
 // shared memory; each thread copies and reads only its own columns there, so the ring needs no
 // barrier. What is missing (columns past the row's end, rows past the last, absent tensors) is zeros
 // in the ring, so the arithmetic has no branches. The sums of a row are one reduction: beside r's own
@@ -381,20 +381,29 @@ constexpr int kFwdTensors = 3, kBwdTensors = 5;
 // Threads of a row (tpr: 8, 16 or 32 lanes of a warp, or a CTA of whole warps) and of a CTA, for ept
 // columns a thread, where a row takes up to `more` columns of another one with it.
 struct RowShape {
-  int tpr, threads;
+  int ept, tpr, threads;
 };
 inline RowShape row_shape(int D, int ept, int more) {
   const int need = (D + more + ept - 1) / ept;
   RowShape s;
+  s.ept = ept;
   s.tpr = need <= 8 ? 8 : need <= 16 ? 16 : (need + 31) / 32 * 32;
-  s.threads = s.tpr <= 32 ? 256 : s.tpr;
+  s.threads = s.tpr > 32 ? s.tpr : ept == 8 ? 256 : 128;
   return s;
 }
-// Columns a thread of the backward: eight up to 512 threads, then sixteen: a CTA of eight has too few
-// registers a thread beyond (D = 5120 in fp32: 242 us with eight, 204 with sixteen). Rows that take a few
-// columns of another one with them need twenty-four to fit 1024 threads at the widest.
-inline int bwd_ept(int D, int more) { return D + more <= 4096 ? 8 : more == 0 || D + more <= 8192 ? 16 : 24; }
-inline RowShape bwd_shape(int D, int more) { return row_shape(D, bwd_ept(D, more), more); }
+// Columns a thread of the backward: as many as keep a CTA at 512 threads, for their registers (D = 5120
+// in fp32: 242 us with eight, 204 with sixteen); the widest rows that are no whole vectors take 704 of
+// twenty-four (bf16, D = 16383: 1050 us, 1150 with thirty-two). bf16 takes sixteen from 257 to 2048, too, where that
+// leaves few lanes idle or a row to a warp: fewer instructions a value (D = 2048: 197 -> 186 us).
+inline RowShape bwd_shape(int D, int more, bool f32) {
+  const int n = D + more;
+  const RowShape s16 = row_shape(D, 16, more);
+  if (n <= 4096) {
+    const bool fits = n > 256 && n <= 2048 && (s16.tpr == 32 || (more == 0 && s16.tpr * 16 * 7 <= n * 8));
+    return !f32 && fits ? s16 : row_shape(D, 8, more);
+  }
+  return n <= 8192 ? s16 : row_shape(D, n <= 12288 || more > 0 ? 24 : 32, more);
+}
 // CTAs of a backward launch at most (its registers hold an SM to 1024 threads): the workspace's rows
 // of partial sums.
 inline int max_parts(const RowShape& s) { return 160 * std::max(1, 1024 / s.threads); }
@@ -425,8 +434,8 @@ cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t sme
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERNEL, s.threads, smem);
   if (e != cudaSuccess) return e;
   *grid = static_cast<int>(std::min<long>({ctas, static_cast<long>(sms) * std::max(1, per_sm), most}));
-  if (slots == 1 && *grid < a.T)  // several slots are a multiple already
-    *grid = static_cast<int>(std::min<long>(a.T, std::max(*grid / apart, 1) * apart));
+  const int unit = static_cast<int>(std::max<long>(apart / slots, 1));  // both powers of two
+  if (*grid < ctas) *grid = static_cast<int>(std::min<long>(ctas, std::max(*grid / unit, 1) * unit));
   KERNEL<<<*grid, s.threads, smem, stream>>>(a, s.tpr);
   note_launches(1);
   return cudaGetLastError();

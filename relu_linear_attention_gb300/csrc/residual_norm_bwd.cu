@@ -8,7 +8,7 @@ namespace {
 using namespace rn;
 
 // Partial column sums of CTA b at part[(b * 2 + k) * D + column], k = 0: G, 1: dw_pre.
-template <typename T, Rows R, int NC, int STAGES, int MAXT, int MINB>
+template <typename T, Rows R, int NC, int STAGES, bool AHEAD, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const ResidualNormArgs a, int tpr) {
   using C = Cols<T, R, NC, (STAGES > 0)>;
   __shared__ __align__(16) float red[2][32][8];
@@ -25,70 +25,101 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
   for (int c = 0; c < NC; ++c) gg[c] = gpre[c] = quad(0.f);
   const long step = static_cast<long>(gridDim.x) * slots, step_off = step * D;
   long row = static_cast<long>(blockIdx.x) * slots + slot, off = row * D;
+  // the ring: STAGES rows of dh, x, gate, dr and y; AHEAD: y apart, and a row further ahead than the
+  // others, so that no row but the one in question has to have arrived
+  constexpr bool kEarly = STAGES == 1;  // x and gate of the next row are fetched when this one's are read
+  constexpr int kYSlot = AHEAD ? 0 : 4;
   uint8_t* const mine = ring + threadIdx.x * C::kBytes;
-  const uint32_t stage_bytes = blockDim.x * C::stride(kBwdTensors);
+  const uint32_t stage_bytes = blockDim.x * C::stride(AHEAD ? 4 : 5), y_bytes = blockDim.x * C::stride(1);
+  uint8_t* const mine_y = mine + (AHEAD ? STAGES * stage_bytes : 0);
   const auto at = [&](const void* t, long o, bool live) { return t != nullptr && live ? static_cast<const T*>(t) + o : nullptr; };
-  // tensor slots of a stage: dh, x, y, gate, dr
-  const auto fetch = [&](uint8_t* st, long rw, long o) {
+  // tensor slots of a stage: dh, dr, x, gate (, y); x and gate are read before the reduction only
+  const auto fetch_early = [&](uint8_t* st, long rw, long o) {
+    if (rw < a.T) {
+      if (normed) in.fetch(st, 2, static_cast<const T*>(a.x) + o);
+      if (gated) in.fetch(st, 3, static_cast<const T*>(a.gate) + o);
+    } else {
+      in.clear(st, 2);
+      in.clear(st, 3);
+    }
+  };
+  const auto fetch_y = [&](uint8_t* st, long rw, long o) {
+    if (rw >= a.T)
+      in.clear(st, 0);
+    else if (joined)
+      in.fetch(st, 0, static_cast<const T*>(a.y) + o);
+  };
+  const auto fetch = [&](uint8_t* st, uint8_t* st_y, long rw, long o) {
     if (rw < a.T) {
       if (normed) {
         in.fetch(st, 0, static_cast<const T*>(a.dh) + o);
-        in.fetch(st, 1, static_cast<const T*>(a.x) + o);
+        if (!kEarly) in.fetch(st, 2, static_cast<const T*>(a.x) + o);
       }
-      if (joined) in.fetch(st, 2, static_cast<const T*>(a.y) + o);
-      if (gated) in.fetch(st, 3, static_cast<const T*>(a.gate) + o);
-      if (a.dr != nullptr) in.fetch(st, 4, static_cast<const T*>(a.dr) + o);
+      if (!AHEAD && joined) in.fetch(st, 4, static_cast<const T*>(a.y) + o);
+      if (!kEarly && gated) in.fetch(st, 3, static_cast<const T*>(a.gate) + o);
+      if (a.dr != nullptr) in.fetch(st, 1, static_cast<const T*>(a.dr) + o);
     } else {
 #pragma unroll
-      for (int k = 0; k < kBwdTensors; ++k) in.clear(st, k);
+      for (int k = 0; k < (AHEAD ? 4 : 5); ++k)
+        if (!kEarly || k < 2) in.clear(st, k);
     }
+    if (AHEAD) fetch_y(st_y, rw + step, o + step_off);
     commit_copies();
   };
   const auto y_square = [&](uint8_t* st, const T* y_row) {
     Quad y[NC];
-    in.read(st, 2, y_row, y);
+    in.read(st, kYSlot, y_row, y);
     float2 q = both(0.f);
 #pragma unroll
     for (int c = 0; c < NC; ++c) q = dot4(y[c], y[c], q);
     return q.x + q.y;
   };
+  if constexpr (AHEAD) {
+    in.clear(mine_y, 0);
+    fetch_y(mine_y, row, off);
+  }
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) {
+    const long rw = row + s * step, o = off + s * step_off;
 #pragma unroll
-    for (int k = 0; k < kBwdTensors; ++k) in.clear(mine + s * stage_bytes, k);
-    fetch(mine + s * stage_bytes, row + s * step, off + s * step_off);
+    for (int k = 0; k < (AHEAD ? 4 : 5); ++k) in.clear(mine + s * stage_bytes, k);
+    if (AHEAD) in.clear(mine_y + (s + 1) * y_bytes, 0);
+    if (kEarly) fetch_early(mine + s * stage_bytes, rw, o);
+    fetch(mine + s * stage_bytes, mine_y + (s + 1) * y_bytes, rw, o);
   }
   float sg = 1.f;
   if (post) {
     wait_copies<STAGES - 1>();
-    float q[1] = {y_square(mine, at(a.y, off, row < a.T))};
+    float q[1] = {y_square(mine_y, at(a.y, off, row < a.T))};
     row_sum<1>(q, tpr, red, half);
     sg = inv_root(fmaf(q[0], inv_d, a.eps));
   }
-  uint32_t s = 0;  // offset of the stage
+  uint32_t s = 0, sy = 0;  // offsets of the stage and, AHEAD, of the row's y
   // the rows of a warp end together: those past T are zeros and not stored
   for (long first = static_cast<long>(blockIdx.x) * slots; first < a.T;
        first += step, row += step, off += step_off) {
     const bool live = row < a.T;
     const uint32_t next = s + stage_bytes == STAGES * stage_bytes ? 0 : s + stage_bytes;
-    uint8_t* const st = mine + s;
-    wait_copies<STAGES - 2>();  // this row and the next
+    const uint32_t next_y = sy == STAGES * y_bytes ? 0 : sy + y_bytes;
+    uint8_t *const st = mine + s, *const st_y = AHEAD ? mine_y + sy : st;
+    wait_copies<STAGES - 2 + AHEAD>();  // this row and the next one's y
     Quad r[NC], av[NC], da[NC];  // x + e, act(z), act'(z): kept over the reduction
     float q[6];
     {
       Quad e[NC], t[NC], d[NC];
       if (gated) in.read(st, 3, at(a.gate, off, live), t);
       act_cols<true>(gated, a.act, t, av, da);
-      in.read(st, 2, at(a.y, off, live), e);
-      in.read(st, 1, at(normed ? a.x : nullptr, off, live), r);
-  #pragma unroll
+      in.read(st_y, kYSlot, at(a.y, off, live), e);
+      in.read(st, 2, at(normed ? a.x : nullptr, off, live), r);
+      if (kEarly) fetch_early(st, row + step, off + step_off);
+#pragma unroll
       for (int c = 0; c < NC; ++c) {
         e[c] = e[c] * sg * ws[c] * av[c];
         r[c] = fma4(e[c], quad(1.f), r[c]);
       }
       in.read(st, 0, at(a.dh, off, live), t);
-      in.read(st, 4, at(a.dr, off, live), d);
-        float2 rr = both(0.f), tr = rr, ed = rr, et = rr, er = rr;
+      in.read(st, 1, at(a.dr, off, live), d);
+      float2 rr = both(0.f), tr = rr, ed = rr, et = rr, er = rr;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         t[c] = t[c] * wpre[c];
@@ -104,15 +135,15 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
       q[3] = et.x + et.y;
       q[4] = er.x + er.y;
     }
-    q[5] = post ? y_square(mine + next, at(a.y, off + step_off, row + step < a.T)) : 0.f;
+    q[5] = post ? y_square(AHEAD ? mine_y + next_y : mine + next, at(a.y, off + step_off, row + step < a.T)) : 0.f;
     row_sum<6>(q, tpr, red, half);
     const float rho = normed ? inv_root(fmaf(q[0], inv_d, a.eps)) : 0.f;
     const float m = rho * q[1] * inv_d;                                            // mean(t rh)
     const float my = post ? inv_d * (q[2] + rho * (q[3] - rho * m * q[4])) : 0.f;  // mean(u yh)
     Quad g[NC], y[NC], t[NC];
-    in.read(st, 4, at(a.dr, off, live), g);
+    in.read(st, 1, at(a.dr, off, live), g);
     in.read(st, 0, at(a.dh, off, live), t);
-    in.read(st, 2, at(a.y, off, live), y);
+    in.read(st_y, kYSlot, at(a.y, off, live), y);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const Quad rh = r[c] * rho;
@@ -130,9 +161,10 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
     }
     in.write(a.dgate != nullptr && live ? static_cast<T*>(a.dgate) + off : nullptr, da);
     in.write(a.dy != nullptr && live ? static_cast<T*>(a.dy) + off : nullptr, g);
-    fetch(st, row + STAGES * step, off + STAGES * step_off);
+    if (STAGES > 0) fetch(st, st_y, row + STAGES * step, off + STAGES * step_off);
     if (post) sg = inv_root(fmaf(q[5], inv_d, a.eps));
     s = next;
+    sy = next_y;
   }
   if (a.part == nullptr) return;
   tc::grid_launch_dependents();  // the sum over the CTAs may be made ready
@@ -187,37 +219,46 @@ __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const GainGrads
   if (a.dscale != nullptr) a.dscale[c] = a.w_post != nullptr ? a.w_post[c] * t : t;
 }
 
-template <typename T, Rows R, int NC, int STAGES, int MAXT, int MINB>
+// A ring that does not fit becomes a shorter one.
+template <typename T, Rows R, int NC, int STAGES, bool AHEAD, int MAXT, int MINB>
 cudaError_t go(const ResidualNormArgs& a, const RowShape& s, int* grid, cudaStream_t stream) {
-  size_t smem = ring_bytes<T, R, NC>(s, STAGES, kBwdTensors);
+  size_t smem = ring_bytes<T, R, NC>(s, STAGES, kBwdTensors) + (AHEAD ? ring_bytes<T, R, NC>(s, 1, 1) : 0);
   // the slots' column sums meet where the ring was
   if (s.tpr <= 32) smem = std::max(smem, static_cast<size_t>(s.threads / s.tpr) * 2 * a.D * 4);
-  if constexpr (STAGES > 0 && NC > 2) {  // eight columns a thread always fit
-    if (smem > kSmemMost) return go<T, R, NC, 0, MAXT, MINB>(a, s, grid, stream);
+  constexpr bool kF32 = sizeof(T) == 4;
+  if constexpr (NC == 6 && STAGES == 2 || kF32 && NC == 4 && STAGES == 2) {
+    if (smem > kSmemMost) return go<T, R, NC, 1, true, MAXT, MINB>(a, s, grid, stream);
+  } else if constexpr (kF32 && NC == 6 && STAGES == 1) {
+    if (smem > kSmemMost) return go<T, R, NC, 0, false, MAXT, MINB>(a, s, grid, stream);
   }
-  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, MAXT, MINB>>(a, s, smem, max_parts(s), kMore<T, R> + 1,
-                                                                             grid, stream);
+  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, AHEAD, MAXT, MINB>>(a, s, smem, max_parts(s),
+                                                                                    kMore<T, R> + 1, grid, stream);
 }
-// Stages of the ring: what lies in flight decides the rate, up to a point. bf16, % of the copy rate with
-// 2 / 3 / 4 stages: D = 256: 74 / 92 / 82, D = 2048 (two CTAs of 256 threads an SM): 60 / 80 / 78,
-// D = 4096 (one of 512): 51 / - / 72. fp32 fills the shared memory with two.
+// Columns a thread, and the ring. us of 128 MiB a tensor, the best choices (columns a thread / stages,
+// + where y is ahead) and what they were taken for:
+//   bf16  D = 2560: 8/4 two CTAs an SM 197, one 269;  5120: 16/3 229, 16/2 314;  6144: 16/3 210, 16/2 282;
+//         8192: 16/2 315, 32/1+ 326, 16/1+ 333;  12288: 24/1+ 447, 16 without a ring 683
+//   fp32  D = 2560: 8/2+ two CTAs an SM 173, 8/2 one 256;  4096: 8/2+ 190, 8/2 202;  5120: 16/2+ 200,
+//         16/2 204;  6144: 16/1+ 210, 16 without a ring 305;  8192: 16/1+ 258, without 299;
+//         12288: 24 without a ring 421, 16 without 544
 template <typename T, Rows R>
 cudaError_t pick(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {
-  constexpr bool kNarrow = sizeof(T) == 2;
-  const RowShape s = bwd_shape(a.D, kMore<T, R>);
-  const int ept = bwd_ept(a.D, kMore<T, R>);
-  if (ept == 8) {
-    if (s.threads <= 256) return go<T, R, 2, kNarrow ? 3 : 2, 256, 2>(a, s, grid, stream);
-    if constexpr (R == Rows::Shifted)  // nine warps twice an SM, at 96 registers a thread: D = 2047 462 -> 334 us
-      if (s.threads <= 288) return go<T, R, 2, kNarrow ? 3 : 2, 288, 2>(a, s, grid, stream);
-    return go<T, R, 2, kNarrow ? 4 : 2, 512, 1>(a, s, grid, stream);
+  constexpr bool kF32 = sizeof(T) == 4;
+  const RowShape s = bwd_shape(a.D, kMore<T, R>, kF32);
+  if (s.ept == 8) {
+    if (s.threads <= 256) return go<T, R, 2, kF32 ? 2 : 3, false, 256, 2>(a, s, grid, stream);
+    if (s.threads <= 320) return go<T, R, 2, kF32 ? 2 : 4, kF32, 320, 2>(a, s, grid, stream);
+    return go<T, R, 2, kF32 ? 2 : 4, kF32, 512, 1>(a, s, grid, stream);
   }
-  if (ept == 16 && s.threads <= 384) return go<T, R, 4, 2, 384, 1>(a, s, grid, stream);
-  if (ept == 16 && s.threads <= 512) return go<T, R, 4, 2, 512, 1>(a, s, grid, stream);
+  if constexpr (!kF32)
+    if (s.ept == 16 && s.threads <= 128) return go<T, R, 4, 3, false, 128, 3>(a, s, grid, stream);
+  if (s.ept == 16 && s.threads <= 384) return go<T, R, 4, kF32 ? 2 : 3, kF32, 384, 1>(a, s, grid, stream);
+  if (s.ept == 16) return go<T, R, 4, kF32 ? 1 : 2, kF32, 512, 1>(a, s, grid, stream);
+  if (s.ept == 24 && s.threads <= 512) return go<T, R, 6, kF32 ? 1 : 2, kF32, 512, 1>(a, s, grid, stream);
   if constexpr (R == Rows::Whole)
-    return go<T, R, 4, 0, 1024, 1>(a, s, grid, stream);
+    return go<T, R, 8, kF32 ? 0 : 1, !kF32, 512, 1>(a, s, grid, stream);
   else
-    return go<T, R, 6, 0, 704, 1>(a, s, grid, stream);
+    return go<T, R, 6, kF32 ? 0 : 1, !kF32, 704, 1>(a, s, grid, stream);
 }
 template <typename T>
 cudaError_t pick_rows(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {
@@ -228,7 +269,7 @@ cudaError_t pick_rows(const ResidualNormArgs& a, int* grid, cudaStream_t stream)
 
 size_t residual_norm_ws_bytes(long T, int D, DType dt) {
   const int vec = dt == DType::F32 ? kVec<float> : kVec<__nv_bfloat16>;
-  const RowShape s = bwd_shape(D, D % vec == 0 ? 0 : vec - 1);
+  const RowShape s = bwd_shape(D, D % vec == 0 ? 0 : vec - 1, dt == DType::F32);
   const long slots = s.threads / s.tpr;
   return static_cast<size_t>(std::min<long>((T + slots - 1) / slots, max_parts(s))) * 2 * D * 4;
 }
