@@ -55,13 +55,19 @@ __device__ __forceinline__ Quad fma4(Quad a, Quad b, Quad c) {
 // s + a . b, the two halves of a pair apart
 __device__ __forceinline__ float2 dot4(Quad a, Quad b, float2 s) { return fma2(a.p[1], b.p[1], fma2(a.p[0], b.p[0], s)); }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // How rows lie: in whole 16-byte vectors, or (D not a multiple of a vector) starting somewhere inside
 // one. In the second case all rows of a thread start at the same place in a vector (a launch's rows of a
 // thread lie a multiple of a vector's elements apart), `shift` columns into it, and the thread's vectors
 // begin that much earlier: the first of a row holds the end of the row before, which is not looked at.
 // So every row moves in 16-byte pieces, and only a row's ends are stored otherwise. Forward / backward,
-// us, D = 1001, 128 MiB a tensor: bf16 151 / 286, fp32 109 / 198 (copies of a word each: 198 / 334 and
-// 153 / 219; D = 1000: 116 / 204 and 118 / 179).
+// us, D = 1001, 128 MiB a tensor: bf16 132 / 266, fp32 121 / 197 (copies of a word each: 198 / 334 and
+// 153 / 219; D = 1000: 116 / 197 and 118 / 178). Where a row is only part of a warp every warp has ends to
+// store: bf16, D = 65: 311 / 497.
 enum class Rows { Whole, Shifted };
 
 // Thread tx of a row's tpr owns 4 NC columns, as 16-byte pieces: piece i starts at column
@@ -74,12 +80,22 @@ struct Cols {
   static constexpr int kPer = kBytes / sizeof(T);  // columns of a piece
   static constexpr int kPieces = 4 * NC / kPer;
   int tx, tpr, D, shift;
-  uint32_t pitch;  // ring bytes of one piece of every thread
+  uint32_t pitch;    // ring bytes of one piece of every thread
+  // bf16, few columns a thread: the bits of the first piece that are this row's (elsewhere four more
+  // registers cost more than what they save)
+  static constexpr bool kMasks = R == Rows::Shifted && sizeof(T) == 2 && NC == 2;
+  uint32_t head[4];
 
   // row0: the first of this thread's rows.
   __device__ __forceinline__ Cols(int tx_, int tpr_, int D_, long row0)
       : tx(tx_), tpr(tpr_), D(D_), shift(R == Rows::Shifted ? static_cast<int>(row0 * D_ & (kPer - 1)) : 0),
-        pitch(blockDim.x * kBytes) {}
+        pitch(blockDim.x * kBytes) {
+#pragma unroll
+    for (int q = 0; q < (kMasks ? 4 : 0); ++q) {
+      const int e = col(0) + 2 * q;
+      head[q] = e >= 0 ? ~0u : e == -1 ? 0xffff0000u : 0u;
+    }
+  }
   // Ring bytes of a thread in one stage of `tensors` rows. The threads' places lie side by side, piece
   // by piece: a warp's copies then arrive as whole lines (a thread's places together made the copies
   // 16-byte writes and the fp32 forward a third slower).
@@ -89,7 +105,7 @@ struct Cols {
   __device__ __forceinline__ bool whole(int i) const {
     return R == Rows::Whole || (col(i) >= 0 && col(i) + kPer <= D);
   }
-  __device__ __forceinline__ bool has(int e) const { return (R == Rows::Whole || e >= 0) && e < D; }
+  __device__ __forceinline__ bool has(int e) const { return static_cast<unsigned>(e) < static_cast<unsigned>(D); }
   // Place of piece i of tensor slot k, given this thread's first place in a stage.
   __device__ __forceinline__ uint8_t* at(uint8_t* stage, int k, int i) const { return stage + (k * kPieces + i) * pitch; }
   // Zeros in a tensor slot that nothing is copied to.
@@ -124,6 +140,18 @@ struct Cols {
       const int e = col(i);
       if constexpr (RING) {
         *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at(stage, k, i));
+        if (R == Rows::Shifted && i == 0) {  // not the end of the row before
+          if constexpr (kMasks) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] &= head[q];
+          } else if (e < 0) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int c = e + q * kPer / 4;
+              w[q] = c >= 0 ? w[q] : sizeof(T) == 2 && c == -1 ? w[q] & 0xffff0000u : 0u;
+            }
+          }
+        }
       } else if (row != nullptr && e < D) {
         if (whole(i)) {
           *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(row + e);
@@ -147,22 +175,10 @@ struct Cols {
           v[i * kPer + 2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
         }
       }
-      if (R == Rows::Shifted && RING && i == 0 && e < 0) {  // the end of the row before
-#pragma unroll
-        for (int q = 0; q < kPer; ++q)
-          if (e + q < 0) v[q] = 0.f;
-      }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
       f[c] = {{make_float2(v[4 * c], v[4 * c + 1]), make_float2(v[4 * c + 2], v[4 * c + 3])}};
-  }
-  // q[k] without an address of its own.
-  static __device__ __forceinline__ float pick(const float* q, int k) {
-    float v = q[0];
-#pragma unroll
-    for (int i = 1; i < kPer; ++i) v = i == k ? q[i] : v;
-    return v;
   }
   // Stores this thread's columns to a row (none where it is null).
   __device__ __forceinline__ void write(T* row, const Quad (&f)[NC]) const {
@@ -174,26 +190,31 @@ struct Cols {
       const int e = col(i);
       if (e >= D) continue;
       const float* q = v + i * kPer;
-      if (whole(i)) {
-        if constexpr (sizeof(T) == 4) {
+      if constexpr (sizeof(T) == 4) {
+        if (whole(i)) {
           *reinterpret_cast<float4*>(row + e) = make_float4(q[0], q[1], q[2], q[3]);
         } else {
-          __nv_bfloat162 b[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(q[2 * k], q[2 * k + 1]);
-          *reinterpret_cast<uint4*>(row + e) = *reinterpret_cast<const uint4*>(b);
+          for (int k = 0; k < 4; ++k)
+            if (has(e + k)) row[e + k] = q[k];
         }
-      } else if constexpr (sizeof(T) == 4) {
+      } else {
+        uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if (has(e + k)) row[e + k] = q[k];
-      } else {  // words, but for a first or last column that shares one with another row
+        for (int k = 0; k < 4; ++k) w[k] = pack_bf16(q[2 * k], q[2 * k + 1]);
+        if (whole(i)) {
+          *reinterpret_cast<uint4*>(row + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {  // words, but for a first or last column that shares one with another row
+          const int first = max(0, (1 - e) / 2), words = (D - e) / 2 - first;
 #pragma unroll
-        for (int k = 0; k < kPer; k += 2)
-          if (has(e + k) && has(e + k + 1))
-            *reinterpret_cast<__nv_bfloat162*>(row + e + k) = __floats2bfloat162_rn(q[k], q[k + 1]);
-        if (e < 0 && (e & 1)) row[0] = from_float<T>(pick(q, -e));
-        if (e + kPer > D && ((D - e) & 1)) row[D - 1] = from_float<T>(pick(q, D - 1 - e));
+          for (int k = 0; k < 4; ++k)
+            if (static_cast<unsigned>(k - first) < static_cast<unsigned>(max(words, 0)))
+              *reinterpret_cast<uint32_t*>(row + e + 2 * k) = w[k];
+          uint16_t* const h = reinterpret_cast<uint16_t*>(row);
+          const auto word = [&](int k) { return k < 2 ? (k == 0 ? w[0] : w[1]) : k == 2 ? w[2] : w[3]; };
+          if (e < 0 && (e & 1)) h[0] = static_cast<uint16_t>(word(-e / 2) >> 16);
+          if (e + kPer > D && ((D - e) & 1)) h[D - 1] = static_cast<uint16_t>(word((D - e) / 2));
+        }
       }
     }
   }

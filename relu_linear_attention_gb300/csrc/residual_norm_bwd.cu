@@ -226,7 +226,7 @@ cudaError_t go(const ResidualNormArgs& a, const RowShape& s, int* grid, cudaStre
   // the slots' column sums meet where the ring was
   if (s.tpr <= 32) smem = std::max(smem, static_cast<size_t>(s.threads / s.tpr) * 2 * a.D * 4);
   constexpr bool kF32 = sizeof(T) == 4;
-  if constexpr (NC == 6 && STAGES == 2 || kF32 && NC == 4 && STAGES == 2) {
+  if constexpr ((kF32 ? NC == 4 : NC == 6) && STAGES == 2) {
     if (smem > kSmemMost) return go<T, R, NC, 1, true, MAXT, MINB>(a, s, grid, stream);
   } else if constexpr (kF32 && NC == 6 && STAGES == 1) {
     if (smem > kSmemMost) return go<T, R, NC, 0, false, MAXT, MINB>(a, s, grid, stream);
@@ -238,8 +238,8 @@ cudaError_t go(const ResidualNormArgs& a, const RowShape& s, int* grid, cudaStre
 // + where y is ahead) and what they were taken for:
 //   bf16  D = 2560: 8/4 two CTAs an SM 197, one 269;  5120: 16/3 229, 16/2 314;  6144: 16/3 210, 16/2 282;
 //         8192: 16/2 315, 32/1+ 326, 16/1+ 333;  12288: 24/1+ 447, 16 without a ring 683
-//   fp32  D = 2560: 8/2+ two CTAs an SM 173, 8/2 one 256;  4096: 8/2+ 190, 8/2 202;  5120: 16/2+ 200,
-//         16/2 204;  6144: 16/1+ 210, 16 without a ring 305;  8192: 16/1+ 258, without 299;
+//   fp32  D = 2560: 8/2+ two CTAs an SM 173, 8/2 one 256;  4096: 8/2+ 190, 8/2 202;  5120: 16/2+ 204,
+//         16/2 247;  6144: 16/1+ 210, 16 without a ring 305;  8192: 16/1+ 258, without 299;
 //         12288: 24 without a ring 421, 16 without 544
 template <typename T, Rows R>
 cudaError_t pick(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {

@@ -116,10 +116,10 @@ cudaError_t go(const ResidualNormArgs& a, const RowShape& s, cudaStream_t stream
 // Columns a thread, and the ring. us of 128 MiB a tensor (columns a thread / stages, + where y is ahead):
 //   bf16  D = 2048: 8/2 113, 16/2+ 119;  3584: 16/2+ 111, 8/3 118;  5120: 16/2+ 110, 8/3 126;
 //         10240: 24/2+ 122, 16/2+ 172;  12288: 24/2+ 107, 16/3 137;  16384: 16/2+ 132, 24/1+ 146
-//         D = 1001, 4098 (rows that are no whole vectors): 16/2+ 131, 142, 8/3 152, 197
+//         D = 1001, 4098 (rows that are no whole vectors): 16/2+ 132, 160, 8/3 152, 197
 //   fp32  D = 512: 16/1+ 109, 8/2 114;  1024: 8/2 113, 16/1+ 111;  5120: 8/2 105, 16/1+ 114;
 //         6144: 16/1+ 105, 8/2 112;  12288: 24/1+ 119, 16 without a ring 145
-//         D = 257, 1001, 4098: 16/1+ 127, 115, 111, 8/2 183, 109, 133
+//         D = 257, 1001, 4098: 16/1+ 127, 115, 111, 8/2 183, 122, 133
 template <typename T, Rows R>
 cudaError_t pick(const ResidualNormArgs& a, cudaStream_t stream) {
   constexpr bool kF32 = sizeof(T) == 4;
