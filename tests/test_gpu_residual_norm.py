@@ -233,3 +233,41 @@ def test_a_row_leaves_its_neighbours(cuda_device, lib, T, D, dtype):
     assert ri.data_ptr() == ill["x"].data_ptr()
     assert torch.equal(ri[rest], r[rest]) and torch.equal(hi[rest], h[rest])
     assert torch.isnan(ri[bad]).all()
+
+
+# Every choice of columns a thread and of ring, with more rows than are in flight at once.
+@pytest.mark.parametrize("T,D", [(12000, 300), (9000, 512), (5000, 768), (4000, 1536), (1500, 2052), (1500, 2560), (800, 3600),
+                                 (700, 4100), (700, 5120), (640, 6144), (640, 7000), (480, 8200), (480, 9300), (480, 10800),
+                                 (480, 12296), (480, 16384)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rings_of_every_width(cuda_device, lib, T, D, dtype):
+    kw, dr, dh = _inputs(T, D, dtype, T * D, cuda_device)
+    _check_fwd(kw, "sigmoid", dtype)
+    _check_bwd(dr, dh, kw, "sigmoid", dtype)
+
+
+@pytest.mark.parametrize("T,D", [(1400, 300), (700, 2560), (400, 6400), (400, 9300)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("parts", PARTS)
+def test_rings_without_some_of_the_inputs(cuda_device, lib, parts, T, D, dtype):
+    kw, dr, dh = _inputs(T, D, dtype, 7, cuda_device)
+    drop = dict(no_gate=["gate"], no_post=["w_post"], no_scale=["scale"], plain_join=["gate", "w_post", "scale"],
+                pre_only=["y", "gate", "w_post", "scale"], no_pre=["w_pre"]).get(parts, [])
+    kw.update((k, None) for k in drop)
+    _check_fwd(kw, "silu", dtype)
+    _check_bwd(None if parts == "dh_only" else dr, None if parts in ("dr_only", "no_pre") else dh, kw, "silu", dtype)
+
+
+@pytest.mark.parametrize("T,D", [(1400, 300), (700, 2560), (400, 6400), (400, 9300), (300, 12401)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rings_in_place(cuda_device, lib, T, D, dtype):
+    kw, dr, dh = _inputs(T, D, dtype, 12, cuda_device)
+    grads = R.rapt_residual_norm_bwd(dr, dh, **kw, act="relu", eps=EPS)
+    own = {k: v.clone() for k, v in kw.items()}
+    got = R.rapt_residual_norm_bwd(dr, dh, **own, act="relu", eps=EPS, dx=own["y"], dy=own["gate"], dgate=own["x"])
+    for a, b in zip(grads, got):
+        assert torch.equal(a, b)
+    r, h = R.rapt_residual_norm_fwd(**kw, act="relu", eps=EPS)
+    own = {k: v.clone() for k, v in kw.items()}
+    ri, hi = R.rapt_residual_norm_fwd(**own, act="relu", eps=EPS, r=own["gate"], h=own["x"])
+    assert torch.equal(r, ri) and torch.equal(h, hi)
