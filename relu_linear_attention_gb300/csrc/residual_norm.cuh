@@ -43,7 +43,7 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // ---------------------------------------------------------------- a thread's columns
 // Four values of a thread, as pairs.
-struct Quad {
+struct alignas(16) Quad {
   float2 p[2];
 };
 __device__ __forceinline__ Quad quad(float x) { return {{both(x), both(x)}}; }

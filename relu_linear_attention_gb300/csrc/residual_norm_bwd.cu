@@ -8,7 +8,7 @@ namespace {
 using namespace rn;
 
 // Partial column sums of CTA b at part[(b * 2 + k) * D + column], k = 0: G, 1: dw_pre.
-template <typename T, Rows R, int NC, int STAGES, bool AHEAD, int MAXT, int MINB>
+template <typename T, Rows R, int NC, int STAGES, bool AHEAD, int GAINS, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const ResidualNormArgs a, int tpr) {
   using C = Cols<T, R, NC, (STAGES > 0)>;
   __shared__ __align__(16) float red[2][32][8];
@@ -17,8 +17,37 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
   const int tx = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr, D = a.D;
   const float inv_d = 1.f / static_cast<float>(D);
   const C in(tx, tpr, D, static_cast<long>(blockIdx.x) * slots + threadIdx.x / tpr);
-  Quad ws[NC], wpre[NC];
-  load_gains(a, in, ws, wpre);
+  // w_post s and w_pre of this thread's columns: the first GAINS of them in shared memory behind the ring
+  // where they would spill (bf16, D = 8192: 315 us with both in registers, 258 with none)
+  Quad ws_kept[GAINS > 0 ? 1 : NC], wpre_kept[GAINS > 1 ? 1 : NC];
+  uint8_t* const gains = ring + blockDim.x * (STAGES * C::stride(kBwdTensors) + AHEAD * C::stride(1)) + threadIdx.x * 16;
+  {
+    Quad ws[NC], wpre[NC];
+    load_gains(a, in, ws, wpre);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if constexpr (GAINS > 0)
+        *reinterpret_cast<Quad*>(gains + c * 16 * blockDim.x) = ws[c];
+      else
+        ws_kept[c] = ws[c];
+      if constexpr (GAINS > 1)
+        *reinterpret_cast<Quad*>(gains + (NC + c) * 16 * blockDim.x) = wpre[c];
+      else
+        wpre_kept[c] = wpre[c];
+    }
+  }
+  const auto ws = [&](int c) {
+    if constexpr (GAINS > 0)
+      return *reinterpret_cast<const Quad*>(gains + c * 16 * blockDim.x);
+    else
+      return ws_kept[c];
+  };
+  const auto wpre = [&](int c) {
+    if constexpr (GAINS > 1)
+      return *reinterpret_cast<const Quad*>(gains + (NC + c) * 16 * blockDim.x);
+    else
+      return wpre_kept[c];
+  };
   const bool post = a.w_post != nullptr, gated = a.gate != nullptr, joined = a.y != nullptr, normed = a.dh != nullptr;
   Quad gg[NC], gpre[NC];
 #pragma unroll
@@ -114,7 +143,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
       if (kEarly) fetch_early(st, row + step, off + step_off);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        e[c] = e[c] * sg * ws[c] * av[c];
+        e[c] = e[c] * sg * ws(c) * av[c];
         r[c] = fma4(e[c], quad(1.f), r[c]);
       }
       in.read(st, 0, at(a.dh, off, live), t);
@@ -122,7 +151,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
       float2 rr = both(0.f), tr = rr, ed = rr, et = rr, er = rr;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        t[c] = t[c] * wpre[c];
+        t[c] = t[c] * wpre(c);
         rr = dot4(r[c], r[c], rr);
         tr = dot4(t[c], r[c], tr);
         ed = dot4(e[c], d[c], ed);
@@ -148,7 +177,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
     for (int c = 0; c < NC; ++c) {
       const Quad rh = r[c] * rho;
       gpre[c] = fma4(t[c], rh, gpre[c]);
-      g[c] = fma4(quad(rho), fma4(rh, quad(-m), t[c] * wpre[c]), g[c]);
+      g[c] = fma4(quad(rho), fma4(rh, quad(-m), t[c] * wpre(c)), g[c]);
     }
     in.write(a.dx != nullptr && live ? static_cast<T*>(a.dx) + off : nullptr, g);
 #pragma unroll
@@ -156,8 +185,9 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
       y[c] = y[c] * sg;  // yh
       const Quad ag = av[c] * g[c];
       gg[c] = fma4(ag, y[c], gg[c]);
-      da[c] = da[c] * g[c] * (y[c] * ws[c]);
-      g[c] = fma4(y[c], quad(-my), ws[c] * ag) * sg;
+      const Quad w = ws(c);
+      da[c] = da[c] * g[c] * (y[c] * w);
+      g[c] = fma4(y[c], quad(-my), w * ag) * sg;
     }
     in.write(a.dgate != nullptr && live ? static_cast<T*>(a.dgate) + off : nullptr, da);
     in.write(a.dy != nullptr && live ? static_cast<T*>(a.dy) + off : nullptr, g);
@@ -219,46 +249,48 @@ __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const GainGrads
   if (a.dscale != nullptr) a.dscale[c] = a.w_post != nullptr ? a.w_post[c] * t : t;
 }
 
-// A ring that does not fit becomes a shorter one.
-template <typename T, Rows R, int NC, int STAGES, bool AHEAD, int MAXT, int MINB>
+template <typename T, Rows R, int NC, int STAGES, bool AHEAD, int GAINS, int MAXT, int MINB>
 cudaError_t go(const ResidualNormArgs& a, const RowShape& s, int* grid, cudaStream_t stream) {
-  size_t smem = ring_bytes<T, R, NC>(s, STAGES, kBwdTensors) + (AHEAD ? ring_bytes<T, R, NC>(s, 1, 1) : 0);
+  size_t smem = ring_bytes<T, R, NC>(s, STAGES, kBwdTensors) + (AHEAD ? ring_bytes<T, R, NC>(s, 1, 1) : 0) +
+                static_cast<size_t>(s.threads) * GAINS * NC * sizeof(Quad);
   // the slots' column sums meet where the ring was
   if (s.tpr <= 32) smem = std::max(smem, static_cast<size_t>(s.threads / s.tpr) * 2 * a.D * 4);
-  constexpr bool kF32 = sizeof(T) == 4;
-  if constexpr ((kF32 ? NC == 4 : NC == 6) && STAGES == 2) {
-    if (smem > kSmemMost) return go<T, R, NC, 1, true, MAXT, MINB>(a, s, grid, stream);
-  } else if constexpr (kF32 && NC == 6 && STAGES == 1) {
-    if (smem > kSmemMost) return go<T, R, NC, 0, false, MAXT, MINB>(a, s, grid, stream);
-  }
-  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, AHEAD, MAXT, MINB>>(a, s, smem, max_parts(s),
-                                                                                    kMore<T, R> + 1, grid, stream);
+  return launch_rows<residual_norm_bwd_kernel<T, R, NC, STAGES, AHEAD, GAINS, MAXT, MINB>>(
+      a, s, smem, max_parts(s), kMore<T, R> + 1, grid, stream);
 }
-// Columns a thread, and the ring. us of 128 MiB a tensor, the best choices (columns a thread / stages,
-// + where y is ahead) and what they were taken for:
+// Columns a thread, the ring and the gains in shared memory. us of 128 MiB a tensor, columns a thread /
+// stages, + where y is ahead, g1 or g2 with gains in shared memory, the best choices and others:
 //   bf16  D = 2560: 8/4 two CTAs an SM 197, one 269;  5120: 16/3 229, 16/2 314;  6144: 16/3 210, 16/2 282;
-//         8192: 16/2 315, 32/1+ 326, 16/1+ 333;  12288: 24/1+ 447, 16 without a ring 683
+//         8192: 16/2 g2 258, 16/2 315, 32/1+ 326;  12288: 24/1+ g1 379, 24/1+ 422, 16 without a ring 683;
+//         16384: 32 without a ring, g2 655, 32/1+ 690
 //   fp32  D = 2560: 8/2+ two CTAs an SM 173, 8/2 one 256;  4096: 8/2+ 190, 8/2 202;  5120: 16/2+ 204,
-//         16/2 247;  6144: 16/1+ 210, 16 without a ring 305;  8192: 16/1+ 258, without 299;
-//         12288: 24 without a ring 421, 16 without 544
+//         16/2 247;  7168: 16/1+ g2 194, 16/1+ 271;  8192: 16/1+ g1 239, 16/1+ 258, without a ring 299;
+//         12288: 24 without a ring, g2 387, 24 411, 16 544;  16384: 32, g2 504, 32 562
 template <typename T, Rows R>
 cudaError_t pick(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {
   constexpr bool kF32 = sizeof(T) == 4;
   const RowShape s = bwd_shape(a.D, kMore<T, R>, kF32);
   if (s.ept == 8) {
-    if (s.threads <= 256) return go<T, R, 2, kF32 ? 2 : 3, false, 256, 2>(a, s, grid, stream);
-    if (s.threads <= 320) return go<T, R, 2, kF32 ? 2 : 4, kF32, 320, 2>(a, s, grid, stream);
-    return go<T, R, 2, kF32 ? 2 : 4, kF32, 512, 1>(a, s, grid, stream);
+    if (s.threads <= 256) return go<T, R, 2, kF32 ? 2 : 3, false, 0, 256, 2>(a, s, grid, stream);
+    if (s.threads <= 320) return go<T, R, 2, kF32 ? 2 : 4, kF32, 0, 320, 2>(a, s, grid, stream);
+    return go<T, R, 2, kF32 ? 2 : 4, kF32, 0, 512, 1>(a, s, grid, stream);
   }
-  if constexpr (!kF32)
-    if (s.ept == 16 && s.threads <= 128) return go<T, R, 4, 3, false, 128, 3>(a, s, grid, stream);
-  if (s.ept == 16 && s.threads <= 384) return go<T, R, 4, kF32 ? 2 : 3, kF32, 384, 1>(a, s, grid, stream);
-  if (s.ept == 16) return go<T, R, 4, kF32 ? 1 : 2, kF32, 512, 1>(a, s, grid, stream);
-  if (s.ept == 24 && s.threads <= 512) return go<T, R, 6, kF32 ? 1 : 2, kF32, 512, 1>(a, s, grid, stream);
+  if constexpr (kF32) {
+    if (s.ept == 16 && s.threads <= 320) return go<T, R, 4, 2, true, 0, 384, 1>(a, s, grid, stream);
+    if (s.ept == 16 && s.threads <= 448) return go<T, R, 4, 1, true, 2, 448, 1>(a, s, grid, stream);
+    if (s.ept == 16) return go<T, R, 4, 1, true, 1, 512, 1>(a, s, grid, stream);
+    if (s.ept == 24 && s.threads <= 512) return go<T, R, 6, 0, false, 2, 512, 1>(a, s, grid, stream);
+  } else {
+    if (s.ept == 16 && s.threads <= 128) return go<T, R, 4, 3, false, 0, 128, 3>(a, s, grid, stream);
+    if (s.ept == 16 && s.threads <= 384) return go<T, R, 4, 3, false, 0, 384, 1>(a, s, grid, stream);
+    if (s.ept == 16) return go<T, R, 4, 2, false, 2, 512, 1>(a, s, grid, stream);
+    if (s.ept == 24 && s.threads <= 448) return go<T, R, 6, 1, true, 2, 448, 1>(a, s, grid, stream);
+    if (s.ept == 24 && s.threads <= 512) return go<T, R, 6, 1, true, 1, 512, 1>(a, s, grid, stream);
+  }
   if constexpr (R == Rows::Whole)
-    return go<T, R, 8, kF32 ? 0 : 1, !kF32, 512, 1>(a, s, grid, stream);
+    return go<T, R, 8, 0, false, 2, 512, 1>(a, s, grid, stream);
   else
-    return go<T, R, 6, kF32 ? 0 : 1, !kF32, 704, 1>(a, s, grid, stream);
+    return go<T, R, 6, 0, false, 2, 704, 1>(a, s, grid, stream);
 }
 template <typename T>
 cudaError_t pick_rows(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {
