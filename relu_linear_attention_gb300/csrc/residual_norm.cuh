@@ -362,6 +362,18 @@ __device__ __forceinline__ void act_cols(bool gated, Act act, const Quad (&z)[NC
       }
     return;
   }
+  if (act == Act::Gelu) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float2 p, d;
+        gelu_two<GRAD>(z[c].p[i], p, d);
+        a[c].p[i] = p;
+        if (GRAD) da[c].p[i] = d;
+      }
+    return;
+  }
   float zz[4 * NC], aa[4 * NC], dd[4 * NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -370,10 +382,7 @@ __device__ __forceinline__ void act_cols(bool gated, Act act, const Quad (&z)[NC
     zz[4 * c + 2] = z[c].p[1].x;
     zz[4 * c + 3] = z[c].p[1].y;
   }
-  if (act == Act::Gelu) {
-#pragma unroll
-    for (int i = 0; i < 4 * NC; ++i) act_one<GRAD>(Act::Gelu, zz[i], aa[i], dd[i]);
-  } else if (act == Act::Relu) {
+  if (act == Act::Relu) {
 #pragma unroll
     for (int i = 0; i < 4 * NC; ++i) act_one<GRAD>(Act::Relu, zz[i], aa[i], dd[i]);
   } else {
