@@ -32,6 +32,15 @@ RAPT_DEV_BAD_CU_SEQLENS = 1
 RAPT_DEV_INTERNAL = 2
 
 
+class _Int32:
+    """An int32_t argument. ctypes takes the low 32 bits of any Python int, so that a size of 2^32 + 8 would
+    arrive as 8; what does not fit goes as the lowest int32_t instead, which every function refuses."""
+
+    @staticmethod
+    def from_param(v):
+        return v if -0x80000000 <= v <= 0x7FFFFFFF else -0x80000000
+
+
 class rapt_params(ctypes.Structure):
     _fields_ = [("eps_norm", c_float), ("rope_base", c_float), ("eps_den", c_float),
                 ("gamma_head_stride", c_int32)]
@@ -156,7 +165,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     for name, (res, args) in SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype = res
-        fn.argtypes = args
+        fn.argtypes = [_Int32 if a is c_int32 else a for a in args]
     _LIB = lib
     return lib
 
