@@ -41,8 +41,8 @@
  *     after the call waits for all of it.
  *   - Host-checkable errors are returned before anything is launched and nothing is written:
  *     RAPT_ERR_INVALID_ARG (null required pointer, size <= 0 where > 0 is required, eps not
- *     finite or <= 0, misalignment, `out` aliasing an input), RAPT_ERR_UNSUPPORTED (d or dtype not
- *     supported), RAPT_ERR_WORKSPACE (workspace pointer null or smaller than the size query).
+ *     finite or <= 0, misalignment, `out` aliasing an input), RAPT_ERR_UNSUPPORTED (d, a row's length,
+ *     an activation or dtype not supported), RAPT_ERR_WORKSPACE (workspace pointer null or smaller than the size query).
  *     RAPT_ERR_CUDA reports a failed launch (cudaGetLastError after the launch); the kernels may
  *     then not have run.
  *   - Optional outputs are skipped when their pointer is NULL; optional inputs count as zero.

@@ -74,7 +74,7 @@ const char* rapt_status_string(rapt_status s) {
   switch (s) {
     case RAPT_OK: return "RAPT_OK";
     case RAPT_ERR_INVALID_ARG: return "RAPT_ERR_INVALID_ARG: invalid argument";
-    case RAPT_ERR_UNSUPPORTED: return "RAPT_ERR_UNSUPPORTED: unsupported head size or dtype";
+    case RAPT_ERR_UNSUPPORTED: return "RAPT_ERR_UNSUPPORTED: unsupported size, activation or dtype";
     case RAPT_ERR_WORKSPACE: return "RAPT_ERR_WORKSPACE: workspace missing or too small";
     case RAPT_ERR_CUDA: return "RAPT_ERR_CUDA: CUDA launch failed";
     default: return "RAPT: unknown status";

@@ -124,3 +124,17 @@ def test_binding_refuses_host_tensors_and_wrong_arguments():
         R.rapt_linear_bwd(b, b, None)
     with pytest.raises(ValueError):
         R._act_code("tanh")
+
+
+@pytest.mark.parametrize("call", [
+    lambda lib: lib.rapt_glu_fwd(P[0], P[1], P[2], 4, 60, 64, 1, P[3], None, None),            # F % 8
+    lambda lib: lib.rapt_linear_bwd(P[0], P[1], P[2], 4, 64, 20, P[3], P[4], None, P[5], 1 << 40, None),  # K % 8
+    lambda lib: lib.rapt_residual_norm_fwd(P[0], P[1], P[2], 1, 4, 16392, 4, P[3], P[4], P[5], 1e-6, P[6], P[7], None),
+    lambda lib: lib.rapt_glu_fwd(P[0], P[1], P[2], 4, 64, 64, 9, P[3], None, None),            # activation
+])
+def test_what_an_unsupported_call_says_names_no_head(lib, call):
+    """The operators without heads report sizes and activations by the same code."""
+    with pytest.raises(_lib.RaptError) as e:
+        _lib.check("f", call(lib))
+    assert e.value.code == UNSUP
+    assert "head" not in str(e.value) and "size" in str(e.value) and "activation" in str(e.value)
