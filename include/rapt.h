@@ -496,6 +496,9 @@ rapt_status rapt_residual_norm_fwd(const void* x, const void* y, const void* gat
  *                    time on the same GPU model.
  *   workspace        rapt_residual_norm_bwd_workspace_size() bytes, 16-byte aligned, where any of
  *                    the three sums is asked for (else it may be NULL).
+ * Where the fp32 mean of r^2 overflows, h is 0 and the gradients are those of r alone. Else the row's sums
+ * of (w_pre dh) r, and of the joined term s act(gate) n times dr, w_pre dh and r, must be in fp32's
+ * range, too, or the gradients of that row are not finite.
  * Requirements as for the forward.
  */
 size_t rapt_residual_norm_bwd_workspace_size(int32_t T, int32_t D, rapt_dtype dtype);
