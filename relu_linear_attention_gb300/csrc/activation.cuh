@@ -8,11 +8,21 @@ namespace rapt {
 
 enum class Act { None = 0, Silu = 1, Gelu = 2, Relu = 3, Sigmoid = 4 };
 
-// 1 / (1 + e^-z) from the hardware's 2^x and 1/x, each within 2 ulp. e^-z overflows to infinity below
-// z = -88; the quotient is then an exact 0.
+// 1 / (1 + e^-z) from the hardware's 2^x and 1/x. The rounding of z log2(e) puts e^-z off by 1.5 |z| 2^-24 of
+// itself beside the 2^-22 of 2^x. e^-z overflows to infinity below z = -88; the quotient is then an exact 0.
 __device__ __forceinline__ float sigmoid_f(float z) {
   float e, s;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
+// The same for a derivative, and e = e^-z: 1 - s is formed as e s, which keeps its bits where s is near one
+// (as a difference it has lost 6 % at z = 16). The exponent stops at 2^127, where s is 0 as well, so that e s is
+// no infinity times zero; a NaN passes.
+__device__ __forceinline__ float sigmoid_f(float z, float& e) {
+  float w, s;
+  asm("min.NaN.f32 %0, %1, 0f42FE0000;" : "=f"(w) : "f"(z * -1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(w));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
   return s;
 }
@@ -77,15 +87,17 @@ __device__ __forceinline__ void act_one(Act act, float z, float& a, float& da) {
       break;
     }
     case Act::Sigmoid: {
-      const float s = sigmoid_f(z);
+      float e;
+      const float s = GRAD ? sigmoid_f(z, e) : sigmoid_f(z);
       a = s;
-      if (GRAD) da = s * (1.f - s);
+      if (GRAD) da = s * (e * s);
       break;
     }
     case Act::Silu: {
-      const float s = sigmoid_f(z);
+      float e;
+      const float s = GRAD ? sigmoid_f(z, e) : sigmoid_f(z);
       a = z * s;
-      if (GRAD) da = s * fmaf(z, 1.f - s, 1.f);
+      if (GRAD) da = s * fmaf(z, e * s, 1.f);
       break;
     }
   }

@@ -351,7 +351,10 @@ __device__ __forceinline__ void act_cols(bool gated, Act act, const Quad (&z)[NC
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 x = z[c].p[i];
-        const float2 s = make_float2(sigmoid_f(x.x), sigmoid_f(x.y)), t = fma2(s, both(-1.f), both(1.f));  // 1 - s
+        float2 s, e;
+        s.x = GRAD ? sigmoid_f(x.x, e.x) : sigmoid_f(x.x);
+        s.y = GRAD ? sigmoid_f(x.y, e.y) : sigmoid_f(x.y);
+        const float2 t = GRAD ? mul2(e, s) : s;  // 1 - s
         if (act == Act::Sigmoid) {
           a[c].p[i] = s;
           if (GRAD) da[c].p[i] = mul2(s, t);
