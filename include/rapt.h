@@ -452,7 +452,9 @@ rapt_status rla_l2_fwd_noalloc(const void* q, const void* k, const void* v, rapt
  */
 
 /* Activations of a gate: z, z sigmoid(z), z Phi(z) (Phi the normal distribution function),
- * max(z, 0) (derivative 0 at 0), sigmoid(z) = 1 / (1 + e^-z). */
+ * max(z, 0) (derivative 0 at 0), sigmoid(z) = 1 / (1 + e^-z). Formed in fp32, where sigmoid(z) is within
+ * (1.5 |z| + 8) 2^-24 and Phi(z) within (1.25 z^2 + 4 |z| + 16) 2^-24 of itself, down to where they fall
+ * below the least normal float (z = -87 and -12.9). */
 typedef enum rapt_act {
   RAPT_ACT_NONE = 0,
   RAPT_ACT_SILU = 1,

@@ -63,7 +63,18 @@ def test_sigmoid_gates_keep_their_relative_accuracy(cuda_device, lib, act):
     _near(dz, da, (3 * one + 4 * U) * mag, "derivative")
 
 
-@pytest.mark.parametrize("act", ["silu"])
+def test_gelu_keeps_its_relative_accuracy(cuda_device, lib):
+    """Phi(z) falls to 1e-36 on the left: its bound is relative all the way."""
+    z, a, da, mag = _truth("gelu")
+    r, dy, dz = _gates(Z, "gelu", cuda_device)
+    # the exponential; the fit and its steps, which lose up to 1.25 |z| where their terms cancel; z Phi
+    phi = (1.25 * z * z + 4 + 4 * np.abs(z) + 12) * U
+    _near(r, a, phi * np.abs(a), "forward")
+    _near(dy, a, phi * np.abs(a), "backward's act(z)")
+    _near(dz, da, (phi + 4 * U) * mag, "derivative")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("M", [1, 20])
 def test_gated_feed_forward_in_the_tails(cuda_device, lib, act, M):
     """g = z and u = 1 exactly: h is act(z) with one rounding to bf16, for few tokens and in tiles."""
