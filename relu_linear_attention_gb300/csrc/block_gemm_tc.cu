@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m0 = (t.m * 2 + rank) * kBM + 32 * quarter, row = m0 + lane;
       more = w.step();
       bool ok = tcp::wait(bar_accf + 8 * buf, (i / 2) & 1, kWait);
-      if (staged_dh) ok = ok && tcp::wait(my_dh, i & 1, kWait);
+      if (staged_dh) ok = tcp::wait(my_dh, i & 1, kWait) && ok;  // in any case: no copy is left under way
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) *s_abort = 1;
         break;
@@ -539,11 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (tid == 0 && rank == 0 && run && *s_abort) {  // given up: what is on its way to either CTA still lands
-    for (int s = 0; s < kStages; ++s) {
+  if (tid == 0 && run && *s_abort) {  // given up: what is on its way to either CTA still lands
+    for (int s = 0; s < (rank == 0 ? kStages : 0); ++s) {
       const uint32_t rounds = ring.round + (s < ring.s ? 1 : 0);
       if (rounds > 0) tcp::wait(bar_full + 8 * s, (rounds - 1) & 1, kWait);
     }
+    // half a millisecond for what no phase here stands for: slices that the other CTA fetched further on, and
+    // products of an issuer that went on without the epilogue
+    for (const long long t0 = clock64(); clock64() - t0 < (1 << 20);) __nanosleep(1000);
   }
   __syncwarp();
   tcp::cluster_sync();  // no CTA leaves while the other may still signal it
