@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_norm_bwd_kernel(const Res
     row_sum<6>(q, tpr, red, half);
     const float rho = normed ? inv_root(fmaf(q[0], inv_d, a.eps)) : 0.f;
     // mean(t rh), mean(u yh). rho = 0 (no dh, or sum r^2 overflowed): rh = 0, and the sums with r, which may have
-    // overflowed, too, do not count. (To form them again where one overflows for rho > 0 took 4 to 16 % of
-    // every call for a second way through the sums, 30 % as a path of its own: registers.)
+    // overflowed, too, do not count. (To form them again where one overflows for rho > 0 made every call 4 to
+    // 16 % slower as another turn of this code, 16 to 38 % in bf16 as a path of its own: registers.)
     const float m = rho > 0.f ? rho * q[1] * inv_d : 0.f;
     const float my = post ? inv_d * (rho > 0.f ? q[2] + rho * (q[3] - rho * m * q[4]) : q[2]) : 0.f;
     Quad g[NC], y[NC], t[NC];
@@ -264,10 +264,10 @@ cudaError_t go(const ResidualNormArgs& a, const RowShape& s, int* grid, cudaStre
 // Columns a thread, the ring and the gains in shared memory. us of 128 MiB a tensor, columns a thread /
 // stages, + where y is ahead, g1 or g2 with gains in shared memory, the best choices and others:
 //   bf16  D = 2560: 8/4 two CTAs an SM 197, one 269;  5120: 16/3 229, 16/2 314;  6144: 16/3 210, 16/2 282;
-//         8192: 16/2 g2 258, 16/2 315, 32/1+ 326;  12288: 24/1+ g1 379, 24/1+ 422, 16 without a ring 683;
-//         16384: 32 without a ring, g2 655, 32/1+ 690
+//         8192: 16/2 g2 258, 16/2 315, 32/1+ 326;  12288: 24/1+ g1 358, 24/1+ 422, 16 without a ring 683;
+//         16384: 32 without a ring, g2 635, 32/1+ 690
 //   fp32  D = 2560: 8/2+ two CTAs an SM 173, 8/2 one 256;  4096: 8/2+ 190, 8/2 202;  5120: 16/2+ 204,
-//         16/2 247;  7168: 16/1+ g2 194, 16/1+ 271;  8192: 16/1+ g1 239, 16/1+ 258, without a ring 299;
+//         16/2 247;  7168: 16/1+ g2 194, 16/1+ 271;  8192: 16/1+ g1 233, 16/1+ 258, without a ring 299;
 //         12288: 24 without a ring, g2 387, 24 411, 16 544;  16384: 32, g2 504, 32 562
 template <typename T, Rows R>
 cudaError_t pick(const ResidualNormArgs& a, int* grid, cudaStream_t stream) {
