@@ -67,7 +67,8 @@ def test_linear_gradients_are_exact_sums(cuda_device, lib, M, N, K):
 
 
 # (M, F, K), as above with two terms in dx and two products in dw
-GLU = [(20, 80, 136), (226, 264, 776),
+GLU = [(1, 8, 8), (7, 2744, 1032), (16, 1024, 264),  # the kernel of few tokens forward
+       (20, 80, 136), (226, 264, 776),
        (139, 3088, 8),           # cut alike, whole
        (5169, 2312, 8),          # both cut alike
        (12947, 5144, 8),         # both cut, shares across tiles

@@ -22,26 +22,27 @@ Z = np.unique(np.concatenate([np.linspace(-12.5, 16.0, 60001), np.geomspace(1e-6
 
 def _gates(z, act, device):
     """(act(z) of the forward, act(z) and act'(z) of the backward) in fp32."""
+    n = z.size
     z = torch.from_numpy(z).to(device).view(1, -1)
     z = torch.nn.functional.pad(z, (0, -z.shape[1] % 1024)).view(-1, 1024)
     one, zero = torch.ones_like(z), torch.zeros_like(z)
     r, _ = R.rapt_residual_norm_fwd(zero, one, gate=z, act=act)
     _, dy, dz = R.rapt_residual_norm_bwd(one, None, zero, one, gate=z, act=act)[:3]
-    n = Z.size
     return [t.flatten()[:n].double().cpu().numpy() for t in (r, dy, dz)]
 
 
-def _near(got, ref, budget, what):
+def _near(got, ref, budget, what, z=Z):
     bad = ~(np.abs(got - ref) <= budget)
     if bad.any():
         i = np.argmax(np.where(bad, np.abs(got - ref) / budget, 0))
         raise AssertionError("%s: %d outside, worst at z = %g: got %r, want %r, %.3g of the bound" % (
-            what, bad.sum(), Z[i], got[i], ref[i], abs(got[i] - ref[i]) / budget[i]))
+            what, bad.sum(), z[i], got[i], ref[i], abs(got[i] - ref[i]) / budget[i]))
 
 
-def _truth(act):
-    """act(z), act'(z) and the magnitudes of act's terms, in 64 bits without a difference of near values."""
-    z = Z.astype(np.float64)
+def _truth(act, z=Z):
+    """z, act(z), act'(z) and the magnitudes of the terms of act', in 64 bits without a difference of near
+    values."""
+    z = z.astype(np.float64)
     s, t = expit(z), expit(-z)
     if act == "sigmoid":
         return z, s, s * t, s * t
@@ -51,16 +52,20 @@ def _truth(act):
     return z, z * cdf, cdf + z * bell, cdf + np.abs(z) * bell
 
 
+FAR = np.unique(np.concatenate([np.linspace(-86.0, -12.0, 20001), np.linspace(12.0, 80.0, 20001)]).astype(np.float32))
+
+
 @pytest.mark.parametrize("act", ["sigmoid", "silu"])
-def test_sigmoid_gates_keep_their_relative_accuracy(cuda_device, lib, act):
+@pytest.mark.parametrize("at", [Z, FAR], ids=["near", "far"])
+def test_sigmoid_gates_keep_their_relative_accuracy(cuda_device, lib, at, act):
     """sigmoid' = s (1 - s) and 1 - s are small where s is near one: formed as e^-z s they keep all bits."""
-    z, a, da, mag = _truth(act)
-    r, dy, dz = _gates(Z, act, cuda_device)
+    z, a, da, mag = _truth(act, at)
+    r, dy, dz = _gates(at, act, cuda_device)
     one = (1.5 * np.abs(z) + 8) * U  # s: the exponent, 2^x, 1 + e, 1/x, and z s
-    _near(r, a, one * np.abs(a), "forward")
-    _near(dy, a, one * np.abs(a), "backward's act(z)")
+    _near(r, a, one * np.abs(a), "forward", at)
+    _near(dy, a, one * np.abs(a), "backward's act(z)", at)
     # s, e and s again, and four operations
-    _near(dz, da, (3 * one + 4 * U) * mag, "derivative")
+    _near(dz, da, (3 * one + 4 * U) * mag, "derivative", at)
 
 
 def test_gelu_keeps_its_relative_accuracy(cuda_device, lib):
