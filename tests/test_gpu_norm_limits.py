@@ -10,7 +10,6 @@ import torch
 
 import block_bounds as BB
 from gpu_helpers import to_host
-from oracle import block as OB
 from relu_linear_attention_gb300 import binding as R
 
 pytestmark = pytest.mark.gpu
