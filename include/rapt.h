@@ -553,6 +553,104 @@ rapt_status rapt_linear_bwd(const void* dy, const void* x, const void* w, int32_
                             int32_t K, void* dx, void* dw, uint32_t* dev_status, void* workspace,
                             size_t workspace_bytes, rapt_stream_t stream);
 
+/*
+ * The selective state space block: a short causal convolution and a scan over a matrix state whose decay
+ * depends on the token, for prompts (dense, packed) and for single tokens, and layer norm. None of them is
+ * on the pages. Unlike the tensors above, x, B, C, z and dt of the scan and x of the convolution need not be
+ * contiguous: a token's values lie side by side, and a stride (in elements) leads from one token's to the
+ * next, so that the columns of one wider matrix (a projection's z | x | B | C | dt) are taken where they
+ * are. Dense: token t of batch row b is row b L + t. Offsets are 64 bits wide.
+ */
+
+/*
+ * Causal convolution of every channel over the tokens of its own document:
+ *   y[t, c] = act(bias[c] + sum_{k<W} w[c, k] x[t - W + 1 + k, c]),
+ * where the W - 1 tokens before a document's first are its rows of `state` (zeros where that is NULL).
+ *   x [B L, D] or [T, D] of `dtype`, x_stride >= D elements from token to token; 16-byte aligned.
+ *   w fp32 [D, W], bias nullable fp32 [D]; 2 <= W <= 4 (RAPT_ERR_UNSUPPORTED otherwise).
+ *   state, state_final  nullable [documents, W - 1, D] of `dtype`, oldest token first: what came before the
+ *             document, and its last W - 1 inputs (rows of `state` in a document shorter than that).
+ *   out       [B L, D] or [T, D], contiguous; no output aliases an input or another output.
+ * fp32 arithmetic, one rounding. Requirements: B >= 1, L >= 0, D >= 1, B L and T <= 2^30, D <= 2^24, documents * D at
+ * most 2^38; varlen: N >= 1, T >= 0; cu_seqlens and dev_status as for rapt_varlen_fwd (tokens of a malformed
+ * cu_seqlens may be computed with another document's bounds, or skipped; nothing outside the tensors is touched).
+ */
+rapt_status rapt_conv_prefill_fwd(const void* x, int64_t x_stride, rapt_dtype dtype, int32_t B, int32_t L,
+                                  int32_t D, const float* w, const float* bias, int32_t W, rapt_act act,
+                                  const void* state, void* out, void* state_final, rapt_stream_t stream);
+rapt_status rapt_conv_varlen_fwd(const void* x, int64_t x_stride, rapt_dtype dtype, int32_t T, int32_t D,
+                                 const int32_t* cu_seqlens, int32_t N, const float* w, const float* bias,
+                                 int32_t W, rapt_act act, const void* state, void* out, void* state_final,
+                                 uint32_t* dev_status, rapt_stream_t stream);
+/* One token of N sequences: x, out [N, D]; state [N, W - 1, D] is read, and the new token shifted in, in place. */
+rapt_status rapt_conv_decode_step(const void* x, int64_t x_stride, rapt_dtype dtype, int32_t N, int32_t D,
+                                  const float* w, const float* bias, int32_t W, rapt_act act, void* state,
+                                  void* out, rapt_stream_t stream);
+
+/*
+ * Selective scan. For head h of group g = h / (H / G), with dt = softplus(dt_raw + dt_bias[h]) (or
+ * dt_raw + dt_bias[h] where dt_softplus is 0):
+ *   S_t = exp(dt A[h]) S_{t-1} + dt B_t[g] (x) x_t[h]     (Ns x P, key-major like every state),
+ *   out_t = (S_t^T C_t[g] + D[h] x_t[h]) * silu(z_t[h]).
+ * The inputs of a call (rows: B L, T, or N single tokens):
+ *   x [rows, H, P], B and C [rows, G, Ns], dt [rows, H], z [rows, H, P] (nullable: no gate), of `dtype`. Each
+ *     with its stride from token to token; x, B, C and z and their strides in multiples of 16 bytes, dt and its
+ *     stride in whole elements.
+ *   A fp32 [H], <= 0; D and dt_bias fp32 [H], nullable (0).
+ * Requirements: P and Ns of 16, 32, 64 or 128 (RAPT_ERR_UNSUPPORTED otherwise), H a multiple of G, dt >= 0 where
+ * dt_softplus is 0.
+ */
+typedef struct rapt_ssm_inputs {
+  const void *x, *dt, *B, *C, *z;
+  int64_t x_stride, dt_stride, B_stride, C_stride, z_stride;
+  const float *A, *D, *dt_bias;
+  int32_t H, P, G, Ns;
+  int32_t dt_softplus;
+  int32_t dtype; /* rapt_dtype */
+} rapt_ssm_inputs;
+
+/*
+ * The scan over prompts, one state per document (dense: batch row).
+ *   S0, S_final  nullable fp32 [documents, H, Ns, P]: the state before and after (they may not alias).
+ *   out          [rows, H, P] of `dtype`, contiguous; aliases no input.
+ *   workspace    at least the matching *_workspace_size() bytes, 16-byte aligned: state increments and decays of
+ *                the segments that long documents are cut into. in's pointers are not looked at by the query.
+ *   cu_seqlens, N, max_seqlen, dev_status as for rapt_varlen_fwd.
+ * fp32 inputs, and P or Ns below 64: the recurrence in fp32. bf16 with P and Ns of 64 or 128: chunks of 128 tokens
+ * on the tensor cores with fp32 accumulation; the decayed scores C_t . B_i and the state that C reads are
+ * rounded to bf16, decays, step sizes and the states themselves are fp32 (the state's increments are products of
+ * B, exact, with dt x under its decay in two bf16 parts, 16 bits).
+ * Requirements: B >= 1, L >= 0 (0 writes S_final alone), rows <= 2^30, documents * H < 2^25.
+ */
+size_t rapt_ssm_prefill_workspace_size(const rapt_ssm_inputs* in, int32_t B, int32_t L);
+rapt_status rapt_ssm_prefill_fwd(const rapt_ssm_inputs* in, int32_t B, int32_t L, const float* S0, void* out,
+                                 float* S_final, uint32_t* dev_status, void* workspace,
+                                 size_t workspace_bytes, rapt_stream_t stream);
+size_t rapt_ssm_varlen_workspace_size(const rapt_ssm_inputs* in, int32_t T, int32_t N, int32_t max_seqlen);
+rapt_status rapt_ssm_varlen_fwd(const rapt_ssm_inputs* in, int32_t T, const int32_t* cu_seqlens, int32_t N,
+                                int32_t max_seqlen, const float* S0, void* out, float* S_final,
+                                uint32_t* dev_status, void* workspace, size_t workspace_bytes,
+                                rapt_stream_t stream);
+/* One token of N sequences: out [N, H, P]; S fp32 [N, H, Ns, P] is updated in place, then read. fp32 throughout. */
+rapt_status rapt_ssm_decode_step(const rapt_ssm_inputs* in, int32_t N, float* S, void* out, rapt_stream_t stream);
+
+/*
+ * Layer norm of every row of D values: y = w (x - mean(x)) (var(x) + eps)^(-1/2) + b.
+ *   x, y [T, D] of `dtype`; y may be x itself. w and b nullable fp32 [D] (ones, zeros).
+ * Its gradients for sum(dy * y), with xh = (x - mean) (var + eps)^(-1/2) formed again from x:
+ *   dx = (var + eps)^(-1/2) (w dy - mean(w dy) - xh mean(w dy xh)),  dw = sum over rows of dy xh,  db = of dy.
+ *   dx nullable [T, D], may be dy or x itself; dw and db nullable fp32 [D] (zeros for T = 0).
+ *   workspace rapt_layer_norm_bwd_workspace_size() bytes, 16-byte aligned, where dw or db is asked for.
+ * All arithmetic is fp32, the variance from differences to the mean; one rounding. The column sums have a fixed
+ * order: the same bits every time on the same GPU model. Requirements as for rapt_residual_norm_fwd.
+ */
+rapt_status rapt_layer_norm_fwd(const void* x, rapt_dtype dtype, int32_t T, int32_t D, const float* w,
+                                const float* b, float eps, void* y, rapt_stream_t stream);
+size_t rapt_layer_norm_bwd_workspace_size(int32_t T, int32_t D, rapt_dtype dtype);
+rapt_status rapt_layer_norm_bwd(const void* dy, const void* x, rapt_dtype dtype, int32_t T, int32_t D,
+                                const float* w, float eps, void* dx, float* dw, float* db, void* workspace,
+                                size_t workspace_bytes, rapt_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,11 +7,13 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "librapt.so")
 
 c_int32 = ctypes.c_int32
+c_int64 = ctypes.c_int64
 c_size_t = ctypes.c_size_t
 c_void_p = ctypes.c_void_p
 c_float = ctypes.c_float
@@ -44,6 +46,19 @@ class _Int32:
 class rapt_params(ctypes.Structure):
     _fields_ = [("eps_norm", c_float), ("rope_base", c_float), ("eps_den", c_float),
                 ("gamma_head_stride", c_int32)]
+
+
+class rapt_ssm_inputs(ctypes.Structure):
+    _fields_ = [(k, c_void_p) for k in ("x", "dt", "B", "C", "z")] + \
+        [(k, c_int64) for k in ("x_stride", "dt_stride", "B_stride", "C_stride", "z_stride")] + \
+        [(k, c_void_p) for k in ("A", "D", "dt_bias")] + \
+        [(k, c_int32) for k in ("H", "P", "G", "Ns", "dt_softplus", "dtype")]
+
+
+# The same as bytes: packing takes 1 us where setting a structure's fields takes 4. A size that does not fit
+# raises struct.error.
+ssm_inputs = struct.Struct("5Q5q3Q6i")
+assert ssm_inputs.size == ctypes.sizeof(rapt_ssm_inputs)
 
 
 # name -> (restype, argtypes), in the order of include/rapt.h
@@ -145,6 +160,22 @@ SIGNATURES = {
     "rapt_linear_bwd_workspace_size": (c_size_t, [c_int32] * 3),
     "rapt_linear_bwd": (c_int32, [c_void_p] * 3 + [c_int32] * 3 + [c_void_p] * 4 +
                         [c_size_t, c_void_p]),
+    "rapt_conv_prefill_fwd": (c_int32, [c_void_p, c_int64] + [c_int32] * 4 + [c_void_p] * 2 + [c_int32] * 2 +
+                              [c_void_p] * 4),
+    "rapt_conv_varlen_fwd": (c_int32, [c_void_p, c_int64] + [c_int32] * 3 + [c_void_p, c_int32] + [c_void_p] * 2 +
+                             [c_int32] * 2 + [c_void_p] * 5),
+    "rapt_conv_decode_step": (c_int32, [c_void_p, c_int64] + [c_int32] * 3 + [c_void_p] * 2 + [c_int32] * 2 +
+                              [c_void_p] * 3),
+    "rapt_ssm_prefill_workspace_size": (c_size_t, [c_void_p] + [c_int32] * 2),
+    "rapt_ssm_prefill_fwd": (c_int32, [c_void_p] + [c_int32] * 2 + [c_void_p] * 5 + [c_size_t, c_void_p]),
+    "rapt_ssm_varlen_workspace_size": (c_size_t, [c_void_p] + [c_int32] * 3),
+    "rapt_ssm_varlen_fwd": (c_int32, [c_void_p, c_int32, c_void_p] + [c_int32] * 2 + [c_void_p] * 5 +
+                            [c_size_t, c_void_p]),
+    "rapt_ssm_decode_step": (c_int32, [c_void_p, c_int32] + [c_void_p] * 3),
+    "rapt_layer_norm_fwd": (c_int32, [c_void_p] + [c_int32] * 3 + [c_void_p] * 2 + [c_float] + [c_void_p] * 2),
+    "rapt_layer_norm_bwd_workspace_size": (c_size_t, [c_int32] * 3),
+    "rapt_layer_norm_bwd": (c_int32, [c_void_p] * 2 + [c_int32] * 3 + [c_void_p, c_float] + [c_void_p] * 4 +
+                            [c_size_t, c_void_p]),
 }
 
 RAPT_L2_NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -568,6 +568,265 @@ def rapt_linear_bwd(dy, x, w, *, need_dx=True, need_dw=True, dx=None, dw=None, d
     return dx, dw
 
 
+def _rows(name, t, dtype, lead, tail, index):
+    """(address, elements from row to row) of t, [*lead, *tail] on CUDA device `index`: a row's values lie side by
+    side and the rows at one stride, so that the columns of a wider matrix are taken as they are."""
+    shape = lead + tail
+    _need(t.dtype is dtype, "%s must be %s, got %s" % (name, dtype, t.dtype))
+    _need(t.shape == shape, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    _need(t.get_device() == index >= 0, "%s must be on cuda:%d, got %s" % (name, index, t.device))
+    st, width, k = t.stride(), 1, len(lead)
+    for i in range(len(shape) - 1, k - 1, -1):
+        _need(st[i] == width or shape[i] <= 1, "%s: a token's values must lie side by side" % name)
+        width *= shape[i]
+    step = rows = None
+    for i in range(k - 1, -1, -1):
+        n = shape[i]
+        if n == 0:
+            return t.data_ptr(), width
+        if n > 1:
+            if step is None:
+                step, rows = st[i], 1
+            _need(st[i] == step * rows, "%s: its tokens must lie at one stride" % name)
+            rows *= n
+    return t.data_ptr(), width if step is None else step
+
+
+def _first_state(name, t, dtype, shape, index, final, want_final):
+    """(address of a carried state, final state, its address)."""
+    if final is None and want_final:
+        final = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    return (_opt_like(name, t, dtype, shape, index), final,
+            _opt_like(name + "_final", final, dtype, shape, index))
+
+
+def _conv_taps(w, bias, D, index):
+    _need(w.dim() == 2, "w must be [D, W]")
+    W = w.shape[1]
+    return (_like("w", w, torch.float32, torch.Size((D, W)), index),
+            _opt_like("bias", bias, torch.float32, torch.Size((D,)), index), W)
+
+
+def rapt_conv_prefill_fwd(x, w, bias=None, *, act="silu", state=None, out=None, final_state=False,
+                          state_final=None, stream=None):
+    """Short causal convolution of every channel with its activation: x [B, L, D] (fp32 or bf16; its tokens may lie
+    at a stride), w fp32 [D, W] with W of 2 to 4, bias fp32 [D]; state [B, W - 1, D] is what came before. Returns
+    (out, state_final), the last W - 1 inputs of every row; None unless requested or passed."""
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_conv_prefill_fwd, di, stream, x, w, bias, act=act, state=state, out=out,
+                          final_state=final_state, state_final=state_final)
+    _need(x.dim() == 3 and x.dtype in _DT, "x must be [B, L, D], float32 or bfloat16")
+    B, L, D = x.shape
+    xp, xs = _rows("x", x, x.dtype, x.shape[:2], x.shape[2:], di)
+    wp, bp, W = _conv_taps(w, bias, D, di)
+    sp, state_final, fp = _first_state("state", state, x.dtype, torch.Size((B, W - 1, D)), di, state_final, final_state)
+    if out is None:
+        out = torch.empty((B, L, D), dtype=x.dtype, device=x.device)
+    op = _like("out", out, x.dtype, x.shape, di)
+    st = _lib.load().rapt_conv_prefill_fwd(xp, xs, _DT[x.dtype], B, L, D, wp, bp, W, _act_code(act), sp, op, fp,
+                                           _handle(di))
+    if st:
+        _lib.check("rapt_conv_prefill_fwd", st)
+    return out, state_final
+
+
+def rapt_conv_varlen_fwd(x, cu_seqlens, w, bias=None, *, act="silu", state=None, out=None, final_state=False,
+                         state_final=None, dev_status=None, stream=None):
+    """The convolution over packed documents: x [T, D], cu_seqlens int32 [N + 1] on the device, state [N, W - 1, D].
+    Returns (out, state_final)."""
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_conv_varlen_fwd, di, stream, x, cu_seqlens, w, bias, act=act, state=state, out=out,
+                          final_state=final_state, state_final=state_final, dev_status=dev_status)
+    _need(x.dim() == 2 and x.dtype in _DT, "x must be [T, D], float32 or bfloat16")
+    T, D = x.shape
+    N = _n_docs(cu_seqlens)
+    xp, xs = _rows("x", x, x.dtype, x.shape[:1], x.shape[1:], di)
+    cp = _like("cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, di)
+    wp, bp, W = _conv_taps(w, bias, D, di)
+    sp, state_final, fp = _first_state("state", state, x.dtype, torch.Size((N, W - 1, D)), di, state_final, final_state)
+    if out is None:
+        out = torch.empty((T, D), dtype=x.dtype, device=x.device)
+    op = _like("out", out, x.dtype, x.shape, di)
+    st = _lib.load().rapt_conv_varlen_fwd(xp, xs, _DT[x.dtype], T, D, cp, N, wp, bp, W, _act_code(act), sp, op, fp,
+                                          _status_ptr(dev_status, di), _handle(di))
+    if st:
+        _lib.check("rapt_conv_varlen_fwd", st)
+    return out, state_final
+
+
+def rapt_conv_decode_step(x, state, w, bias=None, *, act="silu", out=None, stream=None):
+    """One token of N sequences: x [N, D]; state [N, W - 1, D] takes the new token in place. Returns out [N, D]."""
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_conv_decode_step, di, stream, x, state, w, bias, act=act, out=out)
+    dt, shape = x.dtype, x.shape
+    _need(len(shape) == 2 and dt in _DT, "x must be [N, D], float32 or bfloat16")
+    N, D = shape
+    xp, xs = _rows("x", x, dt, shape[:1], shape[1:], di)
+    wp, bp, W = _conv_taps(w, bias, D, di)
+    sp = _like("state", state, dt, torch.Size((N, W - 1, D)), di)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=x.device)
+        op = out.data_ptr()
+    else:
+        op = _like("out", out, dt, shape, di)
+    st = _lib.load().rapt_conv_decode_step(xp, xs, _DT[dt], N, D, wp, bp, W, _act_code(act), sp, op, _handle(di))
+    if st:
+        _lib.check("rapt_conv_decode_step", st)
+    return out
+
+
+def _n_docs(cu_seqlens):
+    _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2, "cu_seqlens must be [N + 1]")
+    return cu_seqlens.numel() - 1
+
+
+def _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, index):
+    """(the packed rapt_ssm_inputs, leading shape, H, Ns, P) of x [*, H, P], dt [*, H], B and C [*, G, Ns]."""
+    ty, shape = x.dtype, x.shape
+    code = _DT.get(ty)
+    _need(code is not None, "dtype must be float32 or bfloat16")
+    lead, heads = shape[:-2], shape[-2:-1]
+    groups = B.shape[-2:]
+    _need(len(groups) == 2, "B must be [..., G, Ns]")
+    xp, xs = _rows("x", x, ty, lead, shape[-2:], index)
+    tp, ts = _rows("dt", dt, ty, lead, heads, index)
+    bp, bs = _rows("B", B, ty, lead, groups, index)
+    cp, cs = _rows("C", C, ty, lead, groups, index)
+    zp, zs = (0, 0) if z is None else _rows("z", z, ty, lead, shape[-2:], index)
+    f32 = torch.float32
+    ap = _like("A", A, f32, heads, index)
+    dp = 0 if D is None else _like("D", D, f32, heads, index)
+    ip = 0 if dt_bias is None else _like("dt_bias", dt_bias, f32, heads, index)
+    sizes = (heads[0], shape[-1], groups[0], groups[1], 1 if dt_softplus else 0, code)
+    _need(max(sizes) < 1 << 31, "sizes must fit 32 bits")
+    return _lib.ssm_inputs.pack(xp, tp, bp, cp, zp, xs, ts, bs, cs, zs, ap, dp, ip, *sizes), lead, heads[0], \
+        groups[1], shape[-1]
+
+
+def rapt_ssm_prefill_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=True, S0=None, out=None,
+                         final_state=False, S_final=None, dev_status=None, workspace=None, stream=None):
+    """Selective scan of prompts: x [B, L, H, P], dt [B, L, H], B and C [B, L, G, Ns], gate z like x (fp32 or bf16;
+    the tokens of each may lie at a stride), A (<= 0), D and dt_bias fp32 [H]. Returns (out [B, L, H, P], S_final
+    [B, H, Ns, P] fp32); the final state is None unless requested or passed."""
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_ssm_prefill_fwd, di, stream, x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias,
+                          dt_softplus=dt_softplus, S0=S0, out=out, final_state=final_state, S_final=S_final,
+                          dev_status=dev_status, workspace=workspace)
+    _need(x.dim() == 4, "x must be [B, L, H, P]")
+    packed, lead, H, Ns, P = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, di)
+    Bn, L = lead
+    sp, S_final, fp = _first_state("S0", S0, torch.float32, torch.Size((Bn, H, Ns, P)), di, S_final, final_state)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    op = _like("out", out, x.dtype, x.shape, di)
+    lib = _lib.load()
+    wsp, wsb, owner = _scratch(lib.rapt_ssm_prefill_workspace_size(packed, Bn, L), workspace, x)
+    st = lib.rapt_ssm_prefill_fwd(packed, Bn, L, sp, op, fp, _status_ptr(dev_status, di), wsp, wsb, _handle(di))
+    if st:
+        _lib.check("rapt_ssm_prefill_fwd", st)
+    return out, S_final
+
+
+def rapt_ssm_varlen_fwd(x, dt, A, B, C, cu_seqlens, *, max_seqlen, D=None, z=None, dt_bias=None, dt_softplus=True,
+                        S0=None, out=None, final_state=False, S_final=None, dev_status=None, workspace=None,
+                        stream=None):
+    """Selective scan of packed documents: x [T, H, P] and so on; cu_seqlens int32 [N + 1] on the device. Returns
+    (out [T, H, P], S_final [N, H, Ns, P])."""
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_ssm_varlen_fwd, di, stream, x, dt, A, B, C, cu_seqlens, max_seqlen=max_seqlen, D=D, z=z,
+                          dt_bias=dt_bias, dt_softplus=dt_softplus, S0=S0, out=out, final_state=final_state,
+                          S_final=S_final, dev_status=dev_status, workspace=workspace)
+    _need(x.dim() == 3, "x must be [T, H, P]")
+    packed, lead, H, Ns, P = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, di)
+    T, N = lead[0], _n_docs(cu_seqlens)
+    cp = _like("cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, di)
+    sp, S_final, fp = _first_state("S0", S0, torch.float32, torch.Size((N, H, Ns, P)), di, S_final, final_state)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    op = _like("out", out, x.dtype, x.shape, di)
+    lib, most = _lib.load(), int(max_seqlen)
+    wsp, wsb, owner = _scratch(lib.rapt_ssm_varlen_workspace_size(packed, T, N, most), workspace, x)
+    st = lib.rapt_ssm_varlen_fwd(packed, T, cp, N, most, sp, op, fp, _status_ptr(dev_status, di), wsp, wsb, _handle(di))
+    if st:
+        _lib.check("rapt_ssm_varlen_fwd", st)
+    return out, S_final
+
+
+def rapt_ssm_decode_step(x, dt, A, B, C, S, *, D=None, z=None, dt_bias=None, dt_softplus=True, out=None, stream=None):
+    """One token of N sequences: x [N, H, P], dt [N, H], B and C [N, G, Ns]; S fp32 [N, H, Ns, P] is updated in
+    place, then read. Returns out [N, H, P]."""
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_ssm_decode_step, di, stream, x, dt, A, B, C, S, D=D, z=z, dt_bias=dt_bias,
+                          dt_softplus=dt_softplus, out=out)
+    _need(x.dim() == 3, "x must be [N, H, P]")
+    packed, lead, H, Ns, P = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, di)
+    sp = _like("S", S, torch.float32, torch.Size((lead[0], H, Ns, P)), di)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        op = out.data_ptr()
+    else:
+        op = _like("out", out, x.dtype, x.shape, di)
+    st = _lib.load().rapt_ssm_decode_step(packed, lead[0], sp, op, _handle(di))
+    if st:
+        _lib.check("rapt_ssm_decode_step", st)
+    return out
+
+
+def rapt_layer_norm_fwd(x, w=None, b=None, *, eps=1e-5, y=None, stream=None):
+    """y = w (x - mean) (var + eps)^(-1/2) + b over the rows of x [..., D] (fp32 or bf16); w and b fp32 [D], ones and
+    zeros where missing. y may be passed to be written, and may be x itself. Returns y."""
+    di = x.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_layer_norm_fwd, di, stream, x, w, b, eps=eps, y=y)
+    dt, shape = x.dtype, x.shape
+    _need(dt in _DT, "dtype must be float32 or bfloat16")
+    _need(len(shape) >= 1, "x must be [..., D]")
+    D, row, f32 = shape[-1], shape[-1:], torch.float32
+    xp, wp, bp = _like("x", x, dt, shape, di), _opt_like("w", w, f32, row, di), _opt_like("b", b, f32, row, di)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _like("y", y, dt, shape, di)
+    st = _lib.load().rapt_layer_norm_fwd(xp, _DT[dt], x.numel() // D if D else 0, D, wp, bp, eps, yp, _handle(di))
+    if st:
+        _lib.check("rapt_layer_norm_fwd", st)
+    return y
+
+
+def rapt_layer_norm_bwd(dy, x, w=None, *, eps=1e-5, need_dx=True, need_dw=True, need_db=True, dx=None, workspace=None,
+                        stream=None):
+    """Gradients of sum(dy y) for rapt_layer_norm_fwd: dy and x [..., D]. Returns (dx, dw, db), dw and db fp32 [D];
+    None for what is not needed. dx may be passed to be written, and may be dy or x itself."""
+    di = dy.get_device()
+    if not _here(di, stream):
+        return _elsewhere(rapt_layer_norm_bwd, di, stream, dy, x, w, eps=eps, need_dx=need_dx, need_dw=need_dw,
+                          need_db=need_db, dx=dx, workspace=workspace)
+    dt, shape = dy.dtype, dy.shape
+    _need(dt in _DT, "dtype must be float32 or bfloat16")
+    _need(len(shape) >= 1, "dy must be [..., D]")
+    D, row, f32 = shape[-1], shape[-1:], torch.float32
+    gp, xp, wp = _like("dy", dy, dt, shape, di), _like("x", x, dt, shape, di), _opt_like("w", w, f32, row, di)
+    T, lib = dy.numel() // D if D else 0, _lib.load()
+    dx, dxp = _out("dx", dx, dy, need_dx, di)
+    dw = torch.empty(row, dtype=f32, device=dy.device) if need_dw else None
+    db = torch.empty(row, dtype=f32, device=dy.device) if need_db else None
+    wsp, wsb, owner = None, 0, None
+    if need_dw or need_db:
+        wsp, wsb, owner = _scratch(lib.rapt_layer_norm_bwd_workspace_size(T, D, _DT[dt]), workspace, dy)
+    st = lib.rapt_layer_norm_bwd(gp, xp, _DT[dt], T, D, wp, eps, dxp, None if dw is None else dw.data_ptr(),
+                                 None if db is None else db.data_ptr(), wsp, wsb, _handle(di))
+    if st:
+        _lib.check("rapt_layer_norm_bwd", st)
+    return dx, dw, db
+
+
 def rapt_layer_fwd(x, w_qkv, w_o, gamma_q, gamma_k, *, heads, eps_norm=1e-6, rope_base=1e4,
                    eps_den=1e-4, pos_offset=0, out=None, dev_status=None, workspace=None,
                    stream=None):

@@ -1,0 +1,273 @@
+// The short causal convolution of every channel over its document's tokens, with its activation (sm_103a):
+//   y[t, c] = act(b[c] + sum_{k<W} w[c, k] x[t - W + 1 + k, c]),  W <= 4.
+//
+// HBM bound: every token is read and written once. A thread owns 16 bytes of channels (8 in bf16, 4 in fp32) and
+// walks kTokens tokens with the last W - 1 of them in registers, the loads of kAhead tokens in flight; the W - 1
+// tokens before its first come from L2, where the tile before has put them. It keeps track of the document that
+// its token is in: at a document's first token the window is that document's carried state. Rows of no whole
+// 16-byte vectors go channel by channel. The last W - 1 inputs of each document are written by CTAs behind the
+// tiles of the same launch.
+#include "ssm.cuh"
+
+namespace rapt {
+namespace {
+
+using namespace ssm;
+
+constexpr int kThreads = 128;
+constexpr int kTokens = 32;
+constexpr int kAhead = 8;
+
+// Channels of a thread: V = 1, or a 16-byte vector.
+template <typename T, int V>
+__device__ __forceinline__ void load(const T* p, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = to_f(*p);
+  } else {
+    widen<T>(*reinterpret_cast<const uint4*>(p), f);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const float (&f)[V]) {
+  if constexpr (V == 1) {
+    *p = from_float<T>(f[0]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = narrow<T>(f);
+  }
+}
+
+// The taps of a thread's channels, [V, W] side by side in w.
+template <int V, int W>
+__device__ __forceinline__ void load_taps(const float* w, const float* bias, int c, float (&taps)[W][V], float (&b)[V]) {
+  float f[V * W];
+  const float* p = w + static_cast<long>(c) * W;
+#pragma unroll
+  for (int i = 0; i < V * W; i += V == 1 ? 1 : 4) {
+    if constexpr (V == 1) {
+      f[i] = p[i];
+    } else {
+      const float4 q = *reinterpret_cast<const float4*>(p + i);
+      f[i] = q.x, f[i + 1] = q.y, f[i + 2] = q.z, f[i + 3] = q.w;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) taps[k][v] = f[v * W + k];
+    b[v] = bias != nullptr ? bias[c + v] : 0.f;
+  }
+}
+template <int V>
+__device__ __forceinline__ void activate(Act act, float (&y)[V]) {
+  float unused[V];
+  if constexpr (V == 1) {
+    act_one<false>(act, y[0], y[0], unused[0]);
+  } else {
+    if (act != Act::None) act_vec<V, false>(act, y, y, unused);
+  }
+}
+
+// The document of row t: the last one that begins at t or before.
+__device__ __forceinline__ int find_doc(const Docs& d, int t) {
+  if (d.cu_seqlens == nullptr) return t / d.doc_len;
+  int lo = 0, hi = d.n_docs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (d.cu_seqlens[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ void bounds(const Docs& d, int doc, int& start, int& end) {
+  if (d.cu_seqlens == nullptr) {
+    start = doc * d.doc_len;
+    end = start + d.doc_len;
+  } else {
+    start = d.cu_seqlens[doc];
+    end = min(d.cu_seqlens[doc + 1], d.total_rows);
+  }
+}
+
+// The last W - 1 inputs of a document.
+template <typename T, int V, int W>
+__device__ __forceinline__ void last_inputs(const ConvArgs& a, long i, int nvec) {
+  const int doc = static_cast<int>(i / nvec), c = static_cast<int>(i % nvec) * V;
+  long row0;
+  int n;
+  const bool good = doc_rows(a.docs, doc, row0, n);
+  if (!good && c == 0 && a.docs.dev_status != nullptr) atomicOr(a.docs.dev_status, 1u);
+  if (!good || a.state_final == nullptr) return;
+  const T* x = static_cast<const T*>(a.x);
+  const T* old = static_cast<const T*>(a.state);
+  T* dst = static_cast<T*>(a.state_final);
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    const int t = n - (W - 1) + k;  // may be before the document
+    float f[V] = {};
+    if (t >= 0) load<T, V>(x + (row0 + t) * a.x_stride + c, f);
+    else if (old != nullptr) load<T, V>(old + (static_cast<long>(doc) * (W - 1) + (t + W - 1)) * a.D + c, f);
+    store<T, V>(dst + (static_cast<long>(doc) * (W - 1) + k) * a.D + c, f);
+  }
+}
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a, int nvec, long tiles, long items) {
+  const long i = static_cast<long>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= items) return;
+  if (i >= tiles) {
+    last_inputs<T, V, W>(a, i - tiles, nvec);
+    return;
+  }
+  const int c = static_cast<int>(i % nvec) * V;
+  const int t0 = static_cast<int>(i / nvec) * kTokens, t1 = min(t0 + kTokens, a.docs.total_rows);
+  const T* x = static_cast<const T*>(a.x) + c;
+  T* out = static_cast<T*>(a.out) + c;
+  float w[W][V], b[V];
+  load_taps<V, W>(a.w, a.bias, c, w, b);
+  int doc = find_doc(a.docs, t0), start, end;
+  bounds(a.docs, doc, start, end);
+  // the W - 1 inputs before token t of the document at hand
+  float win[W - 1][V];
+  const auto carried = [&](int k, float (&f)[V]) {  // row k of the document's state
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = 0.f;
+    if (a.state != nullptr)
+      load<T, V>(static_cast<const T*>(a.state) + (static_cast<long>(doc) * (W - 1) + k) * a.D + c, f);
+  };
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    const int t = t0 - (W - 1) + k;
+    if (start < 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[k][v] = 0.f;
+    } else if (t >= start && t < t0) {
+      load<T, V>(x + t * a.x_stride, win[k]);
+    } else {
+      carried(min(max(t - start + W - 1, 0), W - 2), win[k]);
+    }
+  }
+  for (int t = t0; t < t1; t += kAhead) {
+    float cur[kAhead][V];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (t + j < t1) load<T, V>(x + (t + j) * a.x_stride, cur[j]);
+      else
+#pragma unroll
+        for (int v = 0; v < V; ++v) cur[j][v] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int at = t + j;
+      if (at >= t1) break;
+      if (at >= end && doc + 1 < a.docs.n_docs) {  // the next document that has this token
+        do {
+          ++doc;
+          bounds(a.docs, doc, start, end);
+        } while (at >= end && doc + 1 < a.docs.n_docs);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) carried(k, win[k]);
+      }
+      float y[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        y[v] = b[v];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) y[v] = fmaf(w[k][v], win[k][v], y[v]);
+        y[v] = fmaf(w[W - 1][v], cur[j][v], y[v]);
+      }
+      activate<V>(a.act, y);
+      if (at >= start && at < end) store<T, V>(out + static_cast<long>(at) * a.D, y);
+#pragma unroll
+      for (int k = 0; k + 1 < W - 1; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) win[k][v] = win[k + 1][v];
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[W - 2][v] = cur[j][v];
+    }
+  }
+}
+
+// One token: the window is the state's rows, shifted by the new token.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kThreads)
+    conv_step_kernel(const T* x, long x_stride, const float* w, const float* bias, T* state, T* out, int N, int D,
+                     Act act, int nvec) {
+  const long i = static_cast<long>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= static_cast<long>(N) * nvec) return;
+  const int n = static_cast<int>(i / nvec), c = static_cast<int>(i % nvec) * V;
+  float win[W][V], taps[W][V], y[V];
+  load_taps<V, W>(w, bias, c, taps, y);
+  T* s = state + static_cast<long>(n) * (W - 1) * D + c;
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) load<T, V>(s + static_cast<long>(k) * D, win[k]);
+  load<T, V>(x + n * x_stride + c, win[W - 1]);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int k = 0; k < W; ++k) y[v] = fmaf(taps[k][v], win[k][v], y[v]);
+  activate<V>(act, y);
+  store<T, V>(out + static_cast<long>(n) * D + c, y);
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) store<T, V>(s + static_cast<long>(k) * D, win[k + 1]);
+}
+
+template <typename T, int V, int W>
+cudaError_t go(const ConvArgs& a, cudaStream_t stream) {
+  const int nvec = a.D / V;
+  const long tiles = (static_cast<long>(a.docs.total_rows) + kTokens - 1) / kTokens * nvec;
+  // (documents are looked through for a malformed cu_seqlens, too)
+  const bool ends = a.state_final != nullptr || (a.docs.cu_seqlens != nullptr && a.docs.dev_status != nullptr);
+  const long items = tiles + (ends ? static_cast<long>(a.docs.n_docs) * nvec : 0);
+  if (items == 0) return cudaSuccess;
+  const long grid = (items + kThreads - 1) / kThreads;
+  conv_kernel<T, V, W><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a, nvec, tiles, items);
+  note_launches(1);
+  return cudaGetLastError();
+}
+template <typename T, int V, int W>
+cudaError_t go_step(const void* x, long xs, const float* w, const float* bias, void* state, void* out, int N, int D,
+                    Act act, cudaStream_t stream) {
+  const int nvec = D / V;
+  const long grid = (static_cast<long>(N) * nvec + kThreads - 1) / kThreads;
+  conv_step_kernel<T, V, W><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(
+      static_cast<const T*>(x), xs, w, bias, static_cast<T*>(state), static_cast<T*>(out), N, D, act, nvec);
+  note_launches(1);
+  return cudaGetLastError();
+}
+// Whole vectors: every row and every token of a state begins at a multiple of 16 bytes.
+template <typename T>
+bool whole(int D, long stride) {
+  return D % kVec<T> == 0 && stride % kVec<T> == 0;
+}
+template <typename T>
+cudaError_t pick(const ConvArgs& a, cudaStream_t s) {
+  constexpr int V = kVec<T>;
+  if (whole<T>(a.D, a.x_stride))
+    return a.W == 2 ? go<T, V, 2>(a, s) : a.W == 3 ? go<T, V, 3>(a, s) : go<T, V, 4>(a, s);
+  return a.W == 2 ? go<T, 1, 2>(a, s) : a.W == 3 ? go<T, 1, 3>(a, s) : go<T, 1, 4>(a, s);
+}
+template <typename T>
+cudaError_t pick_step(const void* x, long xs, const float* w, const float* bias, void* st, void* out, int N, int D,
+                      int W, Act act, cudaStream_t s) {
+  constexpr int V = kVec<T>;
+  if (whole<T>(D, xs))
+    return W == 2   ? go_step<T, V, 2>(x, xs, w, bias, st, out, N, D, act, s)
+           : W == 3 ? go_step<T, V, 3>(x, xs, w, bias, st, out, N, D, act, s)
+                    : go_step<T, V, 4>(x, xs, w, bias, st, out, N, D, act, s);
+  return W == 2   ? go_step<T, 1, 2>(x, xs, w, bias, st, out, N, D, act, s)
+         : W == 3 ? go_step<T, 1, 3>(x, xs, w, bias, st, out, N, D, act, s)
+                  : go_step<T, 1, 4>(x, xs, w, bias, st, out, N, D, act, s);
+}
+
+}  // namespace
+
+cudaError_t launch_conv(DType dt, const ConvArgs& a, cudaStream_t stream) {
+  return dt == DType::F32 ? pick<float>(a, stream) : pick<__nv_bfloat16>(a, stream);
+}
+cudaError_t launch_conv_step(DType dt, const void* x, long x_stride, const float* w, const float* bias, void* state,
+                             void* out, int N, int D, int W, Act act, cudaStream_t stream) {
+  return dt == DType::F32 ? pick_step<float>(x, x_stride, w, bias, state, out, N, D, W, act, stream)
+                          : pick_step<__nv_bfloat16>(x, x_stride, w, bias, state, out, N, D, W, act, stream);
+}
+
+}  // namespace rapt

@@ -363,4 +363,81 @@ size_t linear_bwd_ws_bytes(int M, int N, int K, bool dx, bool dw);
 cudaError_t launch_linear_bwd(const void* dy, const void* x, const void* w, void* dx, void* dw, int M, int N, int K,
                               void* ws, uint32_t* dev_status, cudaStream_t stream);
 
+// Documents of a call over rows of tokens: n_docs of doc_len rows each (cu_seqlens == nullptr), or those
+// between cu_seqlens' bounds.
+struct Docs {
+  const int32_t* cu_seqlens;
+  uint32_t* dev_status;  // nullable
+  int n_docs;
+  int doc_len;
+  int total_rows;
+  int max_seqlen;  // bound on a document's length
+};
+
+// The short causal convolution (conv.cu). x has its own row stride; w is [D, W].
+struct ConvArgs {
+  Docs docs;
+  const void* x;
+  long x_stride;
+  const float* w;
+  const float* bias;    // nullable
+  const void* state;    // nullable [n_docs, W - 1, D]
+  void* out;
+  void* state_final;    // nullable [n_docs, W - 1, D]
+  int D, W;
+  Act act;
+};
+cudaError_t launch_conv(DType dt, const ConvArgs& a, cudaStream_t stream);
+// One token of N sequences; state is updated in place.
+cudaError_t launch_conv_step(DType dt, const void* x, long x_stride, const float* w, const float* bias, void* state,
+                             void* out, int N, int D, int W, Act act, cudaStream_t stream);
+
+// The selective scan. The recurrence in fp32 on CUDA cores (ssm_simt.cu), chunks on the tensor cores (ssm_tc.cu,
+// bf16, P and N of 64 or 128), a single token (ssm_step.cu). Documents longer than a segment are cut into nseg
+// segments of seg_len tokens; ws holds a record of N P + kSsmRecTail floats per (document, head, segment): the
+// state increment [N, P] and the decay over the segment.
+struct SsmArgs {
+  Docs docs;
+  const void *x, *dt, *B, *C, *z;  // z nullable
+  long xs, dts, bs, cs, zs;        // elements from token to token
+  const float *A, *D, *dt_bias;    // D and dt_bias nullable
+  const float* S0;                 // nullable [n_docs, H, N, P]
+  float* S_final;                  // nullable
+  void* out;
+  float* ws;
+  int H, P, G, N;
+  bool softplus;
+  int nseg, seg_len;
+  const int* order;  // nullable: documents in the order in which the CTAs take them
+};
+constexpr int kSsmRecTail = 4;
+struct SsmPlan {
+  int nseg, seg_len;
+  size_t ws_bytes;
+};
+bool ssm_tc_supported(DType dt, int P, int N);
+SsmPlan ssm_plan_simt(const SsmArgs& a);
+cudaError_t launch_ssm_simt(DType dt, const SsmArgs& a, cudaStream_t stream);
+SsmPlan ssm_plan_tc(const SsmArgs& a);
+cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t stream);
+// S [rows, H, N, P] is updated in place; docs holds the number of rows alone.
+cudaError_t launch_ssm_step(DType dt, const SsmArgs& a, float* S, cudaStream_t stream);
+
+// Layer norm (layer_norm.cu) over T rows of D columns. Backward: dy is given; part: the column sums' partials,
+// 2 D floats for each CTA, layer_norm_ws_bytes() in all, null where neither sum is asked for.
+struct LayerNormArgs {
+  const void* x;
+  const void* dy;
+  const float* w;  // nullable
+  const float* b;  // nullable
+  void* out;       // y or dx, the latter nullable
+  float* part;
+  long T;
+  int D;
+  float eps;
+};
+size_t layer_norm_ws_bytes(long T, int D, DType dt);
+cudaError_t launch_layer_norm_fwd(DType dt, const LayerNormArgs& a, cudaStream_t stream);
+cudaError_t launch_layer_norm_bwd(DType dt, const LayerNormArgs& a, float* dw, float* db, cudaStream_t stream);
+
 }  // namespace rapt

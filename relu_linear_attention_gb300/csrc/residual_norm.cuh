@@ -450,8 +450,8 @@ size_t ring_bytes(const RowShape& s, int stages, int tensors) {
 }
 
 // `apart`: what the number of rows between a thread's rows is to be a multiple of.
-template <auto KERNEL>
-cudaError_t launch_rows(const ResidualNormArgs& a, const RowShape& s, size_t smem, int most, int apart, int* grid,
+template <auto KERNEL, typename ARGS>
+cudaError_t launch_rows(const ARGS& a, const RowShape& s, size_t smem, int most, int apart, int* grid,
                         cudaStream_t stream) {
   const long slots = s.threads / s.tpr, ctas = (a.T + slots - 1) / slots;
   int per_sm = 1, sms = 0, dev = 0;
