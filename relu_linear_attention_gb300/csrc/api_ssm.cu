@@ -102,8 +102,10 @@ rapt::SsmArgs make_args(const rapt_ssm_inputs* in, const rapt::Docs& docs) {
   return a;
 }
 
+bool on_tensor_cores(const rapt_ssm_inputs* in) { return rapt::ssm_tc_supported(to_dt(in->dtype), in->P, in->Ns); }
+
 rapt::SsmPlan plan(const rapt_ssm_inputs* in, const rapt::SsmArgs& a) {
-  return rapt::ssm_plan_simt(a);
+  return on_tensor_cores(in) ? rapt::ssm_plan_tc(a) : rapt::ssm_plan_simt(a);
 }
 
 rapt_status scan(const rapt_ssm_inputs* in, const rapt::Docs& docs, const float* S0, void* out, float* S_final,
@@ -118,7 +120,8 @@ rapt_status scan(const rapt_ssm_inputs* in, const rapt::Docs& docs, const float*
   a.S0 = S0; a.S_final = S_final; a.out = out;
   a.ws = static_cast<float*>(workspace);
   a.nseg = p.nseg; a.seg_len = p.seg_len;
-  return from_cuda(rapt::launch_ssm_simt(to_dt(in->dtype), a, as_stream(stream)));
+  return from_cuda(on_tensor_cores(in) ? rapt::launch_ssm_tc(a, as_stream(stream))
+                                       : rapt::launch_ssm_simt(to_dt(in->dtype), a, as_stream(stream)));
 }
 
 rapt_status check_norm(rapt_dtype dtype, int32_t T, int32_t D, float eps) {
