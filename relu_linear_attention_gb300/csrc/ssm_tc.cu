@@ -20,12 +20,14 @@
 // e^(that - s_j), one factor a row and block and one a column, both at most 1: no exponential an element, no
 // overflow at any decay. On the diagonal block each element has its own. a_t stops at -160 log 2 (2^-160 is 0).
 //
-// Warps (640 threads, one CTA an SM):
-//   0-7   rows:   G -> M (a TMEM lane quarter and every other block of 32 keys each), then the epilogue of half of
-//                 the tile's columns: y in the place of x in shared memory, from where the TMA stores it;
+// Warps (896 threads, one CTA an SM):
+//   0-7   rows:   step sizes, decays and their sums, a thread a head and token; G -> M, a TMEM lane quarter and every
+//                 other 16 keys each;
 //   8-15  states: the increment into h (fp32, in registers) and its bf16 copy in shared memory, then xw of half of the
-//                 next chunk's tokens (a lane is a column of x);
-//   16    MMA issue, 17 TMA loads and stores, 18-19 step sizes, decays and their sums, one head each.
+//                 next chunk's tokens (a TMEM lane is a column of x);
+//   16-23 ends:   the epilogue of one half of Y (64 columns) after the other, a lane quarter and 32 columns each: Y and x
+//                 are free for what comes next as soon as they are in registers;
+//   24    MMA issue, 25 TMA of B and C, 26 of x (27 idle).
 // Shared memory: two x and two B tiles, one C tile, the state copy, the decay tables. A document is cut into
 // segments where there are fewer units than SMs; kernel A (the same code without reading) gives their increments.
 // Every wait is bounded; one that gives up sets RAPT_DEV_INTERNAL and the CTA winds down.
@@ -34,6 +36,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "ssm.cuh"
 #include "tc_features.cuh"
@@ -46,14 +49,15 @@ namespace {
 using namespace ssm;
 
 constexpr int kC = 128;                       // tokens of a chunk
-constexpr int kRows = 256, kStates = 256;     // threads of the two groups
-constexpr int kThreads = kRows + kStates + 128;
-constexpr int kWarpIssue = (kRows + kStates) / 32, kWarpTma = kWarpIssue + 1, kWarpTab = kWarpIssue + 2;
-constexpr long long kWaitCycles = 2000000000LL;  // ~1 s
+constexpr int kRows = 256, kStates = 256, kEnds = 256;  // threads of the groups
+constexpr int kThreads = kRows + kStates + kEnds + 128;
+constexpr int kWarpIssue = (kRows + kStates + kEnds) / 32, kWarpLoad = kWarpIssue + 1, kWarpX = kWarpIssue + 2;
+constexpr long long kWaitCycles = 1000000000LL;  // ~0.5 s: what is not done by then never will be
 constexpr uint32_t kDevInternal = 2u;
-constexpr int kLaunchRegs = 96, kRegsRows = 104, kRegsStates = 112, kRegsRest = 48;
-static_assert(kRows * kRegsRows + kStates * kRegsStates + 128 * kRegsRest <= kThreads * kLaunchRegs,
+constexpr int kLaunchRegs = 72, kRegsRows = 56, kRegsStates = 104, kRegsEnds = 72, kRegsRest = 40;
+static_assert(kRows * kRegsRows + kStates * kRegsStates + kEnds * kRegsEnds + 128 * kRegsRest <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
+constexpr uint32_t kBarRows = 1, kBarStates = 2, kBarEnds = 3;  // named barriers of the groups
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeastLog = -160.f;  // of a token's decay, base 2
 constexpr float kLeastRow = -64.f;   // of a row's common factor
@@ -63,9 +67,11 @@ template <int N>
 struct Lay {
   static constexpr uint32_t XT = 32768, NT = N / 64 * 16384;
   static constexpr uint32_t X = 0, B = 2 * XT, C = B + 2 * NT, H = C + NT;
-  static constexpr uint32_t TAB = H + NT;  // [2 buffers][p, q, f][2 heads][kC] fp32
-  static constexpr uint32_t TAB1 = 3 * 2 * kC * 4;
-  static constexpr uint32_t BAR = TAB + 2 * TAB1;
+  static constexpr uint32_t TAB = H + NT;  // [2 buffers]: [p, q, f][2 heads][kC] fp32, [2 parts of w][2 heads][kC] bf16
+  static constexpr uint32_t TABW = 3 * 2 * kC * 4, TAB1 = TABW + 2 * 2 * kC * 2;
+  static constexpr uint32_t MASK = TAB + 2 * TAB1;  // [4][32 lanes][4]: bf16 pairs of keys that a lane's row sees
+  static constexpr uint32_t SUMS = MASK + 2048;  // [2 buffers][2 heads][4 blocks]: log2 of the blocks' decays
+  static constexpr uint32_t BAR = SUMS + 64;
   static constexpr int NBAR = 24;
   static constexpr uint32_t MISC = BAR + NBAR * 8;
   static constexpr uint32_t BYTES = MISC + 16;
@@ -83,18 +89,136 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Two bf16 values as floats.
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 __device__ __forceinline__ uint4 lds_v4(const uint8_t* sm, uint32_t off) { return *reinterpret_cast<const uint4*>(sm + off); }
 
-// Sum of the block sums b[from .. to).
-__device__ __forceinline__ float between(const float (&b)[4], int from, int to) {
-  float v = 0.f;
+// Products issued by a converged warp, one elected lane each: the operands stay in uniform registers. (In a branch
+// of one lane a product took 160 cycles to issue in a loop, 64 unrolled; N = 64 from TMEM 48 unrolled, 33 so.)
+// Descriptors are given by their low words; the high one is that of every swizzled tile (8-row groups 1024 bytes
+// apart, version 1, 128-byte swizzle).
+constexpr uint32_t kDescHigh = 64u | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+      " setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 y;\n mov.b64 y, {%2, %5};\n"
+      " setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+
+// One probe of a phase, which may suspend the thread for as long as the hardware likes. (With a time of 20 us to
+// suspend for, the probe becomes a loop of short sleeps: waits then noticed a phase up to 1000 cycles late, and
+// polling took a third of the issue slots; the scan of 16384 tokens x 64 heads: 193 us.)
+__device__ __forceinline__ bool probe(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for a phase; false where that gives up, or the CTA has.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  if (probe(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  for (int i = 1;; ++i) {
+    if (probe(bar, parity)) return true;
+    if ((i & 63) == 0 && ((abort != nullptr && *abort != 0) || clock64() - t0 > kWaitCycles)) return false;
+  }
+}
+// Registers of a thread from here on.
+template <int N>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (N > kLaunchRegs) tc::regs_inc<N>();
+  if constexpr (N < kLaunchRegs) tc::regs_dec<N>();
+}
+// 16 lanes x 16 columns: thread t's value r[2 i + u] goes to lane 8 u + t / 4 and column 4 i + t % 4, which is how a
+// transposing ldmatrix of 8 x 8 bf16 hands out pairs of rows.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// log2 sg_i of row i of lane quarter q4, from a head's sums p inside blocks of 32.
+__device__ __forceinline__ float row_log(const float* p, int i, int q4) {
+  float all = p[i];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) v += k >= from && k < to ? b[k] : 0.f;
-  return v;
+  for (int J = 0; J < 3; ++J) all += J < q4 ? p[32 * J + 31] : 0.f;
+  return fmaxf(all, kLeastRow);
+}
+
+// f times z sigmoid(z) of 16 bf16 values z. (One reciprocal for four, 1 / (a b c d) times the others' products, is
+// five instructions a value more than it saves.)
+__device__ __forceinline__ void gate_by(const uint32_t (&w)[8], float* f) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 z = widen2(w[e]);
+    f[2 * e] *= z.x;
+    f[2 * e + 1] *= z.y;
+    f[2 * e] *= sigmoid_f(z.x);
+    f[2 * e + 1] *= sigmoid_f(z.y);
+  }
+}
+// 32 bytes that nobody reads again.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p));
+}
+
+// 32 bytes, at a multiple of 32 where `sectors`, else of 16.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool sectors) {
+  if (sectors) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 struct Maps {
-  CUtensorMap x, b, c, out;
+  CUtensorMap x, b, c, z;
 };
 
 template <int P, int N, bool READ>
@@ -113,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
   const int doc = a.order != nullptr ? a.order[at_doc] : at_doc;
   const int g = unit / per_group, h0 = g * R + unit % per_group * NH;
   const int nh = min(NH, g * R + R - h0);  // an odd head of a group is alone
+  const int halves = NH == 2 ? nh : 2;     // of the tile's columns
   long row0;
   int n;
   const bool good = doc_rows(a.docs, doc, row0, n);
@@ -132,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
   const uint32_t bars = base + L::BAR;
   const uint32_t b_full = bars, x_full = bars + 16, c_full = bars + 32, tab_full = bars + 40, tab_free = bars + 56;
   const uint32_t g_done = bars + 72, m_ready = bars + 80, h_ready = bars + 88, xw_ready = bars + 96;
-  const uint32_t inc_done = bars + 104, yoff_done = bars + 112, y_done = bars + 120, y_free = bars + 128;
-  const uint32_t staged = bars + 136, drain = bars + 152;
+  const uint32_t inc_done = bars + 104, yoff_done = bars + 112, drain = bars + 120, x_free = bars + 128;
+  const uint32_t y_done = bars + 144, y_free = bars + 160;
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(smem + L::MISC);
   volatile int* const s_abort = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
 
@@ -145,9 +270,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(b_full + 8 * i, 1);
       tc::mbar_init(x_full + 8 * i, 1);
-      tc::mbar_init(tab_full + 8 * i, 32 * NH);
-      tc::mbar_init(tab_free + 8 * i, READ ? kRows + kStates : kStates);
-      tc::mbar_init(staged + 8 * i, kRows);
+      tc::mbar_init(tab_full + 8 * i, kRows);
+      tc::mbar_init(tab_free + 8 * i, READ ? kStates + kEnds : kStates);
+      tc::mbar_init(x_free + 8 * i, kEnds);
+      tc::mbar_init(y_done + 8 * i, 1);
+      tc::mbar_init(y_free + 8 * i, kEnds);
     }
     tc::mbar_init(c_full, 1);
     tc::mbar_init(g_done, 1);
@@ -156,17 +283,28 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     tc::mbar_init(xw_ready, kStates);
     tc::mbar_init(inc_done, 1);
     tc::mbar_init(yoff_done, 1);
-    tc::mbar_init(y_done, 1);
-    tc::mbar_init(y_free, kRows);
     tc::mbar_init(drain, 1);
     tc::mbar_fence_init();
     *s_abort = 0;
+  }
+  if (READ && tid < 512) {  // pair e of keys (2 e, 2 e + 1) for the row of this lane
+    const int l = tid / 4 % 32, e = tid / 128 * 4 + tid % 4;
+    reinterpret_cast<uint32_t*>(smem + L::MASK)[tid] = 2 * e + 1 <= l ? 0xffffffffu : 2 * e <= l ? 0x0000ffffu : 0u;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *s_tmem;
-  const auto wait = [&](uint32_t bar, int parity) { return tc::mbar_wait(bar, parity, kWaitCycles) && *s_abort == 0; };
+  const auto wait = [&](uint32_t bar, int parity) { return wait_phase(bar, parity, s_abort); };
+  // A group of warps: its first one waits, the others at a barrier, where they take no issue slots from those that
+  // compute. False for all of them where the wait gave up.
+  const auto group = [&](uint32_t id, uint32_t threads, bool leader, uint32_t b0, int p0, uint32_t b1, int p1, uint32_t b2, int p2) {
+    int bad = 0;
+    if (leader) bad = !(wait(b0, p0) && (b1 == 0 || wait(b1, p1)) && (b2 == 0 || wait(b2, p2)));
+    return feat::group_sync_or(id, threads, bad) == 0;
+  };
+  // for what is under way, whether or not the CTA has given up
+  const auto last = [&](uint32_t bar, int parity) { wait_phase(bar, parity, nullptr); };
   const auto table = [&](int c, int which, int head) {
     return reinterpret_cast<const float*>(smem + L::TAB + (c & 1) * L::TAB1) + (which * 2 + head) * kC;
   };
@@ -175,143 +313,132 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
 
   if (warp < kRows / 32) {
     // ============================================================ rows
-    tc::regs_inc<kRegsRows>();
+    set_regs<kRegsRows>();
+    // The tables of a chunk: thread (head, token), a warp a block of 32 tokens.
+    const int tk = warp >> 2;
+    const bool tables_mine = tk < NH;
+    const __nv_bfloat16* const dts = static_cast<const __nv_bfloat16*>(a.dt) + row0 * a.dts + h0 + min(tk, nh - 1);
+    const float bias = a.dt_bias != nullptr ? a.dt_bias[h0 + min(tk, nh - 1)] : 0.f, A2 = a.A[h0 + min(tk, nh - 1)] * kLog2e;
+    const auto load_dt = [&](int c) {
+      const int t = c * kC + 32 * q4 + lane;
+      return tables_mine && t < seg_n ? to_f(dts[static_cast<long>(t) * a.dts]) : 0.f;
+    };
+    float raw0 = load_dt(0), raw1 = load_dt(1);  // of the next chunk and the one behind it
+    const auto tables = [&](int c) {
+      const int s = c & 1, t = 32 * q4 + lane;
+      const float d = c * kC + t < seg_n ? step_size(raw0, bias, a.softplus) : 0.f;
+      const float l = fmaxf(d * A2, kLeastLog);
+      raw0 = raw1;
+      raw1 = load_dt(c + 2);
+      // sums inside the block: p up to a token, behind it u
+      float p = l, u = l;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const float x = __shfl_up_sync(0xffffffffu, p, o), y = __shfl_down_sync(0xffffffffu, u, o);
+        if (lane >= o) p += x;
+        if (lane + o < 32) u += y;
+      }
+      const float sum = __shfl_sync(0xffffffffu, p, 31), next = __shfl_down_sync(0xffffffffu, u, 1);
+      u = lane < 31 ? next : 0.f;
+      // the buffer's last readers are done
+      if (c >= 2 && !group(kBarRows, kRows, warp == 0, tab_free + 8 * s, ((c >> 1) + 1) & 1, 0, 0, 0, 0)) return false;
+      float* const sums = reinterpret_cast<float*>(smem + L::SUMS) + 8 * s;
+      if (lane == 0) sums[4 * tk + q4] = sum;
+      tc::named_sync(kBarRows, kRows);
+      if (tables_mine) {
+        const float b1 = sums[4 * tk + 1], b2 = sums[4 * tk + 2], b3 = sums[4 * tk + 3];
+        const float f = ex2(u) * d;
+        const float w = f * ex2(q4 == 0 ? b1 + b2 + b3 : q4 == 1 ? b2 + b3 : q4 == 2 ? b3 : 0.f);
+        float* const dst = reinterpret_cast<float*>(smem + L::TAB + s * L::TAB1) + tk * kC + t;
+        dst[0] = p;
+        dst[2 * kC] = p - lg2(d);  // a step of 0: infinity, whose e^- is 0
+        dst[4 * kC] = f;
+        __nv_bfloat16* const dw = reinterpret_cast<__nv_bfloat16*>(smem + L::TAB + s * L::TAB1 + L::TABW) + tk * kC + t;
+        const __nv_bfloat16 w1 = __float2bfloat16_rn(w);
+        dw[0] = w1;
+        dw[2 * kC] = __float2bfloat16_rn(w - __bfloat162float(w1));
+      }
+      tc::mbar_arrive(tab_full + 8 * s);
+      return true;
+    };
+    bool ok = nchunks == 0 || tables(0);
     if constexpr (READ) {
-      const int hf = warp >> 2;  // keys: the blocks of 32 with this parity; epilogue: this half of the columns
       const int i = 32 * q4 + lane;
-      const int eh = NH == 2 ? hf : 0;               // the head of those columns
-      const bool live = NH == 1 || hf < nh;
-      const int head = h0 + min(eh, nh - 1);
-      const float skip = a.D != nullptr ? a.D[head] : 0.f;
-      const long ecol = static_cast<long>(head) * P + (NH == 1 ? 64 * hf : 0);
-      const __nv_bfloat16* const zg =
-          a.z != nullptr ? static_cast<const __nv_bfloat16*>(a.z) + (row0 + i) * a.zs + ecol : nullptr;
-      __nv_bfloat16* const og =
-          static_cast<__nv_bfloat16*>(a.out) + (row0 + i) * (static_cast<long>(a.H) * P) + ecol;
-      int ok = 1;
       for (int c = 0; c < nchunks; ++c) {
-        const int s = c & 1, ph = (c >> 1) & 1;
-        ok = wait(tab_full + 8 * s, ph);
-        // this row's sums: pl = p_i - log2 sg_i; bs = the block sums
-        float pl[NH], bs[NH][4], sg = 0.f;
+        ok = group(kBarRows, kRows, warp == 0, g_done, c & 1, 0, 0, 0, 0);
+        if (!ok) break;
+        tc::fence_after_sync();
+        float pl[NH], far[NH];  // this row's p_i - log2 sg_i for each head; the same and the blocks up to the keys'
 #pragma unroll
         for (int k = 0; k < NH; ++k) {
           const float* const p = table(c, 0, k);
-#pragma unroll
-          for (int J = 0; J < 4; ++J) bs[k][J] = p[32 * J + 31];
-          const float own = p[i], ls = fmaxf(own + between(bs[k], 0, q4), kLeastRow);
-          pl[k] = own - ls;
-          if (k == eh) sg = ex2(ls);
+          pl[k] = far[k] = p[i] - row_log(p, i, q4);
         }
-        ok = ok && wait(g_done, c & 1);
-        if (__any_sync(0xffffffffu, !ok)) break;  // warp-uniform: TMEM accesses stay converged
-        tc::fence_after_sync();
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const int J = hf + 2 * jj;
-          const uint32_t tg = tmem + tl + L::TG + 32 * J;
+        // 16 keys of every block: their G makes room for the M of both heads
+#pragma unroll 1
+        for (int J = 3; J >= 0; --J) {
+          const int k0 = 32 * J + 16 * (warp >> 2);
+          const uint32_t tg = tmem + tl + L::TG + k0;
+          uint32_t w[NH][8];
           if (J > q4) {
-            uint32_t zero[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) zero[e] = 0u;
-            tc::tmem_st16(tg, zero);
-            if (NH == 2) tc::tmem_st16(tg + 16, zero);
-            continue;
-          }
-          uint32_t u[2][16];
-          tc::tmem_ld16(tg, u[0]);
-          tc::tmem_ld16(tg + 16, u[1]);
-          tc::tmem_wait_ld();
+            for (int k = 0; k < NH; ++k)
 #pragma unroll
-          for (int k = 0; k < NH; ++k) {
-            uint32_t w[16];
+              for (int e = 0; e < 8; ++e) w[k][e] = 0u;
+          } else {
+            uint32_t u[16];
+            tc::tmem_ld16(tg, u);
+            tc::tmem_wait_ld();
+            const auto val = [&](int e) { return __uint_as_float(u[e]); };
             if (J == q4) {
-              const float* const q = table(c, 1, k) + 32 * J;
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(q + e);
-                const float qq[4] = {v.x, v.y, v.z, v.w};
-                float m[4];
+              for (int k = 0; k < NH; ++k) {
+                const float* const q = table(c, 1, k) + k0;
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                  const float x = __uint_as_float(u[e / 16][e % 16 + d]) * ex2(pl[k] - qq[d]);
-                  m[d] = e + d <= lane ? x : 0.f;
+                for (int e = 0; e < 16; e += 4) {
+                  const float4 v = *reinterpret_cast<const float4*>(q + e);
+                  w[k][e / 2] = tc::pack_bf16x2(val(e) * ex2(pl[k] - v.x), val(e + 1) * ex2(pl[k] - v.y));
+                  w[k][e / 2 + 1] = tc::pack_bf16x2(val(e + 2) * ex2(pl[k] - v.z), val(e + 3) * ex2(pl[k] - v.w));
                 }
-                w[e / 2] = tc::pack_bf16x2(m[0], m[1]);
-                w[e / 2 + 1] = tc::pack_bf16x2(m[2], m[3]);
+              }
+#pragma unroll
+              for (int e = 0; e < 8; e += 4) {  // keys behind the row's token: nothing, whatever came out
+                const uint4 keep = lds_v4(smem, L::MASK + (2 * (warp >> 2) + e / 4) * 512 + lane * 16);
+#pragma unroll
+                for (int k = 0; k < NH; ++k)
+                  w[k][e] &= keep.x, w[k][e + 1] &= keep.y, w[k][e + 2] &= keep.z, w[k][e + 3] &= keep.w;
               }
             } else {
-              const float* const f = table(c, 2, k) + 32 * J;
-              const float rf = ex2(pl[k] + between(bs[k], J + 1, q4));
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(f + e);
-                const float2 r2 = make_float2(rf, rf);
-                const float2 m0 = __fmul2_rn(
-                    __fmul2_rn(make_float2(__uint_as_float(u[e / 16][e % 16]), __uint_as_float(u[e / 16][e % 16 + 1])), r2),
-                    make_float2(v.x, v.y));
-                const float2 m1 = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(u[e / 16][e % 16 + 2]),
-                                                                    __uint_as_float(u[e / 16][e % 16 + 3])), r2),
-                                             make_float2(v.z, v.w));
-                w[e / 2] = tc::pack_bf16x2(m0.x, m0.y);
-                w[e / 2 + 1] = tc::pack_bf16x2(m1.x, m1.y);
+              for (int k = 0; k < NH; ++k) {
+                const float* const f = table(c, 2, k) + k0;
+                const float rf = ex2(far[k]);
+                far[k] += table(c, 0, k)[32 * J + 31];
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                  const float4 v = *reinterpret_cast<const float4*>(f + e);
+                  w[k][e / 2] = tc::pack_bf16x2(val(e) * (rf * v.x), val(e + 1) * (rf * v.y));
+                  w[k][e / 2 + 1] = tc::pack_bf16x2(val(e + 2) * (rf * v.z), val(e + 3) * (rf * v.w));
+                }
               }
             }
-            tc::tmem_st16(tg + 16 * k, w);
           }
+#pragma unroll
+          for (int k = 0; k < NH; ++k) tc::tmem_st8(tg + 8 * k, w[k]);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         tc::mbar_arrive(m_ready);
-        tc::mbar_arrive(tab_free + 8 * s);
-        // the epilogue of this row's 64 columns
-        const int lt = c * kC + i;
-        uint4 z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          z[e] = zg != nullptr && live && lt < seg_n
-                     ? __ldg(reinterpret_cast<const uint4*>(zg + static_cast<long>(c) * kC * a.zs) + e)
-                     : make_uint4(0, 0, 0, 0);
-        const bool whole = c * kC + kC <= seg_n;
-        const uint32_t xo = L::X + s * L::XT + hf * 16384;
-        ok = wait(x_full + 8 * s, ph) && wait(y_done, c & 1);
-        if (__any_sync(0xffffffffu, !ok)) break;
-        tc::fence_after_sync();
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t u[2][16];
-          tc::tmem_ld16(tmem + tl + L::TY + 64 * hf + 32 * half, u[0]);
-          tc::tmem_ld16(tmem + tl + L::TY + 64 * hf + 32 * half + 16, u[1]);
-          tc::tmem_wait_ld();
-          if (half == 1) {
-            tc::fence_before_sync();
-            tc::mbar_arrive(y_free);
-          }
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint32_t at = xo + tc::sw128(i, 4 * half + m);
-            float xv[8], zv[8], f[8];
-            widen<__nv_bfloat16>(lds_v4(smem, at), xv);
-            widen<__nv_bfloat16>(z[4 * half + m], zv);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              f[e] = fmaf(sg, __uint_as_float(u[m / 2][m % 2 * 8 + e]), skip * xv[e]);
-              if (zg != nullptr) f[e] *= zv[e] * sigmoid_f(zv[e]);
-            }
-            const uint4 v = narrow<__nv_bfloat16>(f);
-            if (whole) *reinterpret_cast<uint4*>(smem + at) = v;
-            else if (live && lt < seg_n)
-              *reinterpret_cast<uint4*>(og + static_cast<long>(c) * kC * a.H * P + 32 * half + 8 * m) = v;
-          }
-        }
-        if (whole) tc::fence_async_smem();
-        tc::mbar_arrive(staged + 8 * s);
+        if (c + 1 < nchunks) ok = ok && tables(c + 1);
+        if (!ok) break;
       }
-      if (!ok) *s_abort = 1;
+    } else {
+      for (int c = 1; c < nchunks && ok; ++c) ok = tables(c);
     }
+    if (!ok) *s_abort = 1;
   } else if (warp < (kRows + kStates) / 32) {
     // ============================================================ states
-    tc::regs_inc<kRegsStates>();
+    set_regs<kRegsStates>();
     constexpr int HN = N / 2;               // columns n of a thread
     const int half = (warp - kRows / 32) >> 2;
     const int p = 32 * q4 + lane;           // column of the x tile = TMEM lane
@@ -355,8 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     float keep = 1.f, log_all = 0.f;
     // h takes the increment of the chunk before
     const auto update = [&](int c) {
-      const int ok = wait(inc_done, c & 1);
-      if (__any_sync(0xffffffffu, !ok)) return false;
+      if (!group(kBarStates, kStates, warp == kRows / 32, inc_done, c & 1, 0, 0, 0, 0)) return false;
       tc::fence_after_sync();
 #pragma unroll
       for (int m = 0; m < HN / 16; ++m) {
@@ -375,48 +501,41 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
       if (c > 0) {
         ok = update(c - 1);
         if (!ok) break;
-        publish();
+        publish();  // (C h^T of the chunk before came ahead of its increment: its copy has been read)
       }
-      ok = wait(tab_full + 8 * s, ph) && wait(x_full + 8 * s, ph);
-      if (__any_sync(0xffffffffu, !ok)) {
-        ok = false;
-        break;
-      }
+      ok = group(kBarStates, kStates, warp == kRows / 32, tab_full + 8 * s, ph, x_full + 8 * s, ph, 0, 0);
+      if (!ok) break;
       const float* const sums = table(c, 0, k);
-      float bs[4];
-#pragma unroll
-      for (int J = 0; J < 4; ++J) bs[J] = sums[32 * J + 31];
-      const float all = between(bs, 0, 4);
+      const float all = sums[31] + sums[63] + sums[95] + sums[127];
       keep = ex2(all);
       log_all += all;
-      const uint32_t xo = L::X + s * L::XT + (p >> 6) * 16384 + (p & 7) * 2;
-      const int pc = (p & 63) >> 3;
+      // xw of this warp's 32 columns and 64 tokens, two tokens a register as the product wants them: with the weight
+      // in two bf16 parts, w = w1 + w2, hi = bf16(x w1) leaves a remainder that bf16 holds exactly, and
+      // lo = bf16(x w2 + (x w1 - hi)). Three instructions for two values.
+      const uint32_t* const w1 = reinterpret_cast<const uint32_t*>(smem + L::TAB + s * L::TAB1 + L::TABW) + k * (kC / 2);
+      const uint32_t* const w2 = w1 + kC;
+#pragma unroll 2
+      for (int j = 0; j < 4; ++j) {  // 16 columns, 32 tokens
+        const int c16 = 32 * q4 + 16 * (j & 1), t0 = 64 * half + 32 * (j >> 1);
+        // 8 x 8 blocks (tokens t0 + 8 i, columns c16 + 8 u) in the order 2 i + u; this lane's row of one of them
+        const int t = t0 + 8 * (lane >> 4) + (lane & 7), cc = c16 + (lane & 8);
+        const uint32_t from =
+            base + L::X + s * L::XT + (cc >> 6) * 16384 + t * 128 + ((((cc & 63) >> 3) ^ (lane & 7)) << 4);
+        uint32_t x[8], hi[8];
+        ldmatrix_trans(from, x[0], x[1], x[2], x[3]);
+        ldmatrix_trans(from + 16 * 128, x[4], x[5], x[6], x[7]);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {  // 16 tokens: one K step of the product
-        const int t0 = 64 * half + 16 * b;
-        const float after = ex2(between(bs, t0 / 32 + 1, 4));
-        const float* const f = table(c, 2, k) + t0;
-        uint32_t hi[8], lo[8];
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a = w1[t0 / 2 + 4 * i + (lane & 3)], b = w2[t0 / 2 + 4 * i + (lane & 3)];
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 w4 = *reinterpret_cast<const float4*>(f + e);
-          const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-          float v[4];
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const int t = t0 + e + d;
-            const uint16_t raw = *reinterpret_cast<const uint16_t*>(smem + xo + t * 128 + ((pc ^ (t & 7)) << 4));
-            v[d] = __uint_as_float(static_cast<uint32_t>(raw) << 16) * (w[d] * after);
-          }
-#pragma unroll
-          for (int d = 0; d < 4; d += 2) {
-            const uint32_t top = tc::pack_bf16x2(v[d], v[d + 1]);
-            hi[(e + d) / 2] = top;
-            lo[(e + d) / 2] = tc::pack_bf16x2(v[d] - __uint_as_float(top << 16), v[d + 1] - __uint_as_float(top & 0xffff0000u));
+          for (int u = 2 * i; u < 2 * i + 2; ++u) {
+            hi[u] = mul_bf16x2(x[u], a);
+            x[u] = fma_bf16x2(x[u], b, fma_bf16x2(x[u], a, hi[u] ^ 0x80008000u));
           }
         }
-        tc::tmem_st8(tmem + tl + L::TX + t0 / 2, hi);
-        tc::tmem_st8(tmem + tl + L::TX + 64 + t0 / 2, lo);
+        const uint32_t to = tmem + tl + (static_cast<uint32_t>(16 * (j & 1)) << 16) + L::TX + t0 / 2;
+        tmem_st_16x16(to, hi);
+        tmem_st_16x16(to + 64, x);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -438,78 +557,180 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
         for (int e = 0; e < HN; ++e) __stcg(dst + (n0 + e) * P + pl, h[e]);
       }
     }
-  } else {
-    tc::regs_dec<kRegsRest>();  // one call site for the whole warpgroup
-    if (warp == kWarpIssue) {
-      // ========================================================== MMA issue (one thread)
-      if (lane == 0) {
-        constexpr uint32_t kIdTile = tc::idesc_bf16(128, 128, false, false);
-        constexpr uint32_t kIdInc = tc::idesc_bf16(128, N, false, true);
-        constexpr uint32_t kIdY = tc::idesc_bf16(128, P, false, true);
-        bool ok = true;
-        for (int c = 0; c < nchunks; ++c) {
-          const int s = c & 1, ph = (c >> 1) & 1;
-          const uint64_t d_c = tc::desc_sw128(base + L::C, 16, 1024), d_h = tc::desc_sw128(base + L::H, 16, 1024);
-          const uint64_t d_bk = tc::desc_sw128(base + L::B + s * L::NT, 16, 1024);
-          const uint64_t d_bm = tc::desc_sw128(base + L::B + s * L::NT, 16384, 1024);
-          const uint64_t d_x = tc::desc_sw128(base + L::X + s * L::XT, 16384, 1024);
-          ok = wait(b_full + 8 * s, ph);
-          if constexpr (READ) {
-            ok = ok && wait(c_full, c & 1) && wait(x_full + 8 * s, ph);
-            if (!ok) break;
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int k = 0; k < N / 16; ++k) {
-              const uint64_t ko = static_cast<uint64_t>((k / 4) * 1024 + (k % 4) * 2);
-              tc::mma_bf16(tmem + L::TG, d_c + ko, d_bk + ko, kIdTile, k > 0);
-            }
-            tc::mma_commit(g_done);
-            ok = wait(h_ready, c & 1) && (c == 0 || wait(y_free, (c - 1) & 1));
-            if (!ok) break;
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int k = 0; k < N / 16; ++k) {
-              const uint64_t ko = static_cast<uint64_t>((k / 4) * 1024 + (k % 4) * 2);
-              tc::mma_bf16(tmem + L::TY, d_c + ko, d_h + ko, kIdTile, k > 0);
-            }
-            tc::mma_commit(yoff_done);
-          }
-          ok = ok && wait(xw_ready, c & 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-#pragma unroll 1
-          for (int k = 0; k < 16; ++k)  // the high parts of the 128 tokens, then the low ones
-            tc::mma_bf16_ta(tmem + L::TI, tmem + L::TX + 8 * k, d_bm + static_cast<uint64_t>(k & 7) * 128, kIdInc, k > 0);
-          tc::mma_commit(inc_done);
-          if constexpr (READ) {
-            ok = wait(m_ready, c & 1);
-            if (!ok) break;
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int hh = 0; hh < nh; ++hh)
-#pragma unroll 1
-              for (int k = 0; k < kC / 16; ++k)
-                tc::mma_bf16_ta(tmem + L::TY + 64 * hh, tmem + L::TG + 32 * (k / 2) + 16 * hh + 8 * (k % 2),
-                                d_x + static_cast<uint64_t>(hh) * 1024 + static_cast<uint64_t>(k) * 128, kIdY, 1u);
-            tc::mma_commit(y_done);
+  } else if (warp < kWarpIssue) {
+    // ============================================================ ends
+    set_regs<kRegsEnds>();
+    if constexpr (READ) {
+      const int i = 32 * q4 + lane, first = kWarpIssue - kEnds / 32;  // the group's first warp
+      const int hc = 32 * ((warp - first) >> 2);                      // this warp's columns of a half
+      const bool gated = a.z != nullptr;
+      float skip[NH];
+#pragma unroll
+      for (int k = 0; k < NH; ++k) skip[k] = a.D != nullptr ? a.D[h0 + min(k, nh - 1)] : 0.f;
+      // (the columns of a CTA's heads lie side by side)
+      const __nv_bfloat16* zrow =
+          gated ? static_cast<const __nv_bfloat16*>(a.z) + (row0 + i) * a.zs + static_cast<long>(h0) * P + hc : nullptr;
+      // gates of 32 columns; a quarter is fetched again, for the next half of Y, when it has been used. Rows at
+      // multiples of 32 bytes come in whole sectors.
+      uint32_t z[2][8];
+      const bool sectors = gated && (reinterpret_cast<uintptr_t>(a.z) & 31) == 0 && a.zs % 16 == 0;
+      const auto load_z = [&](int b, const __nv_bfloat16* p, bool there) {
+        if (!there) return;  // (what stays there is not stored)
+        if (sectors) {
+          load32(p + 16 * b, z[b]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 16 * b) + e);
+            z[b][4 * e] = v.x, z[b][4 * e + 1] = v.y, z[b][4 * e + 2] = v.z, z[b][4 * e + 3] = v.w;
           }
         }
-        if (!ok) *s_abort = 1;
-        // no product is under way when TMEM and the tiles are given up
-        tc::mma_commit(drain);
-        tc::mbar_wait(drain, 0, kWaitCycles);
+      };
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[b][e] = 0u;
+        if (gated) load_z(b, zrow, i < seg_n);
       }
-    } else if (warp == kWarpTma) {
-      // ========================================================== loads and stores (one thread)
-      if (lane == 0) {
-        const int xc = h0 * P, nc = g * N, row = static_cast<int>(row0);
-        const uint32_t xbytes = (NH == 1 ? 2 : nh) * 16384u;
-        const auto load_x = [&](int c) {
-          tc::mbar_arrive_expect_tx(x_full + 8 * (c & 1), xbytes);
-          for (uint32_t j = 0; j < xbytes / 16384; ++j)
-            tc::tma_load_3d(base + L::X + (c & 1) * L::XT + j * 16384, &maps.x, xc + 64 * j, 0, row + c * kC,
-                            x_full + 8 * (c & 1));
-        };
+      __nv_bfloat16* orow =
+          static_cast<__nv_bfloat16*>(a.out) + ((row0 + i) * a.H + h0) * static_cast<long>(P) + hc;
+      const bool out_sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+      bool ok = true;
+      for (int c = 0; c < nchunks && ok; ++c) {
+        const int s = c & 1, ph = (c >> 1) & 1;
+        const bool mine = c * kC + i < seg_n, more = (c + 1) * kC + i < seg_n;
+        float sg[NH];
+#pragma unroll 1
+        for (int hh = 0; hh < halves; ++hh) {
+          if (hh == 0) {
+            ok = group(kBarEnds, kEnds, warp == first, tab_full + 8 * s, ph, x_full + 8 * s, ph, y_done, c & 1);
+            if (!ok) break;
+#pragma unroll
+            for (int k = 0; k < NH; ++k) sg[k] = ex2(row_log(table(c, 0, k), i, q4));
+            tc::mbar_arrive(tab_free + 8 * s);
+          } else {
+            ok = group(kBarEnds, kEnds, warp == first, y_done + 8, c & 1, 0, 0, 0, 0);
+            if (!ok) break;
+          }
+          tc::fence_after_sync();
+          const float sgk = hh == 0 ? sg[0] : sg[NH - 1], skk = hh == 0 ? skip[0] : skip[NH - 1];
+          uint32_t u[2][16];
+          tc::tmem_ld16(tmem + tl + L::TY + 64 * hh + hc, u[0]);
+          tc::tmem_ld16(tmem + tl + L::TY + 64 * hh + hc + 16, u[1]);
+          tc::tmem_wait_ld();
+          tc::fence_before_sync();
+          tc::mbar_arrive(y_free + 8 * hh);
+          float f[32];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const uint4 x4 = lds_v4(smem, L::X + s * L::XT + hh * 16384 + tc::sw128(i, hc / 8 + b));
+            const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 xv = widen2(xw[e]);
+              const int at = 8 * b + 2 * e;
+              f[at] = fmaf(sgk, __uint_as_float(u[at / 16][at % 16]), skk * xv.x);
+              f[at + 1] = fmaf(sgk, __uint_as_float(u[at / 16][at % 16 + 1]), skk * xv.y);
+            }
+          }
+          if (hh + 1 == halves) tc::mbar_arrive(x_free + 8 * s);
+          const auto finish = [&](auto gate) {
+            constexpr bool kGate = decltype(gate)::value;
+            const __nv_bfloat16* const next = hh + 1 < halves ? zrow + 64 : zrow - 64 * hh + kC * a.zs;
+            const bool there = hh + 1 < halves ? mine : more;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              uint32_t o[8];
+              if constexpr (kGate) gate_by(z[b], f + 16 * b);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = tc::pack_bf16x2(f[16 * b + 2 * e], f[16 * b + 2 * e + 1]);
+              if constexpr (kGate) load_z(b, next, there);
+              if (mine) store32(orow + 64 * hh + 16 * b, o, out_sectors);
+            }
+          };
+          if (gated) {
+            finish(std::true_type{});
+            zrow += hh + 1 < halves ? 64 : kC * a.zs - 64 * hh;
+          } else {
+            finish(std::false_type{});
+          }
+        }
+        orow += static_cast<long>(kC) * a.H * P;
+      }
+      if (!ok) *s_abort = 1;
+    }
+  } else {
+    set_regs<kRegsRest>();  // one call site for the whole warpgroup
+    if (warp == kWarpIssue) {
+      // ========================================================== MMA issue (the whole warp)
+      constexpr uint32_t kIdTile = tc::idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kIdInc = tc::idesc_bf16(128, N, false, true);
+      constexpr uint32_t kIdY = tc::idesc_bf16(128, 64, false, false), kIdMx = tc::idesc_bf16(128, 64, false, true);
+      const auto all = [](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
+      const uint32_t d_c = desc_low(base + L::C, 16), d_h = desc_low(base + L::H, 16);
+      bool ok = true;
+      for (int c = 0; c < nchunks; ++c) {
+        const int s = c & 1, ph = (c >> 1) & 1;
+        const uint32_t d_bk = desc_low(base + L::B + s * L::NT, 16);
+        const uint32_t d_bm = desc_low(base + L::B + s * L::NT, 16384);
+        ok = wait(b_full + 8 * s, ph);
+        if constexpr (READ) {
+          ok = all(ok && wait(c_full, c & 1));
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < N / 16; ++k) {
+            const uint32_t ko = (k / 4) * 1024 + (k % 4) * 2;
+            mma(tmem + L::TG, d_c + ko, d_bk + ko, kIdTile, k > 0);
+          }
+          commit(g_done);
+          ok = all(wait(h_ready, c & 1));
+#pragma unroll 1
+          for (int hh = 0; hh < halves && ok; ++hh) {  // C h^T, 64 columns each
+            ok = all(c == 0 || wait(y_free + 8 * hh, (c - 1) & 1));
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k) {
+              const uint32_t ko = (k / 4) * 1024 + (k % 4) * 2;
+              mma(tmem + L::TY + 64 * hh, d_c + ko, d_h + hh * 512 + ko, kIdY, k > 0);
+            }
+          }
+          if (!ok) break;
+          commit(yoff_done);
+        }
+        ok = all(ok && wait(xw_ready, c & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < 16; ++k)  // the high parts of the 128 tokens, then the low ones
+          mma_ta(tmem + L::TI, tmem + L::TX + 8 * k, d_bm + (k & 7) * 128, kIdInc, k > 0);
+        commit(inc_done);
+        if constexpr (READ) {
+          ok = all(wait(m_ready, c & 1) && wait(x_full + 8 * s, ph));
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t d_x = desc_low(base + L::X + s * L::XT, 16384);
+#pragma unroll 1
+          for (int hh = 0; hh < halves; ++hh) {  // M x
+            const uint32_t tm = tmem + L::TG + (NH == 2 ? 8 * hh : 0);
+#pragma unroll
+            for (int k = 0; k < kC / 16; ++k)
+              mma_ta(tmem + L::TY + 64 * hh, tm + 16 * k, d_x + hh * 1024 + k * 128, kIdMx, 1u);
+            commit(y_done + 8 * hh);
+          }
+        }
+      }
+      if (!ok) *s_abort = 1;
+      // no product is under way when TMEM and the tiles are given up
+      commit(drain);
+      last(drain, 0);
+    } else if (warp == kWarpLoad || warp == kWarpX) {
+      // ========================================================== TMA: one thread for B and C, one for x and out
+      const int xc = h0 * P, nc = g * N, row = static_cast<int>(row0);
+      const uint32_t xbytes = (NH == 1 ? 2 : nh) * 16384u;
+      bool ok = true;
+      if (warp == kWarpLoad && lane == 0) {
         const auto load_b = [&](int c) {
           tc::mbar_arrive_expect_tx(b_full + 8 * (c & 1), L::NT);
           for (int j = 0; j < N / 64; ++j)
@@ -523,15 +744,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
               tc::tma_load_3d(base + L::C + j * 16384, &maps.c, nc + 64 * j, 0, row + c * kC, c_full);
           }
         };
-        int nx = 0, nb = 0, ncl = 0;  // loads issued
-        for (; nb < 2 && nb < nchunks; ++nb, ++nx) {
-          load_b(nb);
-          load_x(nb);
+        int nb = 0, ncl = 0;  // loads issued
+        if (nchunks > 0) {
+          load_b(nb++);
+          if (READ) load_c(ncl++);
+          if (nchunks > 1) load_b(nb++);
         }
-        if (nchunks > 0 && READ) load_c(ncl++);
-        bool ok = true;
-        for (int c = 0; c < nchunks && ok; ++c) {
-          const int s = c & 1, ph = (c >> 1) & 1;
+        for (int c = 0; c < nchunks; ++c) {
           if constexpr (READ) {
             ok = wait(yoff_done, c & 1);
             if (!ok) break;
@@ -540,89 +759,36 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
           ok = wait(inc_done, c & 1);
           if (!ok) break;
           if (c + 2 < nchunks) load_b(nb++);
-          if constexpr (READ) {
-            ok = wait(staged + 8 * s, ph);
-            if (!ok) break;
-            if (c * kC + kC <= seg_n) {  // a whole chunk was staged
-              for (uint32_t j = 0; j < xbytes / 16384; ++j)
-                tc::tma_store_3d(&maps.out, base + L::X + s * L::XT + j * 16384, xc + 64 * j, 0, row + c * kC);
-              tc::bulk_commit();
-              tc::bulk_wait_read0();  // the buffer may be refilled once the store has read it
-            }
-          }
-          if (c + 2 < nchunks) load_x(nx++);  // (without reading: xw came before the increment)
         }
         if (!ok) *s_abort = 1;
-        tc::bulk_wait0();
         if (*s_abort) {  // no copy is under way when the tiles are given up: the last load of each buffer
-          for (int i = 0; i < 2; ++i) {
-            if (nx > i) tc::mbar_wait(x_full + 8 * i, ((nx - 1 - i) >> 1) & 1, kWaitCycles);
-            if (nb > i) tc::mbar_wait(b_full + 8 * i, ((nb - 1 - i) >> 1) & 1, kWaitCycles);
-          }
-          if (ncl > 0) tc::mbar_wait(c_full, (ncl - 1) & 1, kWaitCycles);
+          for (int i = 0; i < 2; ++i)
+            if (nb > i) last(b_full + 8 * i, ((nb - 1 - i) >> 1) & 1);
+          if (ncl > 0) last(c_full, (ncl - 1) & 1);
         }
+      } else if (warp == kWarpX && lane == 0) {
+        const auto load_x = [&](int c) {
+          tc::mbar_arrive_expect_tx(x_full + 8 * (c & 1), xbytes);
+          for (uint32_t j = 0; j < xbytes / 16384; ++j)
+            tc::tma_load_3d(base + L::X + (c & 1) * L::XT + j * 16384, &maps.x, xc + 64 * j, 0, row + c * kC,
+                            x_full + 8 * (c & 1));
+          if (READ && a.z != nullptr)  // the gates into L2: the epilogue's loads are rows of 64 bytes
+            for (uint32_t j = 0; j < xbytes / 16384; ++j) tc::tma_prefetch_3d(&maps.z, xc + 64 * j, 0, row + c * kC);
+        };
+        int nx = 0;
+        for (; nx < 2 && nx < nchunks; ++nx) load_x(nx);
+        for (int c = 0; c < nchunks; ++c) {
+          const int s = c & 1, ph = (c >> 1) & 1;
+          // (without reading: x has been taken before the increment's products)
+          ok = READ ? wait(x_free + 8 * s, ph) : wait(inc_done, c & 1);
+          if (!ok) break;
+          if (c + 2 < nchunks) load_x(nx++);
+        }
+        if (!ok) *s_abort = 1;
+        if (*s_abort)
+          for (int i = 0; i < 2; ++i)
+            if (nx > i) last(x_full + 8 * i, ((nx - 1 - i) >> 1) & 1);
       }
-    } else if (warp - kWarpTab < NH) {
-      // ========================================================== step sizes and decays of a head
-      const int k = warp - kWarpTab, head = h0 + min(k, nh - 1);
-      const float bias = a.dt_bias != nullptr ? a.dt_bias[head] : 0.f, A2 = a.A[head] * kLog2e;
-      const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(a.dt) + row0 * a.dts + head;
-      float raw[4];
-      const auto load = [&](int c) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = c * kC + 4 * lane + e;
-          raw[e] = t < seg_n ? to_f(src[t * a.dts]) : 0.f;
-        }
-      };
-      load(0);
-      bool ok = true;
-      for (int c = 0; c < nchunks; ++c) {
-        const int s = c & 1;
-        float d[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          d[e] = c * kC + 4 * lane + e < seg_n ? step_size(raw[e], bias, a.softplus) : 0.f;
-          l[e] = fmaxf(d[e] * A2, kLeastLog);
-        }
-        load(c + 1);
-        // sums inside the block of 32 tokens (8 lanes): p up to a token, t behind it
-        float p[4], t[4];
-        p[0] = l[0];
-        t[3] = 0.f;
-#pragma unroll
-        for (int e = 1; e < 4; ++e) {
-          p[e] = p[e - 1] + l[e];
-          t[3 - e] = t[4 - e] + l[4 - e];
-        }
-        float up = p[3], down = p[3];
-#pragma unroll
-        for (int o = 1; o < 8; o *= 2) {
-          const float u = __shfl_up_sync(0xffffffffu, up, o, 8), v = __shfl_down_sync(0xffffffffu, down, o, 8);
-          if ((lane & 7) >= o) up += u;
-          if ((lane & 7) + o < 8) down += v;
-        }
-        const float left = __shfl_up_sync(0xffffffffu, up, 1, 8), right = __shfl_down_sync(0xffffffffu, down, 1, 8);
-        const float before = (lane & 7) > 0 ? left : 0.f, behind = (lane & 7) < 7 ? right : 0.f;
-        if (c >= 2) ok = wait(tab_free + 8 * s, ((c >> 1) + 1) & 1);
-        if (__any_sync(0xffffffffu, !ok)) {
-          ok = false;
-          break;
-        }
-        float q[4], f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] += before;
-          q[e] = p[e] - lg2(d[e]);  // a step of 0: infinity, whose e^- is 0
-          f[e] = ex2(t[e] + behind) * d[e];
-        }
-        float* const dst = reinterpret_cast<float*>(smem + L::TAB + s * L::TAB1) + k * kC + 4 * lane;
-        *reinterpret_cast<float4*>(dst) = make_float4(p[0], p[1], p[2], p[3]);
-        *reinterpret_cast<float4*>(dst + 2 * kC) = make_float4(q[0], q[1], q[2], q[3]);
-        *reinterpret_cast<float4*>(dst + 4 * kC) = make_float4(f[0], f[1], f[2], f[3]);
-        tc::mbar_arrive(tab_full + 8 * s);
-      }
-      if (!ok) *s_abort = 1;
     }
   }
 
@@ -679,7 +845,7 @@ cudaError_t both(const SsmArgs& a, cudaStream_t stream) {
     e = make_map(&maps.x, a.x, rows, wide, a.xs);
     if (e == cudaSuccess) e = make_map(&maps.b, a.B, rows, narrow, a.bs);
     if (e == cudaSuccess) e = make_map(&maps.c, a.C, rows, narrow, a.cs);
-    if (e == cudaSuccess) e = make_map(&maps.out, a.out, rows, wide, wide);
+    if (e == cudaSuccess && a.z != nullptr) e = make_map(&maps.z, a.z, rows, wide, a.zs);
   }
   if (e == cudaSuccess && a.nseg > 1) e = go<P, N, false>(a, maps, false, stream);
   return e != cudaSuccess ? e : go<P, N, true>(a, maps, a.nseg > 1, stream);
