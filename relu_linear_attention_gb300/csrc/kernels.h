@@ -418,6 +418,8 @@ struct SsmPlan {
 bool ssm_tc_supported(DType dt, int P, int N);
 SsmPlan ssm_plan_simt(const SsmArgs& a);
 cudaError_t launch_ssm_simt(DType dt, const SsmArgs& a, cudaStream_t stream);
+// Turns the records' increments into the states at the segments' ends (nseg > 1).
+cudaError_t launch_ssm_prefix(const SsmArgs& a, cudaStream_t stream);
 SsmPlan ssm_plan_tc(const SsmArgs& a);
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t stream);
 // S [rows, H, N, P] is updated in place; docs holds the number of rows alone.

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "ssm.cuh"
+#include "tc_utils.cuh"
 
 namespace rapt {
 namespace {
@@ -76,19 +77,15 @@ __global__ void __launch_bounds__(Cfg<T, N, P>::THREADS) ssm_simt_kernel(const S
   const auto row_of = [&](int i) { return ((i / 4) * TN + tn) * 4 + i % 4; };
   constexpr long kRec = N * P + kSsmRecTail;
   if (READ) {
-    if (a.S0 != nullptr) {
+    // (a segment's record holds the state at its end by now)
+    const float* const from = seg > 0           ? a.ws + (dh * (a.nseg - 1) + seg - 1) * kRec
+                              : a.S0 != nullptr ? a.S0 + dh * (N * P)
+                                                : nullptr;
+    if (from != nullptr) {
 #pragma unroll
       for (int i = 0; i < NE; ++i)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) s[i][c] = a.S0[dh * (N * P) + row_of(i) * P + col + c];
-    }
-    for (int j = 0; j < seg; ++j) {
-      const float* rec = a.ws + (dh * (a.nseg - 1) + j) * kRec;
-      const float keep = rec[N * P];
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) s[i][c] = fmaf(keep, s[i][c], rec[row_of(i) * P + col + c]);
+        for (int c = 0; c < NC; ++c) s[i][c] = from[row_of(i) * P + col + c];
     }
   }
 
@@ -240,6 +237,46 @@ __global__ void __launch_bounds__(Cfg<T, N, P>::THREADS) ssm_simt_kernel(const S
   }
 }
 
+// The records of a (document, head)'s segments, increments and decays, become the states at the segments' ends:
+// h_j = decay_j h_{j-1} + increment_j from S0. A thread takes four values through the segments, eight records' loads
+// ahead of their use; the number of segments is the document's own.
+__global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a, int np4) {
+  tc::grid_launch_dependents();
+  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  const long dh = i / np4;
+  const int e = static_cast<int>(i % np4);
+  if (dh >= static_cast<long>(a.docs.n_docs) * a.H) return;
+  long row0;
+  int n;
+  doc_rows(a.docs, static_cast<int>(dh / a.H), row0, n);
+  const int segs = n > 0 ? (n + a.seg_len - 1) / a.seg_len : 1;
+  const long rec = 4L * np4 + kSsmRecTail;
+  float* const base = a.ws + dh * (a.nseg - 1) * rec;
+  float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.S0 != nullptr) h = reinterpret_cast<const float4*>(a.S0)[dh * np4 + e];
+  tc::grid_dep_wait();
+  constexpr int kAhead = 8;
+  for (int j0 = 0; j0 < segs - 1; j0 += kAhead) {
+    float4 inc[kAhead];
+    float keep[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (j0 + j >= segs - 1) break;
+      inc[j] = __ldcg(reinterpret_cast<const float4*>(base + (j0 + j) * rec) + e);
+      keep[j] = __ldcg(base + (j0 + j) * rec + 4 * np4);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (j0 + j >= segs - 1) break;
+      h.x = fmaf(keep[j], h.x, inc[j].x);
+      h.y = fmaf(keep[j], h.y, inc[j].y);
+      h.z = fmaf(keep[j], h.z, inc[j].z);
+      h.w = fmaf(keep[j], h.w, inc[j].w);
+      __stcg(reinterpret_cast<float4*>(base + (j0 + j) * rec) + e, h);
+    }
+  }
+}
+
 template <typename T, int N, int P, bool READ>
 cudaError_t go(const SsmArgs& a, cudaStream_t stream) {
   using C = Cfg<T, N, P>;
@@ -257,7 +294,8 @@ cudaError_t go(const SsmArgs& a, cudaStream_t stream) {
 template <typename T, int N, int P>
 cudaError_t both(const SsmArgs& a, cudaStream_t stream) {
   if (a.nseg > 1) {
-    const cudaError_t e = go<T, N, P, false>(a, stream);
+    cudaError_t e = go<T, N, P, false>(a, stream);
+    if (e == cudaSuccess) e = launch_ssm_prefix(a, stream);
     if (e != cudaSuccess) return e;
   }
   return go<T, N, P, true>(a, stream);
@@ -298,6 +336,23 @@ SsmPlan ssm_plan_simt(const SsmArgs& a) {
   p.nseg = static_cast<int>(std::max<long>((longest + p.seg_len - 1) / p.seg_len, 1));
   p.ws_bytes = static_cast<size_t>(units) * (p.nseg - 1) * (static_cast<size_t>(a.N) * a.P + kSsmRecTail) * 4;
   return p;
+}
+
+cudaError_t launch_ssm_prefix(const SsmArgs& a, cudaStream_t stream) {
+  const int np4 = a.N * a.P / 4;
+  const long items = static_cast<long>(a.docs.n_docs) * a.H * np4;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((items + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;  // behind the increments' kernel, which reads nothing that this one writes
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, ssm_prefix_kernel, a, np4);
+  note_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_ssm_simt(DType dt, const SsmArgs& a, cudaStream_t stream) {

@@ -25,9 +25,11 @@
 //                 other 16 keys each;
 //   8-15  states: the increment into h (fp32, in registers) and its bf16 copy in shared memory, then xw of half of the
 //                 next chunk's tokens (a TMEM lane is a column of x);
-//   16-23 ends:   the epilogue of one half of Y (64 columns) after the other, a lane quarter and 32 columns each: Y and x
-//                 are free for what comes next as soon as they are in registers;
-//   24    MMA issue, 25 TMA of B and C, 26 of x (27 idle).
+//   16-23 ends:   the epilogue of one half of Y (64 columns) after the other, a lane quarter and 32 columns each: Y is
+//                 free for the next chunk's products as soon as it is in registers; y goes where x was in shared
+//                 memory, from where the TMA stores it, and z comes by TMA, half a tile at a time (rows of 64 bytes by
+//                 plain loads and stores kept the load-store unit busy for half of the time);
+//   24    MMA issue, 25 TMA of B and C, 26 of x and the output, 27 of z.
 // Shared memory: two x and two B tiles, one C tile, the state copy, the decay tables. A document is cut into
 // segments where there are fewer units than SMs; kernel A (the same code without reading) gives their increments.
 // Every wait is bounded; one that gives up sets RAPT_DEV_INTERNAL and the CTA winds down.
@@ -51,7 +53,7 @@ using namespace ssm;
 constexpr int kC = 128;                       // tokens of a chunk
 constexpr int kRows = 256, kStates = 256, kEnds = 256;  // threads of the groups
 constexpr int kThreads = kRows + kStates + kEnds + 128;
-constexpr int kWarpIssue = (kRows + kStates + kEnds) / 32, kWarpLoad = kWarpIssue + 1, kWarpX = kWarpIssue + 2;
+constexpr int kWarpIssue = (kRows + kStates + kEnds) / 32, kWarpLoad = kWarpIssue + 1, kWarpX = kWarpIssue + 2, kWarpZ = kWarpIssue + 3;
 constexpr long long kWaitCycles = 1000000000LL;  // ~0.5 s: what is not done by then never will be
 constexpr uint32_t kDevInternal = 2u;
 constexpr int kLaunchRegs = 72, kRegsRows = 56, kRegsStates = 104, kRegsEnds = 72, kRegsRest = 40;
@@ -67,7 +69,8 @@ template <int N>
 struct Lay {
   static constexpr uint32_t XT = 32768, NT = N / 64 * 16384;
   static constexpr uint32_t X = 0, B = 2 * XT, C = B + 2 * NT, H = C + NT;
-  static constexpr uint32_t TAB = H + NT;  // [2 buffers]: [p, q, f][2 heads][kC] fp32, [2 parts of w][2 heads][kC] bf16
+  static constexpr uint32_t Z = H + NT;  // the gates of half a tile's columns
+  static constexpr uint32_t TAB = Z + 16384;  // [2 buffers]: [p, q, f][2 heads][kC] fp32, [2 parts of w][2 heads][kC] bf16
   static constexpr uint32_t TABW = 3 * 2 * kC * 4, TAB1 = TABW + 2 * 2 * kC * 2;
   static constexpr uint32_t MASK = TAB + 2 * TAB1;  // [4][32 lanes][4]: bf16 pairs of keys that a lane's row sees
   static constexpr uint32_t SUMS = MASK + 2048;  // [2 buffers][2 heads][4 blocks]: log2 of the blocks' decays
@@ -93,6 +96,7 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ float2 widen2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
+__device__ __forceinline__ uint32_t pack2(float2 v) { return tc::pack_bf16x2(v.x, v.y); }
 __device__ __forceinline__ uint4 lds_v4(const uint8_t* sm, uint32_t off) { return *reinterpret_cast<const uint4*>(sm + off); }
 
 // Products issued by a converged warp, one elected lane each: the operands stay in uniform registers. (In a branch
@@ -186,39 +190,23 @@ __device__ __forceinline__ float row_log(const float* p, int i, int q4) {
   return fmaxf(all, kLeastRow);
 }
 
-// f times z sigmoid(z) of 16 bf16 values z. (One reciprocal for four, 1 / (a b c d) times the others' products, is
-// five instructions a value more than it saves.)
-__device__ __forceinline__ void gate_by(const uint32_t (&w)[8], float* f) {
+// f times z sigmoid(z) of 8 bf16 values z. (One reciprocal for four, 1 / (a b c d) times the others' products, costs
+// more instructions than it saves.)
+__device__ __forceinline__ void gate_by(const uint4& z4, float2 (&f)[4]) {
+  const uint32_t w[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 z = widen2(w[e]);
-    f[2 * e] *= z.x;
-    f[2 * e + 1] *= z.y;
-    f[2 * e] *= sigmoid_f(z.x);
-    f[2 * e + 1] *= sigmoid_f(z.y);
-  }
-}
-// 32 bytes that nobody reads again.
-__device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p));
-}
-
-// 32 bytes, at a multiple of 32 where `sectors`, else of 16.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool sectors) {
-  if (sectors) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  for (int e = 0; e < 4; ++e) {
+    const float2 z = widen2(w[e]), x = __fmul2_rn(z, make_float2(-kLog2e, -kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+    f[e] = __fmul2_rn(__fmul2_rn(f[e], z), r);
   }
 }
 
 struct Maps {
-  CUtensorMap x, b, c, z;
+  CUtensorMap x, b, c, z, out;
 };
 
 template <int P, int N, bool READ>
@@ -257,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
   const uint32_t bars = base + L::BAR;
   const uint32_t b_full = bars, x_full = bars + 16, c_full = bars + 32, tab_full = bars + 40, tab_free = bars + 56;
   const uint32_t g_done = bars + 72, m_ready = bars + 80, h_ready = bars + 88, xw_ready = bars + 96;
-  const uint32_t inc_done = bars + 104, yoff_done = bars + 112, drain = bars + 120, x_free = bars + 128;
-  const uint32_t y_done = bars + 144, y_free = bars + 160;
+  const uint32_t inc_done = bars + 104, yoff_done = bars + 112, drain = bars + 120, staged = bars + 128;
+  const uint32_t y_done = bars + 144, y_free = bars + 160, z_full = bars + 176, z_free = bars + 184;
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(smem + L::MISC);
   volatile int* const s_abort = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
 
@@ -272,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
       tc::mbar_init(x_full + 8 * i, 1);
       tc::mbar_init(tab_full + 8 * i, kRows);
       tc::mbar_init(tab_free + 8 * i, READ ? kStates + kEnds : kStates);
-      tc::mbar_init(x_free + 8 * i, kEnds);
+      tc::mbar_init(staged + 8 * i, kEnds);
       tc::mbar_init(y_done + 8 * i, 1);
       tc::mbar_init(y_free + 8 * i, kEnds);
     }
@@ -284,6 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     tc::mbar_init(inc_done, 1);
     tc::mbar_init(yoff_done, 1);
     tc::mbar_init(drain, 1);
+    tc::mbar_init(z_full, 1);
+    tc::mbar_init(z_free, kEnds);
     tc::mbar_fence_init();
     *s_abort = 0;
   }
@@ -319,14 +309,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     const bool tables_mine = tk < NH;
     const __nv_bfloat16* const dts = static_cast<const __nv_bfloat16*>(a.dt) + row0 * a.dts + h0 + min(tk, nh - 1);
     const float bias = a.dt_bias != nullptr ? a.dt_bias[h0 + min(tk, nh - 1)] : 0.f, A2 = a.A[h0 + min(tk, nh - 1)] * kLog2e;
-    const auto load_dt = [&](int c) {
+    const auto load_dt = [&](int c) -> uint16_t {  // (as it is: a conversion would wait for it here)
       const int t = c * kC + 32 * q4 + lane;
-      return tables_mine && t < seg_n ? to_f(dts[static_cast<long>(t) * a.dts]) : 0.f;
+      return tables_mine && t < seg_n ? __ldg(reinterpret_cast<const uint16_t*>(dts) + static_cast<long>(t) * a.dts)
+                                      : static_cast<uint16_t>(0);
     };
-    float raw0 = load_dt(0), raw1 = load_dt(1);  // of the next chunk and the one behind it
+    uint16_t raw0 = load_dt(0), raw1 = load_dt(1);  // of the next chunk and the one behind it
     const auto tables = [&](int c) {
       const int s = c & 1, t = 32 * q4 + lane;
-      const float d = c * kC + t < seg_n ? step_size(raw0, bias, a.softplus) : 0.f;
+      const float d = c * kC + t < seg_n 
+                          ? step_size(__uint_as_float(static_cast<uint32_t>(raw0) << 16), bias, a.softplus)
+                          : 0.f;
       const float l = fmaxf(d * A2, kLeastLog);
       raw0 = raw1;
       raw1 = load_dt(c + 2);
@@ -389,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
             uint32_t u[16];
             tc::tmem_ld16(tg, u);
             tc::tmem_wait_ld();
-            const auto val = [&](int e) { return __uint_as_float(u[e]); };
+            const auto val2 = [&](int e) { return make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])); };
             if (J == q4) {
 #pragma unroll
               for (int k = 0; k < NH; ++k) {
@@ -397,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                   const float4 v = *reinterpret_cast<const float4*>(q + e);
-                  w[k][e / 2] = tc::pack_bf16x2(val(e) * ex2(pl[k] - v.x), val(e + 1) * ex2(pl[k] - v.y));
-                  w[k][e / 2 + 1] = tc::pack_bf16x2(val(e + 2) * ex2(pl[k] - v.z), val(e + 3) * ex2(pl[k] - v.w));
+                  w[k][e / 2] = pack2(__fmul2_rn(val2(e), make_float2(ex2(pl[k] - v.x), ex2(pl[k] - v.y))));
+                  w[k][e / 2 + 1] = pack2(__fmul2_rn(val2(e + 2), make_float2(ex2(pl[k] - v.z), ex2(pl[k] - v.w))));
                 }
               }
 #pragma unroll
@@ -413,12 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
               for (int k = 0; k < NH; ++k) {
                 const float* const f = table(c, 2, k) + k0;
                 const float rf = ex2(far[k]);
+                const float2 r2 = make_float2(rf, rf);
                 far[k] += table(c, 0, k)[32 * J + 31];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                   const float4 v = *reinterpret_cast<const float4*>(f + e);
-                  w[k][e / 2] = tc::pack_bf16x2(val(e) * (rf * v.x), val(e + 1) * (rf * v.y));
-                  w[k][e / 2 + 1] = tc::pack_bf16x2(val(e + 2) * (rf * v.z), val(e + 3) * (rf * v.w));
+                  w[k][e / 2] = pack2(__fmul2_rn(val2(e), __fmul2_rn(r2, make_float2(v.x, v.y))));
+                  w[k][e / 2 + 1] = pack2(__fmul2_rn(val2(e + 2), __fmul2_rn(r2, make_float2(v.z, v.w))));
                 }
               }
             }
@@ -447,21 +441,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     const bool live = k < nh;
     const int head = h0 + min(k, nh - 1), n0 = half * HN;
     const long dh = static_cast<long>(doc) * a.H + head;
-    float h[HN];
+    float2 h[HN / 2];
 #pragma unroll
-    for (int e = 0; e < HN; ++e) h[e] = 0.f;
+    for (int e = 0; e < HN / 2; ++e) h[e] = make_float2(0.f, 0.f);
     if constexpr (READ) {
-      if (a.S0 != nullptr) {
-#pragma unroll
-        for (int e = 0; e < HN; ++e) h[e] = a.S0[dh * (N * P) + (n0 + e) * P + pl];
-      }
+      // (a segment's record holds the state at its end by now)
+      const float* const from = seg > 0 ? a.ws + (dh * (a.nseg - 1) + seg - 1) * kRec : a.S0 != nullptr ? a.S0 + dh * (N * P) : nullptr;
       if (seg > 0) tc::grid_dep_wait();
-#pragma unroll 1
-      for (int j = 0; j < seg; ++j) {
-        const float* const rec = a.ws + (dh * (a.nseg - 1) + j) * kRec;
-        const float keep = __ldcg(rec + N * P);
+      if (from != nullptr) {
 #pragma unroll
-        for (int e = 0; e < HN; ++e) h[e] = fmaf(keep, h[e], __ldcg(rec + (n0 + e) * P + pl));
+        for (int e = 0; e < HN / 2; ++e)
+          h[e] = make_float2(__ldcg(from + (n0 + 2 * e) * P + pl), __ldcg(from + (n0 + 2 * e + 1) * P + pl));
       }
     }
     // the bf16 copy [columns p][N] that C h^T reads
@@ -470,10 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
 #pragma unroll
         for (int m = 0; m < HN / 8; ++m) {
           const int col = n0 + 8 * m;
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = h[8 * m + e];
-          *reinterpret_cast<uint4*>(smem + L::H + col / 64 * 16384 + tc::sw128(p, col % 64 / 8)) = narrow<__nv_bfloat16>(f);
+          *reinterpret_cast<uint4*>(smem + L::H + col / 64 * 16384 + tc::sw128(p, col % 64 / 8)) =
+              make_uint4(pack2(h[4 * m]), pack2(h[4 * m + 1]), pack2(h[4 * m + 2]), pack2(h[4 * m + 3]));
         }
         tc::fence_async_smem();
         tc::mbar_arrive(h_ready);
@@ -490,7 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
         tc::tmem_ld16(tmem + tl + L::TI + n0 + 16 * m, u);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) h[16 * m + e] = fmaf(keep, h[16 * m + e], __uint_as_float(u[e]));
+        for (int e = 0; e < 16; e += 2)
+          h[8 * m + e / 2] = __ffma2_rn(make_float2(keep, keep), h[8 * m + e / 2],
+                                        make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])));
       }
       return true;
     };
@@ -554,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
       }
       if (dst != nullptr) {
 #pragma unroll
-        for (int e = 0; e < HN; ++e) __stcg(dst + (n0 + e) * P + pl, h[e]);
+        for (int e = 0; e < HN; ++e) __stcg(dst + (n0 + e) * P + pl, e % 2 == 0 ? h[e / 2].x : h[e / 2].y);
       }
     }
   } else if (warp < kWarpIssue) {
@@ -562,100 +552,73 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     set_regs<kRegsEnds>();
     if constexpr (READ) {
       const int i = 32 * q4 + lane, first = kWarpIssue - kEnds / 32;  // the group's first warp
-      const int hc = 32 * ((warp - first) >> 2);                      // this warp's columns of a half
+      const int j4 = 4 * ((warp - first) >> 2);                       // this warp's 16-byte pieces of a half's rows
       const bool gated = a.z != nullptr;
       float skip[NH];
 #pragma unroll
       for (int k = 0; k < NH; ++k) skip[k] = a.D != nullptr ? a.D[h0 + min(k, nh - 1)] : 0.f;
-      // (the columns of a CTA's heads lie side by side)
-      const __nv_bfloat16* zrow =
-          gated ? static_cast<const __nv_bfloat16*>(a.z) + (row0 + i) * a.zs + static_cast<long>(h0) * P + hc : nullptr;
-      // gates of 32 columns; a quarter is fetched again, for the next half of Y, when it has been used. Rows at
-      // multiples of 32 bytes come in whole sectors.
-      uint32_t z[2][8];
-      const bool sectors = gated && (reinterpret_cast<uintptr_t>(a.z) & 31) == 0 && a.zs % 16 == 0;
-      const auto load_z = [&](int b, const __nv_bfloat16* p, bool there) {
-        if (!there) return;  // (what stays there is not stored)
-        if (sectors) {
-          load32(p + 16 * b, z[b]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 16 * b) + e);
-            z[b][4 * e] = v.x, z[b][4 * e + 1] = v.y, z[b][4 * e + 2] = v.z, z[b][4 * e + 3] = v.w;
-          }
-        }
-      };
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[b][e] = 0u;
-        if (gated) load_z(b, zrow, i < seg_n);
-      }
-      __nv_bfloat16* orow =
-          static_cast<__nv_bfloat16*>(a.out) + ((row0 + i) * a.H + h0) * static_cast<long>(P) + hc;
-      const bool out_sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
       bool ok = true;
       for (int c = 0; c < nchunks && ok; ++c) {
         const int s = c & 1, ph = (c >> 1) & 1;
-        const bool mine = c * kC + i < seg_n, more = (c + 1) * kC + i < seg_n;
-        float sg[NH];
 #pragma unroll 1
         for (int hh = 0; hh < halves; ++hh) {
+          const uint32_t zf = gated ? z_full : 0u;
+          const int zp = (c * halves + hh) & 1;
           if (hh == 0) {
             ok = group(kBarEnds, kEnds, warp == first, tab_full + 8 * s, ph, x_full + 8 * s, ph, y_done, c & 1);
-            if (!ok) break;
-#pragma unroll
-            for (int k = 0; k < NH; ++k) sg[k] = ex2(row_log(table(c, 0, k), i, q4));
-            tc::mbar_arrive(tab_free + 8 * s);
+            if (ok && gated) ok = group(kBarEnds, kEnds, warp == first, zf, zp, 0, 0, 0, 0);
           } else {
-            ok = group(kBarEnds, kEnds, warp == first, y_done + 8, c & 1, 0, 0, 0, 0);
-            if (!ok) break;
+            ok = group(kBarEnds, kEnds, warp == first, y_done + 8, c & 1, zf, zp, 0, 0);
           }
+          if (!ok) break;
           tc::fence_after_sync();
-          const float sgk = hh == 0 ? sg[0] : sg[NH - 1], skk = hh == 0 ? skip[0] : skip[NH - 1];
           uint32_t u[2][16];
-          tc::tmem_ld16(tmem + tl + L::TY + 64 * hh + hc, u[0]);
-          tc::tmem_ld16(tmem + tl + L::TY + 64 * hh + hc + 16, u[1]);
+          tc::tmem_ld16(tmem + tl + L::TY + 64 * hh + 8 * j4, u[0]);
+          tc::tmem_ld16(tmem + tl + L::TY + 64 * hh + 8 * j4 + 16, u[1]);
+          const int k = NH == 2 ? hh : 0;
+          const float sg = ex2(row_log(table(c, 0, k), i, q4)), sk = k == 0 ? skip[0] : skip[NH - 1];
+          const float2 sg2 = make_float2(sg, sg), sk2 = make_float2(sk, sk);
           tc::tmem_wait_ld();
           tc::fence_before_sync();
           tc::mbar_arrive(y_free + 8 * hh);
-          float f[32];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint4 x4 = lds_v4(smem, L::X + s * L::XT + hh * 16384 + tc::sw128(i, hc / 8 + b));
-            const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 xv = widen2(xw[e]);
-              const int at = 8 * b + 2 * e;
-              f[at] = fmaf(sgk, __uint_as_float(u[at / 16][at % 16]), skk * xv.x);
-              f[at + 1] = fmaf(sgk, __uint_as_float(u[at / 16][at % 16 + 1]), skk * xv.y);
-            }
-          }
-          if (hh + 1 == halves) tc::mbar_arrive(x_free + 8 * s);
+          if (hh + 1 == halves) tc::mbar_arrive(tab_free + 8 * s);
           const auto finish = [&](auto gate) {
-            constexpr bool kGate = decltype(gate)::value;
-            const __nv_bfloat16* const next = hh + 1 < halves ? zrow + 64 : zrow - 64 * hh + kC * a.zs;
-            const bool there = hh + 1 < halves ? mine : more;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              uint32_t o[8];
-              if constexpr (kGate) gate_by(z[b], f + 16 * b);
+            for (int b = 0; b < 4; ++b) {  // y in the place of x
+              const uint32_t at = tc::sw128(i, j4 + b), xa = L::X + s * L::XT + hh * 16384 + at;
+              const uint4 x4 = lds_v4(smem, xa);
+              const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
+              float2 f[4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = tc::pack_bf16x2(f[16 * b + 2 * e], f[16 * b + 2 * e + 1]);
-              if constexpr (kGate) load_z(b, next, there);
-              if (mine) store32(orow + 64 * hh + 16 * b, o, out_sectors);
+              for (int e = 0; e < 4; ++e) {
+                const int m = 8 * b + 2 * e;
+                f[e] = __ffma2_rn(sg2, make_float2(__uint_as_float(u[m / 16][m % 16]), __uint_as_float(u[m / 16][m % 16 + 1])),
+                                  __fmul2_rn(sk2, widen2(xw[e])));
+              }
+              if constexpr (decltype(gate)::value) gate_by(lds_v4(smem, L::Z + at), f);
+              *reinterpret_cast<uint4*>(smem + xa) = make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
             }
           };
           if (gated) {
             finish(std::true_type{});
-            zrow += hh + 1 < halves ? 64 : kC * a.zs - 64 * hh;
+            tc::mbar_arrive(z_free);
           } else {
             finish(std::false_type{});
           }
         }
-        orow += static_cast<long>(kC) * a.H * P;
+        if (!ok) break;
+        if (c * kC + kC > seg_n) {  // the ragged end of a document: its rows alone, through the staged tile
+          tc::named_sync(kBarEnds, kEnds);
+          __nv_bfloat16* const out =
+              static_cast<__nv_bfloat16*>(a.out) + ((row0 + c * kC) * a.H + h0) * static_cast<long>(P);
+          for (int e = tid - 32 * first; e < (seg_n - c * kC) * 8 * halves; e += kEnds) {
+            const int r = e / (8 * halves), m = e % (8 * halves);
+            *reinterpret_cast<uint4*>(out + static_cast<long>(r) * a.H * P + 8 * m) =
+                lds_v4(smem, L::X + s * L::XT + (m >> 3) * 16384 + tc::sw128(r, m & 7));
+          }
+        }
+        tc::fence_async_smem();
+        tc::mbar_arrive(staged + 8 * s);
       }
       if (!ok) *s_abort = 1;
     }
@@ -725,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
       // no product is under way when TMEM and the tiles are given up
       commit(drain);
       last(drain, 0);
-    } else if (warp == kWarpLoad || warp == kWarpX) {
-      // ========================================================== TMA: one thread for B and C, one for x and out
+    } else {
+      // ========================================================== TMA: one thread for B and C, for x and out, for z
       const int xc = h0 * P, nc = g * N, row = static_cast<int>(row0);
       const uint32_t xbytes = (NH == 1 ? 2 : nh) * 16384u;
       bool ok = true;
@@ -772,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
           for (uint32_t j = 0; j < xbytes / 16384; ++j)
             tc::tma_load_3d(base + L::X + (c & 1) * L::XT + j * 16384, &maps.x, xc + 64 * j, 0, row + c * kC,
                             x_full + 8 * (c & 1));
-          if (READ && a.z != nullptr)  // the gates into L2: the epilogue's loads are rows of 64 bytes
+          if (READ && a.z != nullptr)  // the gates as far as L2
             for (uint32_t j = 0; j < xbytes / 16384; ++j) tc::tma_prefetch_3d(&maps.z, xc + 64 * j, 0, row + c * kC);
         };
         int nx = 0;
@@ -780,14 +743,31 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
         for (int c = 0; c < nchunks; ++c) {
           const int s = c & 1, ph = (c >> 1) & 1;
           // (without reading: x has been taken before the increment's products)
-          ok = READ ? wait(x_free + 8 * s, ph) : wait(inc_done, c & 1);
+          ok = READ ? wait(staged + 8 * s, ph) : wait(inc_done, c & 1);
           if (!ok) break;
+          if (READ && c * kC + kC <= seg_n) {  // a whole chunk was staged
+            for (uint32_t j = 0; j < xbytes / 16384; ++j)
+              tc::tma_store_3d(&maps.out, base + L::X + s * L::XT + j * 16384, xc + 64 * j, 0, row + c * kC);
+            tc::bulk_commit();
+            tc::bulk_wait_read0();  // the buffer may be refilled once the store has read it
+          }
           if (c + 2 < nchunks) load_x(nx++);
         }
         if (!ok) *s_abort = 1;
+        tc::bulk_wait0();
         if (*s_abort)
           for (int i = 0; i < 2; ++i)
             if (nx > i) last(x_full + 8 * i, ((nx - 1 - i) >> 1) & 1);
+      } else if (READ && warp == kWarpZ && lane == 0 && a.z != nullptr) {
+        int nz = 0;
+        for (; nz < nchunks * halves; ++nz) {
+          if (nz > 0) ok = wait(z_free, (nz - 1) & 1);
+          if (!ok) break;
+          tc::mbar_arrive_expect_tx(z_full, 16384);
+          tc::tma_load_3d(base + L::Z, &maps.z, xc + 64 * (nz % halves), 0, row + nz / halves * kC, z_full);
+        }
+        if (!ok) *s_abort = 1;
+        if (nz > 0 && *s_abort) last(z_full, (nz - 1) & 1);
       }
     }
   }
@@ -846,8 +826,10 @@ cudaError_t both(const SsmArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = make_map(&maps.b, a.B, rows, narrow, a.bs);
     if (e == cudaSuccess) e = make_map(&maps.c, a.C, rows, narrow, a.cs);
     if (e == cudaSuccess && a.z != nullptr) e = make_map(&maps.z, a.z, rows, wide, a.zs);
+    if (e == cudaSuccess) e = make_map(&maps.out, a.out, rows, wide, wide);
   }
   if (e == cudaSuccess && a.nseg > 1) e = go<P, N, false>(a, maps, false, stream);
+  if (e == cudaSuccess && a.nseg > 1) e = launch_ssm_prefix(a, stream);
   return e != cudaSuccess ? e : go<P, N, true>(a, maps, a.nseg > 1, stream);
 }
 
