@@ -91,7 +91,7 @@ rapt_status check_inputs(const rapt_ssm_inputs* in, long long rows, long long do
   return among(out, {in->x, in->dt, in->B, in->C, in->z}) ? RAPT_ERR_INVALID_ARG : RAPT_OK;
 }
 
-rapt::SsmArgs make_args(const rapt_ssm_inputs* in, const rapt::Docs& docs) {
+rapt::SsmArgs make_args(const rapt_ssm_inputs* in, const rapt::Docs& docs, bool packed) {
   rapt::SsmArgs a{};
   a.docs = docs;
   a.x = in->x; a.dt = in->dt; a.B = in->B; a.C = in->C; a.z = in->z;
@@ -99,6 +99,7 @@ rapt::SsmArgs make_args(const rapt_ssm_inputs* in, const rapt::Docs& docs) {
   a.A = in->A; a.D = in->D; a.dt_bias = in->dt_bias;
   a.H = in->H; a.P = in->P; a.G = in->G; a.N = in->Ns;
   a.softplus = in->dt_softplus != 0;
+  a.packed = packed;
   return a;
 }
 
@@ -113,13 +114,13 @@ rapt_status scan(const rapt_ssm_inputs* in, const rapt::Docs& docs, const float*
   if (any_off16({S0, S_final}) || off(docs.dev_status, 4)) return RAPT_ERR_INVALID_ARG;
   if (among(S_final, {S0, in->x, in->dt, in->B, in->C, in->z, out, in->A, in->D, in->dt_bias}) || among(out, {S0}))
     return RAPT_ERR_INVALID_ARG;
-  rapt::SsmArgs a = make_args(in, docs);
+  rapt::SsmArgs a = make_args(in, docs, docs.cu_seqlens != nullptr);
   const rapt::SsmPlan p = plan(in, a);
   if (workspace_bytes < p.ws_bytes || (p.ws_bytes > 0 && (workspace == nullptr || off(workspace, 16))))
     return RAPT_ERR_WORKSPACE;
   a.S0 = S0; a.S_final = S_final; a.out = out;
   a.ws = static_cast<float*>(workspace);
-  a.nseg = p.nseg; a.seg_len = p.seg_len;
+  a.nseg = p.nseg; a.seg_len = p.seg_len; a.sorted = p.sorted;
   return from_cuda(on_tensor_cores(in) ? rapt::launch_ssm_tc(a, as_stream(stream))
                                        : rapt::launch_ssm_simt(to_dt(in->dtype), a, as_stream(stream)));
 }
@@ -168,7 +169,7 @@ rapt_status rapt_conv_decode_step(const void* x, int64_t x_stride, rapt_dtype dt
 
 size_t rapt_ssm_prefill_workspace_size(const rapt_ssm_inputs* in, int32_t B, int32_t L) {
   if (check_shape(in) != RAPT_OK || B < 1 || L < 0 || static_cast<long long>(B) * L > kMostRows) return 0;
-  return plan(in, make_args(in, dense_docs(B, L, nullptr))).ws_bytes;
+  return plan(in, make_args(in, dense_docs(B, L, nullptr), false)).ws_bytes;
 }
 
 rapt_status rapt_ssm_prefill_fwd(const rapt_ssm_inputs* in, int32_t B, int32_t L, const float* S0, void* out,
@@ -185,7 +186,7 @@ rapt_status rapt_ssm_prefill_fwd(const rapt_ssm_inputs* in, int32_t B, int32_t L
 
 size_t rapt_ssm_varlen_workspace_size(const rapt_ssm_inputs* in, int32_t T, int32_t N, int32_t max_seqlen) {
   if (check_shape(in) != RAPT_OK || T < 0 || T > kMostRows || N < 1 || max_seqlen < 0) return 0;
-  return plan(in, make_args(in, {nullptr, nullptr, N, 0, T, max_seqlen < T ? max_seqlen : T})).ws_bytes;
+  return plan(in, make_args(in, {nullptr, nullptr, N, 0, T, max_seqlen < T ? max_seqlen : T}, true)).ws_bytes;
 }
 
 rapt_status rapt_ssm_varlen_fwd(const rapt_ssm_inputs* in, int32_t T, const int32_t* cu_seqlens, int32_t N,
@@ -209,7 +210,7 @@ rapt_status rapt_ssm_decode_step(const rapt_ssm_inputs* in, int32_t N, float* S,
   if (st != RAPT_OK) return st;
   if (S == nullptr || off(S, 16) || among(S, {in->x, in->dt, in->B, in->C, in->z, out, in->A, in->D, in->dt_bias}))
     return RAPT_ERR_INVALID_ARG;
-  rapt::SsmArgs a = make_args(in, dense_docs(N, 1, nullptr));
+  rapt::SsmArgs a = make_args(in, dense_docs(N, 1, nullptr), false);
   a.out = out;
   return from_cuda(rapt::launch_ssm_step(to_dt(in->dtype), a, S, as_stream(stream)));
 }

@@ -407,12 +407,15 @@ struct SsmArgs {
   float* ws;
   int H, P, G, N;
   bool softplus;
+  bool packed;                     // documents of cu_seqlens' lengths
   int nseg, seg_len;
-  const int* order;  // nullable: documents in the order in which the CTAs take them
+  bool sorted;                     // ws holds the documents' order, the longest first, instead of records
+  const int* order;                // nullable: documents in the order in which the CTAs take them
 };
 constexpr int kSsmRecTail = 4;
 struct SsmPlan {
   int nseg, seg_len;
+  bool sorted;
   size_t ws_bytes;
 };
 bool ssm_tc_supported(DType dt, int P, int N);

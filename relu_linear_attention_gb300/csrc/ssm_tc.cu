@@ -56,7 +56,7 @@ constexpr int kThreads = kRows + kStates + kEnds + 128;
 constexpr int kWarpIssue = (kRows + kStates + kEnds) / 32, kWarpLoad = kWarpIssue + 1, kWarpX = kWarpIssue + 2, kWarpZ = kWarpIssue + 3;
 constexpr long long kWaitCycles = 1000000000LL;  // ~0.5 s: what is not done by then never will be
 constexpr uint32_t kDevInternal = 2u;
-constexpr int kLaunchRegs = 72, kRegsRows = 56, kRegsStates = 104, kRegsEnds = 72, kRegsRest = 40;
+constexpr int kLaunchRegs = 72, kRegsRows = 56, kRegsStates = 96, kRegsEnds = 80, kRegsRest = 40;
 static_assert(kRows * kRegsRows + kStates * kRegsStates + kEnds * kRegsEnds + 128 * kRegsRest <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kBarRows = 1, kBarStates = 2, kBarEnds = 3;  // named barriers of the groups
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
       // lo = bf16(x w2 + (x w1 - hi)). Three instructions for two values.
       const uint32_t* const w1 = reinterpret_cast<const uint32_t*>(smem + L::TAB + s * L::TAB1 + L::TABW) + k * (kC / 2);
       const uint32_t* const w2 = w1 + kC;
-#pragma unroll 2
+#pragma unroll 1
       for (int j = 0; j < 4; ++j) {  // 16 columns, 32 tokens
         const int c16 = 32 * q4 + 16 * (j & 1), t0 = 64 * half + 32 * (j >> 1);
         // 8 x 8 blocks (tokens t0 + 8 i, columns c16 + 8 u) in the order 2 i + u; this lane's row of one of them
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
           ok = all(ok && wait(c_full, c & 1));
           if (!ok) break;
           tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 4
           for (int k = 0; k < N / 16; ++k) {
             const uint32_t ko = (k / 4) * 1024 + (k % 4) * 2;
             mma(tmem + L::TG, d_c + ko, d_bk + ko, kIdTile, k > 0);
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
             ok = all(c == 0 || wait(y_free + 8 * hh, (c - 1) & 1));
             if (!ok) break;
             tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 4
             for (int k = 0; k < N / 16; ++k) {
               const uint32_t ko = (k / 4) * 1024 + (k % 4) * 2;
               mma(tmem + L::TY + 64 * hh, d_c + ko, d_h + hh * 512 + ko, kIdY, k > 0);
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
         ok = all(ok && wait(xw_ready, c & 1));
         if (!ok) break;
         tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < 16; ++k)  // the high parts of the 128 tokens, then the low ones
           mma_ta(tmem + L::TI, tmem + L::TX + 8 * k, d_bm + (k & 7) * 128, kIdInc, k > 0);
         commit(inc_done);
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
 #pragma unroll 1
           for (int hh = 0; hh < halves; ++hh) {  // M x
             const uint32_t tm = tmem + L::TG + (NH == 2 ? 8 * hh : 0);
-#pragma unroll
+#pragma unroll 4
             for (int k = 0; k < kC / 16; ++k)
               mma_ta(tmem + L::TY + 64 * hh, tm + 16 * k, d_x + hh * 1024 + k * 128, kIdMx, 1u);
             commit(y_done + 8 * hh);
@@ -816,7 +816,13 @@ cudaError_t go(const SsmArgs& a, const Maps& maps, bool dependent, cudaStream_t 
 }
 
 template <int P, int N>
-cudaError_t both(const SsmArgs& a, cudaStream_t stream) {
+cudaError_t both(SsmArgs a, cudaStream_t stream) {
+  if (a.sorted) {
+    int* const order = reinterpret_cast<int*>(a.ws);
+    const cudaError_t e = launch_doc_order(a.docs.cu_seqlens, a.docs.n_docs, a.docs.total_rows, order, stream);
+    if (e != cudaSuccess) return e;
+    a.order = order;
+  }
   Maps maps;
   memset(&maps, 0, sizeof(maps));  // no rows: the kernels issue no copy
   const long rows = a.docs.total_rows, wide = static_cast<long>(a.H) * P, narrow = static_cast<long>(a.G) * N;
@@ -840,7 +846,9 @@ bool ssm_tc_supported(DType dt, int P, int N) {
 }
 
 // Segments of a document, by an estimate in units of one chunk of the scan: waves of one CTA an SM, each its chunks
-// and 1.5 of set-up; kernel A's chunks cost 0.6. A longer plan has to be 5 % faster.
+// and 1.5 of set-up; kernel A's chunks cost 0.6. A longer plan has to be 5 % faster. Packed documents whole, the
+// longest first, take the longest one's time or their share of an SM, whichever is more (65536 tokens x 32 heads of 64
+// in documents of 128 to 8192: cut 373 us, whole and sorted 270).
 SsmPlan ssm_plan_tc(const SsmArgs& a) {
   const int NH = a.P == 64 ? 2 : 1, R = a.H / a.G;
   const long units = static_cast<long>(a.G) * ((R + NH - 1) / NH);
@@ -861,7 +869,16 @@ SsmPlan ssm_plan_tc(const SsmArgs& a) {
       best.seg_len = static_cast<int>(len) * kC;
     }
   }
+  if (a.packed && docs <= 1024) {
+    const double each = units * (static_cast<double>(a.docs.total_rows) / kC + 0.5 * docs) / 152.0;
+    if (std::max(static_cast<double>(longest), each) + 2.5 < best_cost) {
+      best.nseg = 1;
+      best.seg_len = static_cast<int>(longest) * kC;
+      best.sorted = docs > 1;
+    }
+  }
   best.ws_bytes = static_cast<size_t>(docs) * a.H * (best.nseg - 1) * (static_cast<size_t>(a.N) * a.P + kSsmRecTail) * 4;
+  if (best.sorted) best.ws_bytes = static_cast<size_t>(docs) * sizeof(int);  // (a whole document has no records)
   return best;
 }
 
