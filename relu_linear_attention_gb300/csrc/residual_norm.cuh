@@ -73,8 +73,8 @@ enum class Rows { Whole, Shifted };
 // Thread tx of a row's tpr owns 4 NC columns, as 16-byte pieces: piece i starts at column
 // (i tpr + tx) kPer - shift, so that a warp's accesses are contiguous. RING false: no ring (the rows are
 // too wide for one); what would be read there is read from the row itself. Rows are given by the address
-// of column 0.
-template <typename T, Rows R, int NC, bool RING>
+// of column 0. FULL: whole rows with D = 4 NC tpr, so that no piece needs a check.
+template <typename T, Rows R, int NC, bool RING, bool FULL = false>
 struct Cols {
   static constexpr int kBytes = 16;                // of a piece
   static constexpr int kPer = kBytes / sizeof(T);  // columns of a piece
@@ -105,7 +105,9 @@ struct Cols {
   __device__ __forceinline__ bool whole(int i) const {
     return R == Rows::Whole || (col(i) >= 0 && col(i) + kPer <= D);
   }
-  __device__ __forceinline__ bool has(int e) const { return static_cast<unsigned>(e) < static_cast<unsigned>(D); }
+  __device__ __forceinline__ bool has(int e) const {
+    return FULL || static_cast<unsigned>(e) < static_cast<unsigned>(D);
+  }
   // Place of piece i of tensor slot k, given this thread's first place in a stage.
   __device__ __forceinline__ uint8_t* at(uint8_t* stage, int k, int i) const { return stage + (k * kPieces + i) * pitch; }
   // Zeros in a tensor slot that nothing is copied to.
@@ -121,7 +123,7 @@ struct Cols {
 #pragma unroll
     for (int i = 0; i < (RING ? kPieces : 0); ++i) {
       const int e = col(i);
-      if (e >= D) continue;
+      if (!FULL && e >= D) continue;
       const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(at(stage, k, i)));
       if (R == Rows::Whole || e + kPer <= D)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + e) : "memory");
@@ -188,7 +190,7 @@ struct Cols {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int e = col(i);
-      if (e >= D) continue;
+      if (!FULL && e >= D) continue;
       const float* q = v + i * kPer;
       if constexpr (sizeof(T) == 4) {
         if (whole(i)) {
