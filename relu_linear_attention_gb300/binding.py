@@ -572,13 +572,16 @@ def _rows(name, t, dtype, lead, tail, index):
     """(address, elements from row to row) of t, [*lead, *tail] on CUDA device `index`: a row's values lie side by
     side and the rows at one stride, so that the columns of a wider matrix are taken as they are."""
     shape = lead + tail
-    _need(t.dtype is dtype, "%s must be %s, got %s" % (name, dtype, t.dtype))
-    _need(t.shape == shape, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    _need(t.get_device() == index >= 0, "%s must be on cuda:%d, got %s" % (name, index, t.device))
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0:
+        raise ValueError("%s must be %s %s on cuda:%d, got %s %s on %s" % (name, dtype, tuple(shape), index, t.dtype,
+                                                                           tuple(t.shape), t.device))
     st, width, k = t.stride(), 1, len(lead)
-    for i in range(len(shape) - 1, k - 1, -1):
-        _need(st[i] == width or shape[i] <= 1, "%s: a token's values must lie side by side" % name)
-        width *= shape[i]
+    for n, by in zip(reversed(tail), reversed(st)):
+        if by != width and n > 1:
+            raise ValueError("%s: a token's values must lie side by side" % name)
+        width *= n
+    if k == 1:
+        return t.data_ptr(), st[0] if shape[0] > 1 else width
     step = rows = None
     for i in range(k - 1, -1, -1):
         n = shape[i]
@@ -587,7 +590,8 @@ def _rows(name, t, dtype, lead, tail, index):
         if n > 1:
             if step is None:
                 step, rows = st[i], 1
-            _need(st[i] == step * rows, "%s: its tokens must lie at one stride" % name)
+            if st[i] != step * rows:
+                raise ValueError("%s: its tokens must lie at one stride" % name)
             rows *= n
     return t.data_ptr(), width if step is None else step
 
