@@ -75,20 +75,6 @@ __global__ void __launch_bounds__(Cfg<T, N, P>::THREADS) ssm_simt_kernel(const S
     for (int c = 0; c < NC; ++c) s[i][c] = 0.f;
   // row of S of this lane's element i: four consecutive ones, then those of the other lanes
   const auto row_of = [&](int i) { return ((i / 4) * TN + tn) * 4 + i % 4; };
-  constexpr long kRec = N * P + kSsmRecTail;
-  if (READ) {
-    // (a segment's record holds the state at its end by now)
-    const float* const from = seg > 0           ? a.ws + (dh * (a.nseg - 1) + seg - 1) * kRec
-                              : a.S0 != nullptr ? a.S0 + dh * (N * P)
-                                                : nullptr;
-    if (from != nullptr) {
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) s[i][c] = from[row_of(i) * P + col + c];
-    }
-  }
-
   const T* const xg = static_cast<const T*>(a.x) + row0 * a.xs + static_cast<long>(h) * P;
   const T* const bg = static_cast<const T*>(a.B) + row0 * a.bs + static_cast<long>(g) * N;
   const T* const cg = static_cast<const T*>(a.C) + row0 * a.cs + static_cast<long>(g) * N;
@@ -117,6 +103,19 @@ __global__ void __launch_bounds__(Cfg<T, N, P>::THREADS) ssm_simt_kernel(const S
   for (int i = 0; i < kStages - 1; ++i) {
     if (i * kTokens < len) fetch(i * kTokens);
     asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  constexpr long kRec = N * P + kSsmRecTail;
+  if (READ) {
+    if (a.nseg > 1) tc::grid_dep_wait();  // a segment's record holds the state at its end by now
+    const float* const from = seg > 0           ? a.ws + (dh * (a.nseg - 1) + seg - 1) * kRec
+                              : a.S0 != nullptr ? a.S0 + dh * (N * P)
+                                                : nullptr;
+    if (from != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) s[i][c] = from[row_of(i) * P + col + c];
+    }
   }
   const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.f, A = a.A[h];
   const float skip = READ && a.D != nullptr ? a.D[h] : 0.f;
@@ -287,9 +286,19 @@ cudaError_t go(const SsmArgs& a, cudaStream_t stream) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
   }
-  ssm_simt_kernel<T, N, P, READ><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, stream>>>(a);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = READ && a.nseg > 1 ? 1 : 0;  // behind the prefix kernel alone: inputs are read before it ends
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, ssm_simt_kernel<T, N, P, READ>, a);
   note_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <typename T, int N, int P>
 cudaError_t both(const SsmArgs& a, cudaStream_t stream) {
@@ -323,12 +332,14 @@ cudaError_t by_n(const SsmArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Segments: as many as give the GPU about 16 warps an SM, none shorter than 256 tokens.
+// Segments: as many as give the GPU about 16 warps an SM, none shorter than 96 tokens (3 x 1531 tokens x 24 heads of
+// 32, N = 16, fp32: 39 us; 68 with 256 tokens, whose few warps wait for their own arithmetic, 43 with 64, whose CTAs
+// no longer fit the SMs at once).
 SsmPlan ssm_plan_simt(const SsmArgs& a) {
   const int warps = std::max(1, a.P / (a.N <= 32 ? (a.P >= 32 ? 32 : 16) : 16));
   const long units = static_cast<long>(a.docs.n_docs) * a.H, longest = a.docs.max_seqlen;
   const long want = 152L * 16 / warps;
-  long nseg = std::min<long>({(want + units - 1) / units, (longest + 255) / 256, 32});
+  long nseg = std::min<long>({(want + units - 1) / units, (longest + 95) / 96, 64});
   nseg = std::max<long>(nseg, 1);
   SsmPlan p{};
   p.seg_len = static_cast<int>((longest + nseg - 1) / nseg + kTokens - 1) / kTokens * kTokens;
