@@ -614,12 +614,14 @@ typedef struct rapt_ssm_inputs {
  *   S0, S_final  nullable fp32 [documents, H, Ns, P]: the state before and after (they may not alias).
  *   out          [rows, H, P] of `dtype`, contiguous; aliases no input.
  *   workspace    at least the matching *_workspace_size() bytes, 16-byte aligned: state increments and decays of
- *                the segments that long documents are cut into. in's pointers are not looked at by the query.
+ *                the segments that long documents are cut into, or the documents' order by length. in's pointers are
+ *                not looked at by the query.
  *   cu_seqlens, N, max_seqlen, dev_status as for rapt_varlen_fwd.
  * fp32 inputs, and P or Ns below 64: the recurrence in fp32. bf16 with P and Ns of 64 or 128: chunks of 128 tokens
  * on the tensor cores with fp32 accumulation; the decayed scores C_t . B_i and the state that C reads are
  * rounded to bf16, decays, step sizes and the states themselves are fp32 (the state's increments are products of
- * B, exact, with dt x under its decay in two bf16 parts, 16 bits).
+ * B, exact, with dt x under its decay in two bf16 parts, 16 bits); where the decay from a chunk's start to a token
+ * is below 2^-64, the state before the chunk counts 2^-64 for it.
  * Requirements: B >= 1, L >= 0 (0 writes S_final alone), rows <= 2^30, documents * H < 2^25.
  */
 size_t rapt_ssm_prefill_workspace_size(const rapt_ssm_inputs* in, int32_t B, int32_t L);
@@ -641,8 +643,8 @@ rapt_status rapt_ssm_decode_step(const rapt_ssm_inputs* in, int32_t N, float* S,
  *   dx = (var + eps)^(-1/2) (w dy - mean(w dy) - xh mean(w dy xh)),  dw = sum over rows of dy xh,  db = of dy.
  *   dx nullable [T, D], may be dy or x itself; dw and db nullable fp32 [D] (zeros for T = 0).
  *   workspace rapt_layer_norm_bwd_workspace_size() bytes, 16-byte aligned, where dw or db is asked for.
- * All arithmetic is fp32, the variance from differences to the mean; one rounding. The column sums have a fixed
- * order: the same bits every time on the same GPU model. Requirements as for rapt_residual_norm_fwd.
+ * All arithmetic is fp32, the variance from differences to the mean; one rounding. A row's sums (of x, of squared
+ * differences) have to be in fp32's range. The column sums have a fixed order: the same bits every time on the same GPU model. Requirements as for rapt_residual_norm_fwd.
  */
 rapt_status rapt_layer_norm_fwd(const void* x, rapt_dtype dtype, int32_t T, int32_t D, const float* w,
                                 const float* b, float eps, void* y, rapt_stream_t stream);

@@ -30,13 +30,14 @@
 //                 memory, from where the TMA stores it, and z comes by TMA, half a tile at a time (rows of 64 bytes by
 //                 plain loads and stores kept the load-store unit busy for half of the time);
 //   24    MMA issue, 25 TMA of B and C, 26 of x and the output, 27 of z.
-// Shared memory: two x and two B tiles, one C tile, the state copy, half a tile of gates, the decay tables. A document is cut into
-// segments where there are fewer units than SMs; kernel A (the same code without reading) gives their increments.
+// Shared memory: two x and two B tiles, one C tile, the state copy, half a tile of gates, the decay tables. A document
+// is cut into segments where there are fewer units than SMs; kernel A (the same code without reading) gives their
+// increments.
 // Every wait is bounded; one that gives up sets RAPT_DEV_INTERNAL and the CTA winds down.
 //
 // 4 x 4096 tokens x 64 heads of 64, N = 128: 149 us (the bytes alone 62, the products 47); 65536 packed tokens x 32
-// heads of 64, N = 64: 270 us; 32768 tokens x 16 heads of 128, N = 128: 178 us in 9 segments. What bounds it is a chunk's
-// chain, 9 thousand cycles: the state and its copy wait for the increment, the rows for G, the epilogue for Y, one
+// heads of 64, N = 64: 270 us; 32768 tokens x 16 heads of 128, N = 128: 178 us in segments. What bounds it is a
+// chunk's chain, 9 thousand cycles: the state and its copy wait for the increment, the rows for G, the epilogue for Y, one
 // after the other; the tensor pipe is busy for a third of it and the issue slots for half.
 #include <cuda.h>
 
