@@ -220,7 +220,7 @@ rapt_status rapt_layer_norm_fwd(const void* x, rapt_dtype dtype, int32_t T, int3
   const rapt_status st = check_norm(dtype, T, D, eps);
   if (st != RAPT_OK) return st;
   if (T == 0) return RAPT_OK;
-  if (any_null({x, y}) || any_off16({x, w, b, y})) return RAPT_ERR_INVALID_ARG;
+  if (any_null({x, y}) || any_off16({x, w, b, y}) || among(y, {w, b})) return RAPT_ERR_INVALID_ARG;
   rapt::LayerNormArgs a{};
   a.x = x; a.w = w; a.b = b; a.out = y;
   a.T = T; a.D = D; a.eps = eps;

@@ -266,13 +266,16 @@ __global__ void __launch_bounds__(1024)
   out[c] = t;
 }
 
+// CTAs of a backward at most: 32 columns a thread take 168 registers and more.
+inline int parts(const RowShape& s) { return s.ept == 32 ? 160 * std::max(1, 384 / s.threads) : max_parts(s); }
+
 template <bool BWD, typename T, Rows R, int NC, int STAGES, int MAXT, int MINB, bool FULL = false>
 cudaError_t go(const LayerNormArgs& a, const RowShape& s, int* grid, cudaStream_t stream) {
   size_t smem = ring_bytes<T, R, NC>(s, STAGES, BWD ? 2 : 1);
   // the slots' column sums meet where the ring was
   if (BWD && s.tpr <= 32) smem = std::max(smem, static_cast<size_t>(s.threads / s.tpr) * 2 * a.D * 4);
   return launch_rows<layer_norm_kernel<BWD, T, R, NC, STAGES, MAXT, MINB, FULL>>(
-      a, s, smem, BWD ? max_parts(s) : 1 << 30, kMore<T, R> + 1, grid, stream);
+      a, s, smem, BWD ? parts(s) : 1 << 30, kMore<T, R> + 1, grid, stream);
 }
 // Columns a thread. 128 MiB a tensor, us: backward with 32 where the row is 32 times its threads, else 16: bf16
 // D = 2048 76 / 83, 4096 80 / 97, 8192 108 / 117. Forward, bf16: 6144 66 with 16, 83 with 24; 8192 72 with 24, 74
@@ -321,7 +324,7 @@ size_t layer_norm_ws_bytes(long T, int D, DType dt) {
   const int vec = dt == DType::F32 ? kVec<float> : kVec<__nv_bfloat16>;
   const RowShape s = shape(D, D % vec == 0 ? 0 : vec - 1, true);
   const long slots = s.threads / s.tpr;
-  return static_cast<size_t>(std::min<long>((T + slots - 1) / slots, max_parts(s))) * 2 * D * 4;
+  return static_cast<size_t>(std::min<long>((T + slots - 1) / slots, parts(s))) * 2 * D * 4;
 }
 
 cudaError_t launch_layer_norm_fwd(DType dt, const LayerNormArgs& a, cudaStream_t stream) {

@@ -118,7 +118,8 @@ def test_conv_without_tokens_does_nothing(lib):
 
 @pytest.mark.parametrize("at,v,code", [
     (0, None, BAD), (0, P[0] + 2, BAD), (1, 5, NOT), (2, -1, BAD), (3, 0, BAD), (3, 16385, NOT), (4, P[1] + 4, BAD),
-    (5, P[2] + 4, BAD), (6, 0.0, BAD), (6, float("nan"), BAD), (6, 1e-39, BAD), (7, None, BAD), (7, P[3] + 4, BAD)])
+    (5, P[2] + 4, BAD), (6, 0.0, BAD), (6, float("nan"), BAD), (6, 1e-39, BAD), (7, None, BAD), (7, P[3] + 4, BAD),
+    (7, P[1], BAD), (7, P[2], BAD)])
 def test_layer_norm_refuses(lib, at, v, code):
     a = [P[0], BF16, 4, 64, P[1], P[2], 1e-5, P[3], None]
     a[at] = v
