@@ -152,3 +152,38 @@ def test_gradients_are_differences(cuda_device):
             flat[i] = keep
             # 2 y values of each of D columns, their rounding 2^-22 of |y| < 8, over 2 h; dy below 4
             assert abs((up - down) / (2 * h) - grad.view(-1)[i].item()) < 2 * D * 4 * 8 * 2.0 ** -22 / h + h * h
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 2048), ("f32", 1001)])
+def test_streams_and_graphs(cuda_device, dtype, D):
+    """Two graphs captured with one workspace, replayed in turn with new inputs, and two streams at once."""
+    x, dy, w, b = inputs(6, 500, D, dtype)
+    x2, dy2, _, _ = inputs(7, 500, D, dtype)
+    want = [(R.rapt_layer_norm_fwd(p, w, b), *R.rapt_layer_norm_bwd(q, p, w)) for p, q in ((x, dy), (x2, dy2))]
+    same = lambda got, k: all(torch.equal(u, v) for u, v in zip(got, want[k]))
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    p, q = x.clone(), dy.clone()
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                outs.append((R.rapt_layer_norm_fwd(p, w, b), *R.rapt_layer_norm_bwd(q, p, w, workspace=ws)))
+            graphs.append(g)
+    torch.cuda.current_stream().wait_stream(side)
+    for k, (a, c) in enumerate(((x, dy), (x2, dy2), (x, dy))):
+        p.copy_(a)
+        q.copy_(c)
+        for g in graphs:
+            g.replay()
+        assert same(outs[0], k % 2) and same(outs[1], k % 2)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    got = [None, None]
+    for _ in range(5):
+        got[0] = (R.rapt_layer_norm_fwd(x, w, b), *R.rapt_layer_norm_bwd(dy, x, w))
+        got[1] = (R.rapt_layer_norm_fwd(x2, w, b, stream=other), *R.rapt_layer_norm_bwd(dy2, x2, w, stream=other))
+    torch.cuda.synchronize()
+    assert same(got[0], 0) and same(got[1], 1)
