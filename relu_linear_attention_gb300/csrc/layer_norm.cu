@@ -12,10 +12,10 @@
 // stay in registers over the CTA's rows (fp32); a second small launch adds the CTAs' in a fixed order.
 //
 // What it costs beside the bytes is instructions: unpacking, five to ten of arithmetic a value, and the reductions,
-// which a thread pays once a row. So threads take many columns (bf16, 16384 x 2048, forward: 8 columns 39 us, 16
-// 33; the next row's sum beside this row's instead of a second reduction: 16 columns 31 us with it, and 26 when
-// D = 16 x threads besides and no column needs a check). 16384 x 2048 bf16: forward 26 us, backward 44 us (32
-// columns; 48 with 16), of it 6 us for the sum over the CTAs; 4099 x 5121 fp32, backward: 70 us.
+// which a thread pays once a row. So threads take many columns, and rows that fill them take no checks. The forward of
+// 16384 x 2048 bf16: one reduction that carries the next row's sum (x unpacked twice) 39 us with 8 columns a thread, 33
+// with 16; two reductions 31; no checks 26. Its backward: 44 us (48 with 16 columns instead of 32), some 6 of it for
+// the sum over the CTAs. 4099 x 5121 fp32, backward: 70 us.
 #include "residual_norm.cuh"
 #include "tc_utils.cuh"
 

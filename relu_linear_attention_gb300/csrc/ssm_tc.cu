@@ -37,8 +37,8 @@
 //
 // 4 x 4096 tokens x 64 heads of 64, N = 128: 149 us (the bytes alone 62, the products 47); 65536 packed tokens x 32
 // heads of 64, N = 64: 270 us; 32768 tokens x 16 heads of 128, N = 128: 178 us in segments. What bounds it is a
-// chunk's chain, 9 thousand cycles: the state and its copy wait for the increment, the rows for G, the epilogue for Y, one
-// after the other; the tensor pipe is busy for a third of it and the issue slots for half.
+// chunk's chain, 9 thousand cycles: the state and its copy wait for the increment, the rows for G, the epilogue for
+// Y, one after the other; the tensor pipe is busy for a third of it and the issue slots for half.
 #include <cuda.h>
 
 #include <algorithm>
