@@ -196,8 +196,8 @@ __device__ __forceinline__ float row_log(const float* p, int i, int q4) {
   return fmaxf(all, kLeastRow);
 }
 
-// f times z sigmoid(z) of 8 bf16 values z. (One reciprocal for four, 1 / (a b c d) times the others' products, costs
-// more instructions than it saves.)
+// f times z sigmoid(z) of 8 bf16 values z, that product first: f z may overflow where sigmoid(z) is 0. (One reciprocal
+// for four, 1 / (a b c d) times the others' products, costs more instructions than it saves.)
 __device__ __forceinline__ void gate_by(const uint4& z4, float2 (&f)[4]) {
   const uint32_t w[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
@@ -207,7 +207,7 @@ __device__ __forceinline__ void gate_by(const uint4& z4, float2 (&f)[4]) {
     float2 r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-    f[e] = __fmul2_rn(__fmul2_rn(f[e], z), r);
+    f[e] = __fmul2_rn(f[e], __fmul2_rn(z, r));
   }
 }
 

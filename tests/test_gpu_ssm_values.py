@@ -1,0 +1,52 @@
+"""The selective scan at the ends of its inputs' range, and with values that are not finite: the gate, the step
+sizes and decays, and tokens that belong to others. Prompts (on the tensor cores and on the CUDA cores) and single
+tokens, against the fp64 oracle or against the bits of the same call without such values."""
+
+import numpy as np
+import pytest
+import torch
+
+import ssm_bounds as SB
+from block_bounds import within
+from relu_linear_attention_gb300 import binding as R
+from ssm_inputs import document, host, scan_inputs, state
+
+pytestmark = pytest.mark.gpu
+
+# tensor cores: pairs of heads, a head alone, heads of 128; CUDA cores
+FORMS = [("bf16", (2, 64, 1, 64)), ("bf16", (3, 64, 1, 128)), ("bf16", (2, 128, 1, 64)), ("bf16", (2, 32, 1, 16)),
+         ("f32", (2, 64, 1, 64))]
+
+
+def _pack(lens):
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    return cu, torch.from_numpy(cu).cuda()
+
+
+@pytest.mark.parametrize("dtype,shape", FORMS)
+def test_gate_at_the_ends_of_its_range(cuda_device, dtype, shape):
+    """z silu far out: closed (a mask of the type's lowest value) or open, in prompts and single tokens alike."""
+    H, P, G, N = shape
+    args, opts = scan_inputs(1, (1, 140), H, P, G, N, dtype)
+    lowest = torch.finfo(args["x"].dtype).min
+    far = torch.tensor([lowest, -1e30, -200.0, -90.0, 90.0, 200.0, 1e30], device="cuda")
+    z = opts["z"] = far[torch.arange(140 * H * P, device="cuda") % 7].view(1, 140, H, P).to(args["x"].dtype)
+    args["x"] = args["x"].contiguous() * 16  # outputs well above 1
+    out = R.rapt_ssm_prefill_fwd(**args, **opts)[0]
+    chunks = dtype == "bf16" and P >= 64
+    with np.errstate(over="ignore"):
+        ref, _, eo, _ = SB.scan(dtype, **document(args, opts, 0), chunks=chunks)
+        within(host(out[0]), ref, eo + 1e-30, "prompt")
+        assert torch.equal(out[z == lowest], torch.zeros_like(out[z == lowest]))
+        # an open gate is its own value: z times what a call without a gate gives, four roundings of the type
+        wide = z == z.max()
+        plain = (R.rapt_ssm_prefill_fwd(**args, **{**opts, "z": None})[0].double() * z.double())[wide]
+        assert plain.abs().max() > 1e30
+        assert ((out[wide].double() - plain).abs() <= 2 * torch.finfo(out.dtype).eps * plain.abs()).all()
+        S = torch.zeros(140, H, N, P, device="cuda")
+        one = {k: v if k == "A" else v[0] for k, v in args.items()}
+        tok = {k: v[0] if k == "z" else v for k, v in opts.items()}
+        out = R.rapt_ssm_decode_step(**one, **tok, S=S)
+        for i in (0, 77, 139):
+            ref, _, eo, _ = SB.scan(dtype, **document(one, tok, slice(i, i + 1)))
+            within(host(out[i:i + 1]), ref, eo + 1e-30, "token %d" % i)
