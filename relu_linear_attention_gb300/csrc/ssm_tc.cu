@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
       const float d = c * kC + t < seg_n 
                           ? step_size(__uint_as_float(static_cast<uint32_t>(raw0) << 16), bias, a.softplus)
                           : 0.f;
-      const float l = fmaxf(d * A2, kLeastLog);
+      const float l = c * kC + t < seg_n ? fmaxf(d * A2, kLeastLog) : 0.f;  // (0 times an infinite A is no number)
       raw0 = raw1;
       raw1 = load_dt(c + 2);
       // sums inside the block: p up to a token, behind it u

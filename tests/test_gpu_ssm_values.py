@@ -50,3 +50,22 @@ def test_gate_at_the_ends_of_its_range(cuda_device, dtype, shape):
         for i in (0, 77, 139):
             ref, _, eo, _ = SB.scan(dtype, **document(one, tok, slice(i, i + 1)))
             within(host(out[i:i + 1]), ref, eo + 1e-30, "token %d" % i)
+
+
+@pytest.mark.parametrize("dtype,shape", FORMS)
+def test_a_decay_that_forgets_everything(cuda_device, dtype, shape):
+    """A = -infinity: every state is its last token's; a document's end inside a chunk changes nothing."""
+    H, P, G, N = shape
+    lens = [150, 128, 1, 37]
+    cu, dev = _pack(lens)
+    args, opts = scan_inputs(9, (int(cu[-1]),), H, P, G, N, dtype)
+    args["A"][0] = float("-inf")
+    S0 = state(10, len(lens), H, N, P)
+    out, S = R.rapt_ssm_varlen_fwd(**args, **opts, cu_seqlens=dev, max_seqlen=150, S0=S0, final_state=True)
+    for i in range(len(lens)):
+        at = slice(cu[i], cu[i + 1])
+        k = document(args, opts, at)
+        k["A"] = np.maximum(k["A"], -1e6)
+        ref, refS, eo, eS = SB.scan(dtype, **k, S0=host(S0[i]), chunks=dtype == "bf16" and P >= 64)
+        within(host(out[at]), ref, eo + 1e-30, "document %d out" % i)
+        within(host(S[i]), refS, eS + 1e-30, "document %d S" % i)
