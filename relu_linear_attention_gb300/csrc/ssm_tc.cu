@@ -98,6 +98,11 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // Two bf16 values as floats.
 __device__ __forceinline__ float2 widen2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -326,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
       const float d = c * kC + t < seg_n 
                           ? step_size(__uint_as_float(static_cast<uint32_t>(raw0) << 16), bias, a.softplus)
                           : 0.f;
-      const float l = c * kC + t < seg_n ? fmaxf(d * A2, kLeastLog) : 0.f;  // (0 times an infinite A is no number)
+      // (a NaN stays one; behind the document's end the state is kept, whatever A)
+      const float l = c * kC + t < seg_n ? max_nan(d * A2, kLeastLog) : 0.f;
       raw0 = raw1;
       raw1 = load_dt(c + 2);
       // sums inside the block: p up to a token, behind it u

@@ -69,3 +69,24 @@ def test_a_decay_that_forgets_everything(cuda_device, dtype, shape):
         ref, refS, eo, eS = SB.scan(dtype, **k, S0=host(S0[i]), chunks=dtype == "bf16" and P >= 64)
         within(host(out[at]), ref, eo + 1e-30, "document %d out" % i)
         within(host(S[i]), refS, eS + 1e-30, "document %d S" % i)
+
+
+@pytest.mark.parametrize("dtype,shape", FORMS)
+def test_a_parameter_that_is_no_number_shows(cuda_device, dtype, shape):
+    """NaN in A: its head's outputs and state are NaN, the others keep their bits; prompts and single tokens."""
+    H, P, G, N = shape
+    args, opts = scan_inputs(7, (1, 150), H, P, G, N, dtype)
+    S0 = state(8, 1, H, N, P)
+    res = []
+    for bad in (False, True):
+        if bad:
+            args["A"][1] = float("nan")
+        one = {k: v if k == "A" else v[:, 0] for k, v in args.items()}
+        tok = {k: v[:, 0] if k == "z" else v for k, v in opts.items()}
+        out, Sf = R.rapt_ssm_prefill_fwd(**args, **opts, S0=S0, final_state=True)
+        S = S0.clone()
+        y = R.rapt_ssm_decode_step(**one, **tok, S=S)
+        res.append([v.movedim(d, 0) for v, d in ((out, 2), (Sf, 1), (y, 1), (S, 1))])
+    for clean, got in zip(*res):
+        assert torch.isnan(got[1]).all()
+        assert all(torch.equal(got[h], clean[h]) for h in range(H) if h != 1)
