@@ -507,6 +507,23 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
       }
       ok = group(kBarStates, kStates, warp == kRows / 32, tab_full + 8 * s, ph, x_full + 8 * s, ph, 0, 0);
       if (!ok) break;
+      if (READ && c * kC + kC > seg_n) {
+        // The tiles go on with the next document's tokens, of weight 0: zeros in their place, as 0 times what is not
+        // finite is no number. B after the scores have read it; x and B before the products with a weight of 0.
+        ok = group(kBarStates, kStates, warp == kRows / 32, b_full + 8 * s, ph, g_done, c & 1, 0, 0);
+        if (!ok) break;
+        const int t = tid - kRows;
+        for (int r = seg_n - c * kC + (t >> 3); r < kC; r += kStates / 8) {
+          const uint32_t at = tc::sw128(r, t & 7);
+          for (int j = 0; j < halves; ++j)
+            *reinterpret_cast<uint4*>(smem + L::X + s * L::XT + j * 16384 + at) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int j = 0; j < N / 64; ++j)
+            *reinterpret_cast<uint4*>(smem + L::B + s * L::NT + j * 16384 + at) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        tc::fence_async_smem();
+        tc::named_sync(kBarStates, kStates);
+      }
       const float* const sums = table(c, 0, k);
       const float all = sums[31] + sums[63] + sums[95] + sums[127];
       keep = ex2(all);

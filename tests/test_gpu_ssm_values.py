@@ -53,6 +53,49 @@ def test_gate_at_the_ends_of_its_range(cuda_device, dtype, shape):
 
 
 @pytest.mark.parametrize("dtype,shape", FORMS)
+@pytest.mark.parametrize("what", ["x", "B", "C", "dt", "z"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_not_finite_stays_in_its_document(cuda_device, dtype, shape, what, value):
+    """Documents that end inside a chunk, the next one's first tokens not finite: the bits of the others are those of
+    the call without them, outputs and final states. Packed, and rows of a batch."""
+    H, P, G, N = shape
+    lens = [5, 130, 1, 127, 128, 300, 17, 33]
+    cu, dev = _pack(lens)
+    args, opts = scan_inputs(2, (int(cu[-1]),), H, P, G, N, dtype, sliced=False)
+    S0 = state(3, len(lens), H, N, P)
+    call = lambda: R.rapt_ssm_varlen_fwd(**args, **opts, cu_seqlens=dev, max_seqlen=300, S0=S0, final_state=True)
+    out, S = call()
+    t = args.get(what, opts.get(what))
+    for bad in (1, 3, 5, 7):
+        t[cu[bad]:cu[bad] + 3] = value
+    out2, S2 = call()
+    for i, n in enumerate(lens):
+        same, same_S = torch.equal(out[cu[i]:cu[i + 1]], out2[cu[i]:cu[i + 1]]), torch.equal(S[i], S2[i])
+        assert (same, same_S) == ((True, True) if i % 2 == 0 else (False, what in ("C", "z"))), i
+    args, opts = scan_inputs(4, (3, 150), H, P, G, N, dtype, sliced=False)
+    S0 = state(5, 3, H, N, P)
+    call = lambda: R.rapt_ssm_prefill_fwd(**args, **opts, S0=S0, final_state=True)
+    out, S = call()
+    args.get(what, opts.get(what))[1, :100] = value
+    out2, S2 = call()
+    assert all(torch.equal(out[b], out2[b]) and torch.equal(S[b], S2[b]) for b in (0, 2))
+    assert not torch.isfinite(out2[1].float()).all()
+
+
+@pytest.mark.parametrize("dtype,shape", FORMS)
+@pytest.mark.parametrize("what", ["B", "C", "dt", "z"])
+def test_not_finite_reaches_no_token_before_it(cuda_device, dtype, shape, what):
+    H, P, G, N = shape
+    args, opts = scan_inputs(6, (1, 300), H, P, G, N, dtype, sliced=False)
+    out = R.rapt_ssm_prefill_fwd(**args, **opts)[0]
+    args.get(what, opts.get(what))[0, 200] = float("nan")
+    out2 = R.rapt_ssm_prefill_fwd(**args, **opts)[0]
+    assert torch.equal(out[0, :200], out2[0, :200]) and torch.isnan(out2[0, 200]).all()
+    later = torch.isnan(out2[0, 201:])
+    assert not later.any() if what in ("C", "z") else later.all()
+
+
+@pytest.mark.parametrize("dtype,shape", FORMS)
 def test_a_decay_that_forgets_everything(cuda_device, dtype, shape):
     """A = -infinity: every state is its last token's; a document's end inside a chunk changes nothing."""
     H, P, G, N = shape
