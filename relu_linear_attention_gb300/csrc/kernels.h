@@ -394,8 +394,9 @@ cudaError_t launch_conv_step(DType dt, const void* x, long x_stride, const float
 
 // The selective scan. The recurrence in fp32 on CUDA cores (ssm_simt.cu), chunks on the tensor cores (ssm_tc.cu,
 // bf16, P and N of 64 or 128), a single token (ssm_step.cu). Documents longer than a segment are cut into nseg
-// segments of seg_len tokens; ws holds a record of N P + kSsmRecTail floats per (document, head, segment): the
-// state increment [N, P] and the decay over the segment.
+// segments of seg_len tokens; ws holds a record of N P + kSsmRecTail floats for every segment but a document's last
+// and every head: the state increment [N, P] and the decay over the segment. A packed document's records begin at its
+// first token / seg_len: there are ssm_records(), as many as the tokens fill, whatever the documents.
 struct SsmArgs {
   Docs docs;
   const void *x, *dt, *B, *C, *z;  // z nullable
@@ -413,6 +414,12 @@ struct SsmArgs {
   const int* order;                // nullable: documents in the order in which the CTAs take them
 };
 constexpr int kSsmRecTail = 4;
+// Records of a head. Documents of tokens [s, s + n) have floor((n - 1) / seg_len) each, from floor(s / seg_len), and
+// floor(s / seg_len) + floor((n - 1) / seg_len) <= floor((s + n - 1) / seg_len): they do not overlap.
+inline long ssm_records(const SsmArgs& a, int nseg, int seg_len) {
+  if (nseg == 1) return 0;
+  return a.packed ? (a.docs.total_rows - 1L) / seg_len : static_cast<long>(a.docs.n_docs) * (nseg - 1);
+}
 struct SsmPlan {
   int nseg, seg_len;
   bool sorted;

@@ -22,6 +22,11 @@ __device__ __forceinline__ bool doc_rows(const Docs& d, int doc, long& row0, int
   return !bad;
 }
 
+// Where the record of segment seg of head h is in the workspace, in records; `start` is the document's first row.
+__device__ __forceinline__ long record(const SsmArgs& a, int doc, long start, int seg, int h) {
+  return ((a.packed ? start / a.seg_len : static_cast<long>(doc) * (a.nseg - 1)) + seg) * a.H + h;
+}
+
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(Cfg<T, N, P>::THREADS) ssm_simt_kernel(const S
   if (seg >= (READ ? segs : segs - 1)) return;
   if (READ && !good) return;
   const int t0 = seg * a.seg_len, len = min(a.seg_len, n - t0);  // 0: an empty document
+  const long start = row0;
   row0 += t0;
 
   const int tn = lane % TN, tc = lane / TN, col = warp * C::CW + tc * NC;
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(Cfg<T, N, P>::THREADS) ssm_simt_kernel(const S
   constexpr long kRec = N * P + kSsmRecTail;
   if (READ) {
     if (a.nseg > 1) tc::grid_dep_wait();  // a segment's record holds the state at its end by now
-    const float* const from = seg > 0           ? a.ws + (dh * (a.nseg - 1) + seg - 1) * kRec
+    const float* const from = seg > 0           ? a.ws + record(a, doc, start, seg - 1, h) * kRec
                               : a.S0 != nullptr ? a.S0 + dh * (N * P)
                                                 : nullptr;
     if (from != nullptr) {
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(Cfg<T, N, P>::THREADS) ssm_simt_kernel(const S
   }
   float* dst = nullptr;
   if (!READ) {
-    dst = a.ws + (dh * (a.nseg - 1) + seg) * kRec;
+    dst = a.ws + record(a, doc, start, seg, h) * kRec;
     if (tid == 0) dst[N * P] = total;
   } else if (seg == segs - 1 && a.S_final != nullptr) {
     dst = a.S_final + dh * (N * P);
@@ -245,12 +246,13 @@ __global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a, int np
   const long dh = i / np4;
   const int e = static_cast<int>(i % np4);
   if (dh >= static_cast<long>(a.docs.n_docs) * a.H) return;
+  const int doc = static_cast<int>(dh / a.H);
   long row0;
   int n;
-  doc_rows(a.docs, static_cast<int>(dh / a.H), row0, n);
+  doc_rows(a.docs, doc, row0, n);
   const int segs = n > 0 ? (n + a.seg_len - 1) / a.seg_len : 1;
-  const long rec = 4L * np4 + kSsmRecTail;
-  float* const base = a.ws + dh * (a.nseg - 1) * rec;
+  const long rec = 4L * np4 + kSsmRecTail, step = rec * a.H;  // from a segment's to the next one's
+  float* const base = a.ws + record(a, doc, row0, 0, static_cast<int>(dh % a.H)) * rec;
   float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.S0 != nullptr) h = reinterpret_cast<const float4*>(a.S0)[dh * np4 + e];
   tc::grid_dep_wait();
@@ -261,8 +263,8 @@ __global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a, int np
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (j0 + j >= segs - 1) break;
-      inc[j] = __ldcg(reinterpret_cast<const float4*>(base + (j0 + j) * rec) + e);
-      keep[j] = __ldcg(base + (j0 + j) * rec + 4 * np4);
+      inc[j] = __ldcg(reinterpret_cast<const float4*>(base + (j0 + j) * step) + e);
+      keep[j] = __ldcg(base + (j0 + j) * step + 4 * np4);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a, int np
       h.y = fmaf(keep[j], h.y, inc[j].y);
       h.z = fmaf(keep[j], h.z, inc[j].z);
       h.w = fmaf(keep[j], h.w, inc[j].w);
-      __stcg(reinterpret_cast<float4*>(base + (j0 + j) * rec) + e, h);
+      __stcg(reinterpret_cast<float4*>(base + (j0 + j) * step) + e, h);
     }
   }
 }
@@ -345,7 +347,8 @@ SsmPlan ssm_plan_simt(const SsmArgs& a) {
   p.seg_len = static_cast<int>((longest + nseg - 1) / nseg + kTokens - 1) / kTokens * kTokens;
   p.seg_len = std::max(p.seg_len, kTokens);
   p.nseg = static_cast<int>(std::max<long>((longest + p.seg_len - 1) / p.seg_len, 1));
-  p.ws_bytes = static_cast<size_t>(units) * (p.nseg - 1) * (static_cast<size_t>(a.N) * a.P + kSsmRecTail) * 4;
+  p.ws_bytes = static_cast<size_t>(ssm_records(a, p.nseg, p.seg_len)) * a.H *
+               (static_cast<size_t>(a.N) * a.P + kSsmRecTail) * 4;
   return p;
 }
 

@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     for (int e = 0; e < HN / 2; ++e) h[e] = make_float2(0.f, 0.f);
     if constexpr (READ) {
       // (a segment's record holds the state at its end by now)
-      const float* const from = seg > 0 ? a.ws + (dh * (a.nseg - 1) + seg - 1) * kRec : a.S0 != nullptr ? a.S0 + dh * (N * P) : nullptr;
+      const float* const from = seg > 0 ? a.ws + record(a, doc, row0 - seg_start, seg - 1, head) * kRec : a.S0 != nullptr ? a.S0 + dh * (N * P) : nullptr;
       if (seg > 0) tc::grid_dep_wait();
       if (from != nullptr) {
 #pragma unroll
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
     if (ok && live) {
       float* dst = nullptr;
       if (!READ) {
-        dst = a.ws + (dh * (a.nseg - 1) + seg) * kRec;
+        dst = a.ws + record(a, doc, row0 - seg_start, seg, head) * kRec;
         if (half == 0 && pl == 0) __stcg(dst + N * P, ex2(log_all));
       } else if (seg == segs - 1 && a.S_final != nullptr) {
         dst = a.S_final + dh * (N * P);
@@ -875,9 +875,12 @@ bool ssm_tc_supported(DType dt, int P, int N) {
 }
 
 // Segments of a document, by an estimate in units of one chunk of the scan: waves of one CTA an SM, each its chunks
-// and 1.5 of set-up; kernel A's chunks cost 0.6. A longer plan has to be 5 % faster. Packed documents whole, the
-// longest first, take the longest one's time or their share of an SM, whichever is more (65536 tokens x 32 heads of 64
-// in documents of 128 to 8192: cut 373 us, whole and sorted 270).
+// and 1.5 of set-up; kernel A's chunks cost 0.6. Of a document shorter than the longest, the CTAs without a segment
+// cost 0.35 each (1.65 us: 1100 documents of 7 tokens x 16 heads of 64, N = 64, called with room for 60 segments each:
+// 12.1 ms, without 0.54). A longer plan has to be 5 % faster. Packed documents whole, the longest first, take the
+// longest one's time or their share of an SM, whichever is more (65536 tokens x 32 heads of 64 in documents of 128 to
+// 8192: cut 373 us, whole and sorted 270); more than 1024, which the sort by pairs would be too slow for, come in
+// their own order, and the longest may begin last.
 SsmPlan ssm_plan_tc(const SsmArgs& a) {
   const int NH = a.P == 64 ? 2 : 1, R = a.H / a.G;
   const long units = static_cast<long>(a.G) * ((R + NH - 1) / NH);
@@ -892,21 +895,25 @@ SsmPlan ssm_plan_tc(const SsmArgs& a) {
     const auto waves = [](double ctas) { return static_cast<double>(static_cast<long>((ctas + 151.0) / 152.0)); };
     double cost = waves(units * docs * per_doc) * (len + 1.5);
     if (nseg > 1) cost += waves(units * docs * std::max(1.0, per_doc - 1)) * (0.6 * len + 1.5);
+    if (nseg > 1 && a.packed) cost += 2 * 0.35 / 152.0 * static_cast<double>(units * docs) * (nseg - per_doc);
     if (cost < 0.95 * best_cost) {
       best_cost = cost;
       best.nseg = static_cast<int>(nseg);
       best.seg_len = static_cast<int>(len) * kC;
     }
   }
-  if (a.packed && docs <= 1024) {
+  if (a.packed) {
+    const bool sort = docs <= 1024;
+    const double most = static_cast<double>(longest);
     const double each = units * (static_cast<double>(a.docs.total_rows) / kC + 0.5 * docs) / 152.0;
-    if (std::max(static_cast<double>(longest), each) + 2.5 < best_cost) {
+    if ((sort ? std::max(most, each) : most + each) + 2.5 < best_cost) {
       best.nseg = 1;
       best.seg_len = static_cast<int>(longest) * kC;
-      best.sorted = docs > 1;
+      best.sorted = sort && docs > 1;
     }
   }
-  best.ws_bytes = static_cast<size_t>(docs) * a.H * (best.nseg - 1) * (static_cast<size_t>(a.N) * a.P + kSsmRecTail) * 4;
+  best.ws_bytes = static_cast<size_t>(ssm_records(a, best.nseg, best.seg_len)) * a.H *
+                  (static_cast<size_t>(a.N) * a.P + kSsmRecTail) * 4;
   if (best.sorted) best.ws_bytes = static_cast<size_t>(docs) * sizeof(int);  // (a whole document has no records)
   return best;
 }

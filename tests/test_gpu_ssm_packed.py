@@ -159,3 +159,24 @@ def test_a_prompt_in_pieces(cuda_device, dtype, shape):
     chunks = dtype == "bf16" and P >= 64
     for out, Sf in ((whole, last), (torch.cat(outs, 1), S)):
         check(out[0], Sf, flat(args), flat(opts), [0, L], 0, dtype, S0, chunks=chunks)
+
+
+@pytest.mark.parametrize("lens", [[3] * 700 + [2000] + [1, 0, 129] * 150, [7] * 1024 + [1200]])
+@pytest.mark.parametrize("shape", [(1, 64, 1, 64), (8, 64, 4, 64), (2, 128, 2, 128)])
+def test_many_documents(cuda_device, lens, shape):
+    """More documents than are sorted, one of them long."""
+    H, P, G, N = shape
+    cu, dev = pack(lens)
+    T = int(cu[-1])
+    args, opts = scan_inputs(5, (T,), H, P, G, N, "bf16")
+    assert plan_bytes(args, T, len(lens), max(lens)) <= H * (T // 128) * (N * P + 4) * 4
+    S0 = state(6, len(lens), H, N, P)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, S = R.rapt_ssm_varlen_fwd(**args, **opts, cu_seqlens=dev, max_seqlen=max(lens), S0=S0, final_state=True,
+                                   dev_status=status)
+    assert status.item() == 0
+    for i in (0, 1, 699, 700, 701, 703, 704, len(lens) - 2, len(lens) - 1):
+        check(out, S, args, opts, cu, i, "bf16", S0)
+    whole = R.rapt_ssm_varlen_fwd(**args, **opts, cu_seqlens=dev, max_seqlen=T, S0=S0, final_state=True)
+    for i in (0, 700, len(lens) - 1):  # a looser bound on the lengths, another plan
+        check(*whole, args, opts, cu, i, "bf16", S0)
