@@ -113,10 +113,11 @@ __device__ __forceinline__ void bounds(const Docs& d, int doc, int& start, int& 
   }
 }
 
-// The last W - 1 inputs of a document.
+// The last W - 1 inputs of a document; without state_final, a document an item, a look at its bounds alone.
 template <typename T, int V, int W>
 __device__ __forceinline__ void last_inputs(const ConvArgs& a, long i, int nvec) {
-  const int doc = static_cast<int>(i / nvec), c = static_cast<int>(i % nvec) * V;
+  const int per_doc = a.state_final != nullptr ? nvec : 1;
+  const int doc = static_cast<int>(i / per_doc), c = static_cast<int>(i % per_doc) * V;
   long row0;
   int n;
   const bool good = doc_rows(a.docs, doc, row0, n);
@@ -264,8 +265,8 @@ cudaError_t go(const ConvArgs& a, cudaStream_t stream) {
   while (tokens > kAhead && count() < 152L * 1024) tokens /= 2;
   const long tiles = count();
   // (documents are looked through for a malformed cu_seqlens, too)
-  const bool ends = a.state_final != nullptr || (a.docs.cu_seqlens != nullptr && a.docs.dev_status != nullptr);
-  const long items = tiles + (ends ? static_cast<long>(a.docs.n_docs) * nvec : 0);
+  const bool look = a.docs.cu_seqlens != nullptr && a.docs.dev_status != nullptr;
+  const long items = tiles + static_cast<long>(a.docs.n_docs) * (a.state_final != nullptr ? nvec : look ? 1 : 0);
   if (items == 0) return cudaSuccess;
   const long grid = (items + kThreads - 1) / kThreads;
   conv_kernel<T, V, W, PATH><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a, nvec, tokens, tiles, items);
