@@ -2,6 +2,7 @@
 #pragma once
 
 #include "kernels.h"
+#include "tc_utils.cuh"
 
 namespace rapt {
 namespace ssm {
@@ -20,6 +21,13 @@ __device__ __forceinline__ bool doc_rows(const Docs& d, int doc, long& row0, int
   row0 = bad ? 0 : s;
   n = bad ? 0 : e - s;
   return !bad;
+}
+
+// For a launch that may begin before the ones that form its records have ended, at the end of its first CTA: a grid
+// in which no CTA has waited (every document of one segment) could end before them, and what the stream does next
+// would meet them still running.
+__device__ __forceinline__ void end_behind_records(const SsmArgs& a) {
+  if (a.nseg > 1 && blockIdx.x == 0) tc::grid_dep_wait();
 }
 
 // Where the record of segment seg of head h is in the workspace, in records; `start` is the document's first row.

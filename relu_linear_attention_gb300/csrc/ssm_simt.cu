@@ -62,8 +62,10 @@ __global__ void __launch_bounds__(Cfg<T, N, P>::THREADS) ssm_simt_kernel(const S
   const bool good = doc_rows(a.docs, doc, row0, n);
   if (READ && !good && seg == 0 && h == 0 && tid == 0 && a.docs.dev_status != nullptr) atomicOr(a.docs.dev_status, 1u);
   const int segs = n > 0 ? (n + a.seg_len - 1) / a.seg_len : 1;
-  if (seg >= (READ ? segs : segs - 1)) return;
-  if (READ && !good) return;
+  if (seg >= (READ ? segs : segs - 1) || (READ && !good)) {
+    if (READ) end_behind_records(a);
+    return;
+  }
   const int t0 = seg * a.seg_len, len = min(a.seg_len, n - t0);  // 0: an empty document
   const long start = row0;
   row0 += t0;

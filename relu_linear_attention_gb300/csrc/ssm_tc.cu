@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
   const bool good = doc_rows(a.docs, doc, row0, n);
   if (READ && !good && seg == 0 && unit == 0 && tid == 0 && a.docs.dev_status != nullptr) atomicOr(a.docs.dev_status, 1u);
   const int segs = n > 0 ? (n + a.seg_len - 1) / a.seg_len : 1;
-  if (!good || seg >= (READ ? segs : segs - 1)) return;  // uniform across the CTA, before any allocation
+  if (!good || seg >= (READ ? segs : segs - 1)) {  // uniform across the CTA, before any allocation
+    if (READ) end_behind_records(a);
+    return;
+  }
   const int seg_start = seg * a.seg_len, seg_n = min(a.seg_len, n - seg_start);  // 0: an empty document
   const int nchunks = (seg_n + kC - 1) / kC;
   row0 += seg_start;
@@ -806,6 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_tc_kernel(const SsmArgs a, co
   __syncthreads();
   if (*s_abort && tid == 0 && a.docs.dev_status != nullptr) atomicOr(a.docs.dev_status, kDevInternal);
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
+  if (READ) end_behind_records(a);
 }
 
 // [rows, cols] with `stride` elements from row to row: boxes of 64 columns x 128 rows.

@@ -180,3 +180,26 @@ def test_many_documents(cuda_device, lens, shape):
     whole = R.rapt_ssm_varlen_fwd(**args, **opts, cu_seqlens=dev, max_seqlen=T, S0=S0, final_state=True)
     for i in (0, 700, len(lens) - 1):  # a looser bound on the lengths, another plan
         check(*whole, args, opts, cu, i, "bf16", S0)
+
+
+@pytest.mark.parametrize("shape,dtype", [((2, 64, 1, 64), "bf16"), ((2, 32, 1, 16), "f32")])
+def test_short_documents_in_a_plan_of_segments(cuda_device, shape, dtype):
+    """A bound on the lengths far above them: segments that no document has; bounds and workspace are overwritten right
+    behind the call."""
+    H, P, G, N = shape
+    lens = [60, 64, 0, 17, 1, 50] * 4
+    cu, dev = pack(lens)
+    args, opts = scan_inputs(15, (int(cu[-1]),), H, P, G, N, dtype)
+    need = plan_bytes(args, int(cu[-1]), len(lens), 1 << 20)
+    S0 = state(16, len(lens), H, N, P)
+    want = None
+    for _ in range(20):
+        c, ws = dev.clone(), torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        out, S = R.rapt_ssm_varlen_fwd(**args, **opts, cu_seqlens=c, max_seqlen=1 << 20, S0=S0, final_state=True,
+                                       workspace=ws)
+        c.zero_()
+        ws.zero_()
+        want = want or (out, S)
+        assert torch.equal(out, want[0]) and torch.equal(S, want[1]) and not ws.any()
+    for i in range(len(lens)):
+        check(out, S, args, opts, cu, i, dtype, S0, chunks=dtype == "bf16")
