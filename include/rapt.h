@@ -622,6 +622,8 @@ typedef struct rapt_ssm_inputs {
  * rounded to bf16, decays, step sizes and the states themselves are fp32 (the state's increments are products of
  * B, exact, with dt x under its decay in two bf16 parts, 16 bits); where the decay from a chunk's start to a token
  * is below 2^-64, the state before the chunk counts 2^-64 for it.
+ * The scores and outputs of a chunk are held over that factor: in magnitude, dt C_t . B_i and what a chunk's own tokens
+ * add up to in S_t^T C_t have to stay below 2^63 (elsewhere: in fp32's range).
  * Inputs should be finite; what is not stays in its document: a token's B, dt and x reach its outputs from that token on
  * and its final state, C and z the token's own outputs. In chunks, x may reach outputs of the 127 tokens before it, too.
  * Requirements: B >= 1, L >= 0 (0 writes S_final alone), rows <= 2^30, documents * H < 2^25.

@@ -133,3 +133,18 @@ def test_a_parameter_that_is_no_number_shows(cuda_device, dtype, shape):
     for clean, got in zip(*res):
         assert torch.isnan(got[1]).all()
         assert all(torch.equal(got[h], clean[h]) for h in range(H) if h != 1)
+
+
+@pytest.mark.parametrize("dtype,shape", FORMS)
+@pytest.mark.parametrize("decay", [(1.0, 16.0), (200.0, 4000.0)])
+def test_large_values(cuda_device, dtype, shape, decay):
+    """Scores and outputs of up to some 2^60 with decays below 2^-64: inside the range that the header gives."""
+    H, P, G, N = shape
+    args, opts = scan_inputs(11, (1, 300), H, P, G, N, dtype, z=False, decay=decay)
+    args["x"], args["B"], args["C"] = (args[k].contiguous() * 2.0 ** e for k, e in (("x", 22), ("B", 16), ("C", 16)))
+    S0 = state(12, 1, H, N, P) * 2.0 ** 30
+    out, S = R.rapt_ssm_prefill_fwd(**args, **opts, S0=S0, final_state=True)
+    ref, refS, eo, eS = SB.scan(dtype, **document(args, opts, 0), S0=host(S0[0]), chunks=dtype == "bf16" and P >= 64)
+    assert 2.0 ** 52 < np.abs(ref).max() < 2.0 ** 62
+    within(host(out[0]), ref, eo + 1e-30, "out")
+    within(host(S[0]), refS, eS + 1e-30, "S")
