@@ -620,8 +620,8 @@ typedef struct rapt_ssm_inputs {
  * fp32 inputs, and P or Ns below 64: the recurrence in fp32. bf16 with P and Ns of 64 or 128: chunks of 128 tokens
  * on the tensor cores with fp32 accumulation; the decayed scores C_t . B_i and the state that C reads are
  * rounded to bf16, decays, step sizes and the states themselves are fp32 (the state's increments are products of
- * B, exact, with dt x under its decay in two bf16 parts, 16 bits); where the decay from a chunk's start to a token
- * is below 2^-64, the state before the chunk counts 2^-64 for it.
+ * B, exact, with dt x under its decay in two bf16 parts, off by at most 1.5 x 2^-15); where the decay from a chunk's start
+ * to a token is below 2^-64, the state before the chunk counts 2^-64 for it.
  * The scores and outputs of a chunk are held over that factor: in magnitude, dt C_t . B_i and what a chunk's own tokens
  * add up to in S_t^T C_t have to stay below 2^63 (elsewhere: in fp32's range).
  * Inputs should be finite; what is not stays in its document: a token's B, dt and x reach its outputs from that token on

@@ -2,13 +2,14 @@
 // small for the tensor cores' tiles.
 //   S_t = exp(dt_t A) S_{t-1} + dt_t B_t x_t^T,   y_t = (S_t^T C_t + D x_t) silu(z_t).
 //
-// Three fused multiply-adds a state element and token, so the issue slots bound it (where rows are wide: HBM). S
-// stays in registers: a warp owns CW columns of a head's state, TN lanes along its N rows and TC along the
-// columns, each lane NE x NC elements, so that a value of B or C read from shared memory serves NC columns. The
-// TN partial sums of y meet by halving exchanges. Tokens come in stages of kTokens through a ring of cp.async
-// copies; bf16 is widened once per stage for all warps. A document cut into segments (few heads, long documents)
-// is first run without reading S out, for the increments of all its segments but the last; each segment then
-// starts from S0 and the increments before it, in order.
+// Three multiply-adds a state element and token, and a chain within each token (B and C from shared memory, the sums
+// over lanes) that the few warps whose states fit do not hide: 4 x 4096 tokens x 64 heads of 64, N = 128, fp32: 1.96 ms
+// (issue slots 43 % busy; the bytes alone 123 us); N = 16 in bf16: 515 us (52 %; 60 us). S stays in registers: a warp
+// owns CW columns of a head's state, TN lanes along its N rows and TC along the columns, each lane NE x NC elements, so
+// that a value of B or C read from shared memory serves NC columns. The TN partial sums of y meet by halving exchanges.
+// Tokens come in stages of kTokens through a ring of cp.async copies; bf16 is widened once per stage for all warps. A
+// document cut into segments (few heads, long documents) is first run without reading S out, for the increments of all
+// its segments but the last; each segment then starts from S0 and the increments before it, in order.
 #include <algorithm>
 
 #include "ssm.cuh"
@@ -336,9 +337,9 @@ cudaError_t by_n(const SsmArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Segments: as many as give the GPU about 16 warps an SM, none shorter than 96 tokens (3 x 1531 tokens x 24 heads of
-// 32, N = 16, fp32: 39 us; 68 with 256 tokens, whose few warps wait for their own arithmetic, 43 with 64, whose CTAs
-// no longer fit the SMs at once).
+// Segments: as many as give the GPU about 16 warps an SM, of about 96 tokens at least (what a document leaves is spread:
+// never below 64). 3 x 1531 tokens x 24 heads of 32, N = 16, fp32: 39 us; 68 with 256 tokens, whose few warps wait for
+// their own arithmetic, 43 with 64, whose CTAs no longer fit the SMs at once. Measured at that size alone.
 SsmPlan ssm_plan_simt(const SsmArgs& a) {
   const int warps = std::max(1, a.P / (a.N <= 32 ? (a.P >= 32 ? 32 : 16) : 16));
   const long units = static_cast<long>(a.docs.n_docs) * a.H, longest = a.docs.max_seqlen;

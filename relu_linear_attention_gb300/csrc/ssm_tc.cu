@@ -12,8 +12,10 @@
 //   h <- e^(s_128) h + xw^T B               (128 x N)    xw_j = e^(s_128 - s_j) dt_j x_j in two bf16 parts, in TMEM
 //
 // Taking sg_i out of both products lets them share an accumulator: where a row's decay is below 2^-64, C h counts
-// 2^-64 for 0. Two bf16 parts of xw (16 bits) keep the fp32 state to 2^-17 of its terms: with one part it would be
-// 2^-9, and the state is an output and the start of everything later. B and x enter exactly as they are.
+// 2^-64 for 0. Two bf16 parts of xw keep the fp32 state to 1.5 x 2^-15 of its terms (the weight's second part is off by
+// 2^-16 of it, the sum that makes the low part by 2^-15; 16 M random pairs: 2^-14.9): with one part it would be 2^-7,
+// and the state is an output and the start of everything later. For a third part TMEM has no room at N = 128 (all 512
+// columns: G, xw, the increment, Y). B and x enter exactly as they are.
 //
 // Decays are formed from sums inside blocks of 32 tokens, so that a difference of logarithms is that of sums of at
 // most 32 and what lies between: left of the diagonal block, e^(s_i - s_j) = e^(s_i - s at the end of j's block) x
