@@ -52,3 +52,15 @@ def test_malformed_documents_touch_nothing_else(cuda_device, dtype, D):
                 if n:
                     want[W - 1 - n:] = x[e - n:e]
             assert torch.equal(last[16 + i], want), (cu, i)
+
+
+def test_documents_without_a_token(cuda_device):
+    x, w = torch.randn(0, 16, device="cuda"), torch.randn(16, 4, device="cuda")
+    state, status = torch.randn(50, 3, 16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.zeros(51, dtype=torch.int32, device="cuda")
+    out, last = R.rapt_conv_varlen_fwd(x, cu, w, state=state, final_state=True, dev_status=status)
+    assert out.shape == (0, 16) and torch.equal(last, state) and status.item() == 0
+    assert not R.rapt_conv_varlen_fwd(x, cu, w, final_state=True)[1].any()
+    cu[7] = 1
+    R.rapt_conv_varlen_fwd(x, cu, w, dev_status=status)
+    assert status.item() == 1

@@ -203,3 +203,38 @@ def test_short_documents_in_a_plan_of_segments(cuda_device, shape, dtype):
         assert torch.equal(out, want[0]) and torch.equal(S, want[1]) and not ws.any()
     for i in range(len(lens)):
         check(out, S, args, opts, cu, i, dtype, S0, chunks=dtype == "bf16")
+
+
+@pytest.mark.parametrize("shape,dtype", [((2, 64, 1, 64), "bf16"), ((8, 64, 4, 128), "bf16"), ((2, 32, 1, 16), "f32")])
+@pytest.mark.parametrize("longest", [0, 1 << 20])
+def test_documents_without_a_token(cuda_device, shape, dtype, longest):
+    """T = 0: the final states are the ones before, or zeros; bounds that are not all 0 are reported."""
+    H, P, G, N = shape
+    args, opts = scan_inputs(17, (0,), H, P, G, N, dtype, sliced=False)
+    S0 = state(18, 50, H, N, P)
+    cu = torch.zeros(51, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda **kw: R.rapt_ssm_varlen_fwd(**args, **opts, cu_seqlens=cu, max_seqlen=longest, final_state=True,
+                                              dev_status=status, **kw)
+    out, S = call(S0=S0)
+    assert out.shape == (0, H, P) and torch.equal(S, S0)
+    assert torch.equal(call()[1], torch.zeros_like(S0)) and status.item() == 0
+    cu[7] = 1
+    call(S0=S0)
+    assert status.item() == 1
+
+
+@pytest.mark.parametrize("dtype,shape", [("bf16", (2, 64, 1, 64)), ("f32", (2, 32, 1, 16))])
+def test_tokens_that_change_nothing(cuda_device, dtype, shape):
+    """Padding with a raw step of -infinity at the end of the rows of a batch: the final states are those of the rows
+    without it, and the outputs before it their bits."""
+    H, P, G, N = shape
+    args, opts = scan_inputs(19, (3, 300), H, P, G, N, dtype, sliced=False)
+    ends = (300, 131, 1)
+    for b, n in enumerate(ends):
+        args["dt"][b, n:] = float("-inf")
+    S0 = state(20, 3, H, N, P)
+    out, S = R.rapt_ssm_prefill_fwd(**args, **opts, S0=S0, final_state=True)
+    for b, n in enumerate(ends):
+        flat = lambda d: {k: v[b] if k in ("x", "dt", "B", "C", "z") else v for k, v in d.items()}
+        check(out[b], S[b:b + 1], flat(args), flat(opts), [0, n], 0, dtype, S0[b:b + 1], chunks=dtype == "bf16")
