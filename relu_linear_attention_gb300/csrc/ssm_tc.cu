@@ -37,8 +37,8 @@
 // increments.
 // Every wait is bounded; one that gives up sets RAPT_DEV_INTERNAL and the CTA winds down.
 //
-// 4 x 4096 tokens x 64 heads of 64, N = 128: 149 us (the bytes alone 62, the products 47); 65536 packed tokens x 32
-// heads of 64, N = 64: 270 us; 32768 tokens x 16 heads of 128, N = 128: 178 us in segments. What bounds it is a
+// 4 x 4096 tokens x 64 heads of 64, N = 128: 146 us (the bytes alone 62, the products 47); 65536 packed tokens x 32
+// heads of 64, N = 64: 263 us; 32768 tokens x 16 heads of 128, N = 128: 177 us in segments. What bounds it is a
 // chunk's chain, 9 thousand cycles: the state and its copy wait for the increment, the rows for G, the epilogue for
 // Y, one after the other; the tensor pipe is busy for a third of it and the issue slots for half.
 #include <cuda.h>
@@ -893,7 +893,7 @@ bool ssm_tc_supported(DType dt, int P, int N) {
 // Segments of a document, by an estimate in units of one chunk of the scan: waves of one CTA an SM, each its chunks
 // and 1.5 of set-up; kernel A's chunks cost 0.6. Of a document shorter than the longest, the CTAs without a segment
 // cost 0.35 each (1.65 us: 1100 documents of 7 tokens x 16 heads of 64, N = 64, called with room for 60 segments each:
-// 12.1 ms, without 0.54). A longer plan has to be 5 % faster. Packed documents whole, the longest first, take the
+// 12.1 ms, without 0.52). A longer plan has to be 5 % faster. Packed documents whole, the longest first, take the
 // longest one's time or their share of an SM, whichever is more (65536 tokens x 32 heads of 64 in documents of 128 to
 // 8192: cut 373 us, whole and sorted 270); more than 1024, which the sort by pairs would be too slow for, come in
 // their own order, and the longest may begin last.
